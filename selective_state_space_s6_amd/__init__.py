@@ -829,3 +829,9 @@ def ssd_cplx_mimo_chunk_scan_fwd(x, dt, dt_bias, A_log, B, C, D, h0=None, *, chu
                                            workspace.numel() * workspace.element_size(), _stream(dev))
     _check(rc)
     return (y, h_final) if (return_final or h_final is not None) else y
+
+
+from . import attn as _attn  # noqa: E402  (needs the library and the helpers above)
+from .attn import *  # noqa: E402,F401,F403
+
+__all__ += _attn.__all__

@@ -8,11 +8,12 @@
 #include <string.h>
 
 #include "../../include/ssm_scan.h"
+#include "abi_common.hpp"
 #include "launchers.hpp"
 
-namespace {
+namespace ssm {
 
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 int fail(int code, const char *fmt, ...) {
     va_list ap;
@@ -22,23 +23,6 @@ int fail(int code, const char *fmt, ...) {
     return code;
 }
 
-bool aligned16(const void *p) { return p == nullptr || ((uintptr_t)p & 15u) == 0; }
-
-#define REQUIRE_PTR(entry, p)                                                        \
-    do {                                                                             \
-        if ((p) == nullptr) return fail(SSM_ERR_INVALID_ARG, "%s: %s is NULL", entry, #p); \
-    } while (0)
-#define REQUIRE_POS(entry, v)                                                                  \
-    do {                                                                                       \
-        if ((v) <= 0) return fail(SSM_ERR_INVALID_ARG, "%s: %s must be > 0 (got %lld)", entry, \
-                                  #v, (long long)(v));                                         \
-    } while (0)
-#define REQUIRE_ALIGN(entry, p)                                                                 \
-    do {                                                                                        \
-        if (!aligned16(p)) return fail(SSM_ERR_UNSUPPORTED, "%s: %s is not 16-byte aligned", \
-                                       entry, #p);                                              \
-    } while (0)
-
 int launched(const char *entry, hipError_t e, const char *kernel) {
     if (e != hipSuccess)
         return fail(SSM_ERR_HIP, "%s: launch of %s failed: %s", entry, kernel, hipGetErrorString(e));
@@ -46,18 +30,16 @@ int launched(const char *entry, hipError_t e, const char *kernel) {
     return SSM_OK;
 }
 
-// elements of a tensor must stay addressable with 64-bit offsets and the grid
-// with 32-bit block counts
-bool too_big(int64_t a, int64_t b, int64_t c, int64_t d) {
-    const double n = (double)a * (double)b * (double)c * (double)d;
-    return n > 9.0e15;
-}
+}  // namespace ssm
 
-}  // namespace
+using ssm::aligned16;
+using ssm::fail;
+using ssm::launched;
+using ssm::too_big;
 
 extern "C" {
 
-const char *ssm_last_error(void) { return g_err; }
+const char *ssm_last_error(void) { return ssm::g_err; }
 
 size_t ssm_s6_scan_fwd_workspace_size(int64_t batch, int64_t L, int64_t d_inner, int64_t d_state) {
     if (batch <= 0 || L <= 0 || d_inner <= 0 || d_state <= 0) return 0;

@@ -185,7 +185,8 @@ int ssm_qk_norm_rope_cache_fwd(const void *q, const void *k, const void *v, cons
  * 8-bit cache), <= SSM_ATTN_MAX_HEADDIM; q, o, k_cache, v_cache 16-byte aligned
  * and every stride of q and of the caches a multiple of 16 bytes; max_pages *
  * page_size at most 2^30, n_pages * page_size below 2^31; a cache's extent below
- * 2^36 bytes; batch * max_pages * page_size * n_kv_heads / 128 below 2^31.
+ * 2^36 bytes; batch * n_kv_heads * max_pages * page_size / 16 below 2^31 (all
+ * times the passes).
  * The cache is read once per 16 query heads of a kv head.  Work is cut by
  * length, not by row, into equal shares over the chip, whatever the lengths
  * are, and the shares of a row are joined by their maxima and sums.

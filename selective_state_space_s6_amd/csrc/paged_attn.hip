@@ -2,9 +2,10 @@
 // (ssm_paged_attn_decode_fwd in include/ssm_attn.h).
 //
 // Every cached byte is read once, for the query heads that share it, so the bound
-// is HBM (one request alone: latency).  The work is cut by length: a unit is 128
-// tokens of one (row, kv head), the units of all rows stand in one line, and each
-// block takes an equal piece of it, whatever the rows' lengths are.  A piece that
+// is HBM (one request alone: latency).  The work is cut by length: a unit is a tile
+// for each wave of a block (128 tokens; fp32: 64) of one (row, kv head), the units of
+// all rows stand in one line, and each resident block takes an equal piece of it,
+// whatever the rows' lengths are.  A piece that
 // does not hold a whole (row, kv head) leaves its unnormalised output, maximum and
 // sum in the workspace, and a second kernel joins those.
 //
@@ -36,11 +37,10 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kNT = 256;
-constexpr int kWaves = kNT / 64;
+constexpr int kNT = 256;            // threads of the joining kernel's blocks
 constexpr int kHeads = 16;          // query heads of a pass
-constexpr int kUnit = 128;          // tokens of a unit of work
-constexpr int kBlocks = 768;        // pieces of work: 3 blocks on each of 256 compute units
+constexpr int kCUs = 256;
+
 
 enum { KBF16, KF8, KF32 };
 
@@ -52,18 +52,18 @@ struct Kp {
     int64_t table_stride, q_sr, q_sh, c_sh;    // q and cache strides in bytes
     uint32_t c_sp16, c_st16;        // cache strides of page and token in 16 bytes
     int batch, n_heads, n_kv, group, passes, gmax;   // group: query heads a kv head; passes of gmax <= 16 of them
-    int d, n_pages, page_size, max_len, window;
+    int d, n_pages, page_size, max_len, window, unit, unit_lg;
+    int wh_lg;                      // 2^wh_lg kv heads side by side (place_of_block)
     float scale2, v_scale;          // scale2: score -> log2 units
 };
 
-// The tokens of a row: [lo, hi), from `base` (a multiple of a tile) in `units` units
-struct Span { int lo, hi, base, units; };
-__device__ __forceinline__ Span span_of(const Kp &a, int r) {
+// The tokens of a row: [lo, hi), in `units` units
+struct Span { int lo, hi, units; };
+__device__ __forceinline__ Span span_of(const Kp &a, int len) {
     Span s;
-    s.hi = min(max(a.lens[r], 0), a.max_len);
+    s.hi = min(max(len, 0), a.max_len);
     s.lo = a.window > 0 ? max(0, s.hi - a.window) : 0;
-    s.base = s.lo & ~31;
-    s.units = (s.hi - s.base + kUnit - 1) / kUnit;
+    s.units = (s.hi - s.lo + a.unit - 1) >> a.unit_lg;
     return s;
 }
 
@@ -86,6 +86,18 @@ __device__ __forceinline__ uint32_t widen(uint32_t w) {
 __device__ __forceinline__ uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) {
     return __builtin_amdgcn_perm(hi, lo, sel);
 }
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ int dpp_i(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, true); }
+// inclusive sums over a wave: within rows of 16 lanes, then the rows' last lanes onward
+__device__ __forceinline__ int wave_scan(int v) {
+    v += dpp_i<0x111>(v);
+    v += dpp_i<0x112>(v);
+    v += dpp_i<0x114>(v);
+    v += dpp_i<0x118>(v);
+    v += dpp_i<0x142, 0xa>(v);
+    v += dpp_i<0x143, 0xc>(v);
+    return v;
+}
 // over the four lanes that hold a head
 __device__ __forceinline__ float head_max(float v) {
     v = fmaxf(v, __shfl_xor(v, 16));
@@ -97,10 +109,11 @@ __device__ __forceinline__ float head_sum(float v) {
 }
 
 // One (cache type, padded head size): register shapes of a tile
-template <int CT, int DP> struct Tile {
-    static constexpr int NT = CT == KF32 ? 16 : 32;            // tokens
-    static constexpr int SUB = NT / 16;                        // 16-token blocks of scores
+template <int CT, int DP, int W> struct Tile {
     static constexpr int E = CT == KF32 ? 4 : CT == KBF16 ? 2 : 1;
+    // tokens: about 8 KiB of K (and of V), so that a wave has that much on its way at any time
+    static constexpr int NT = CT == KF32 ? (DP <= 64 ? 32 : 16) : CT == KBF16 ? (DP <= 64 ? 64 : 32) : 64;
+    static constexpr int SUB = NT / 16;                        // 16-token blocks of scores
     static constexpr int KD = 16 / E;                          // dims of a 16-byte load of K
     static constexpr int KC = DP / (4 * KD);                   // loads of a K row (four lanes each)
     static constexpr int VD = CT == KF32 || DP % 128 ? 4 : 8;  // dims of a lane's load of V
@@ -108,6 +121,13 @@ template <int CT, int DP> struct Tile {
     static constexpr int VW = VD * E / 4;                      // dwords of one
     static constexpr int VR = NT / 4;                          // V rows of a lane
     static constexpr int QW = CT == KF8 ? 2 : 1;               // operands of q to a K load
+    static constexpr int UNIT = W * NT;
+    // resident blocks of a compute unit, by the registers of a tile's K, V and output (and of q,
+    // which waits in LDS where those leave it no room)
+    static constexpr int PER_SIMD = DP <= 128 ? 2 : 1;         // waves on one of a compute unit's 4
+    static constexpr int RES = PER_SIMD * 4 / W;
+    static constexpr bool QLDS = DP > 128;
+    static constexpr uint64_t ALL = NT == 64 ? ~uint64_t(0) : (uint64_t(1) << NT) - 1;
 };
 
 template <int N> struct Words { uint32_t w[N]; };
@@ -126,88 +146,131 @@ __device__ __forceinline__ Words<N> ld_words(const char *p) {
     return r;
 }
 
-template <int CT, int DP, bool EXACT>      // EXACT: headdim == DP
-__global__ void __launch_bounds__(kNT, 2) paged_attn_kernel(Kp a) {
-    using T = Tile<CT, DP>;
+template <int CT, int DP> struct KRows { u32x4 r[Tile<CT, DP, 1>::SUB][Tile<CT, DP, 1>::KC]; };
+// K rows of a tile: lane (grp, col) takes dims grp * KD (+ 4 KD c) of tokens col (+ 16)
+template <int CT, int DP, bool EXACT>
+__device__ __forceinline__ void load_k(KRows<CT, DP> &kf, const char *kb, uint32_t off, int col, int grp, int d) {
+    using T = Tile<CT, DP, 1>;
+#pragma unroll
+    for (int s = 0; s < T::SUB; ++s) {
+        const char *p = kb + (uint64_t)(uint32_t)__shfl((int)off, 16 * s + col) * 16;
+#pragma unroll
+        for (int c = 0; c < T::KC; ++c) {
+            // past headdim: the row's own first dims, and zero instead
+            const bool in = EXACT || (c * 4 + grp) * T::KD < d;
+            const u32x4 x = *(const u32x4 *)(p + (in ? c * 64 : -grp * 16));
+            kf.r[s][c] = in ? x : (u32x4){0, 0, 0, 0};
+        }
+    }
+}
+
+// 2^lg kv heads side by side take the same tokens at the same time, on blocks of one XCD
+// (blocks go round the 8 of them): where a row of the cache holds the heads next to
+// each other and one head's part of it does not fill whole cache lines, the lines that
+// two heads share then come from that XCD's L2 for the second of them.
+__device__ __forceinline__ int worker_of(int blk, int lg) { return (blk >> (3 + lg)) * 8 + (blk & 7); }
+__device__ __forceinline__ int side_of(int blk, int lg) { return (blk >> 3) & ((1 << lg) - 1); }
+__device__ __forceinline__ int block_of(int worker, int side, int lg) {
+    return lg == 0 ? worker : (((worker >> 3) << lg) + side) * 8 + (worker & 7);
+}
+
+template <int CT, int DP, bool EXACT, int W>      // EXACT: headdim == DP; W: waves of a block
+__global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_attn_kernel(Kp a) {
+    using T = Tile<CT, DP, W>;
     constexpr int VD = T::VD, VB = T::VB;
-    extern __shared__ float lds[];          // the waves' outputs, at a piece's end
-    __shared__ int scan[kWaves], found[3];
-    __shared__ float wave_m[kWaves][kHeads], wave_l[kWaves][kHeads];
+    extern __shared__ float lds[];          // q, and at a piece's end the waves' outputs
+    u32x4 *q_lds = (u32x4 *)lds;
+    __shared__ int scan[W], found[3];
+    __shared__ float wave_m[W][kHeads], wave_l[W][kHeads];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int col = lane & 15, grp = lane >> 4;
 
     // ---- this block's piece [u, u_end) of the line of units, and the row that u is in
-    const int per = a.n_kv * a.passes;      // (kv head, pass) of a row
-    int units = 0;
-    for (int r0 = 0; r0 < a.batch; r0 += kNT) {
-        const int r = r0 + tid;
-        units += r < a.batch ? span_of(a, r).units : 0;
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) units += __shfl_xor(units, o);
-    if (lane == 0) scan[wave] = units;
+    const int per = (a.n_kv >> a.wh_lg) * a.passes;      // (kv heads side by side, pass) of a row
+    const int blk = worker_of(blockIdx.x, a.wh_lg), side = side_of(blockIdx.x, a.wh_lg);
+    const int mine = (a.batch + W * 64 - 1) / (W * 64), r0 = tid * mine, r1 = min(r0 + mine, a.batch);   // a thread's rows
+    int own_units = 0;
+    for (int r = r0; r < r1; ++r) own_units += span_of(a, a.lens[r]).units * per;
+    int before = wave_scan(own_units), units = 0;
+    if (lane == 63) scan[wave] = before;
     __syncthreads();
-    units = 0;
+    before -= own_units;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) units += scan[w];
-    units *= per;
-    const int blocks = min((int)gridDim.x, units), blk = blockIdx.x;
+    for (int w = 0; w < W; ++w) {
+        before += w < wave ? scan[w] : 0;
+        units += scan[w];
+    }
+    const int blocks = min((int)gridDim.x >> a.wh_lg, units);
     if (blk > 0 && blk >= blocks) return;
     int u = blocks ? (int)((int64_t)blk * units / blocks) : 0;
     const int u_end = blocks ? (int)((int64_t)(blk + 1) * units / blocks) : 0;
-    for (int r0 = 0, base = 0; r0 < a.batch; r0 += kNT) {
-        const int r = r0 + tid;
-        const int n = r < a.batch ? span_of(a, r).units * per : 0;
-        int v = n;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int b = __shfl_up(v, o);
-            if (lane >= o) v += b;
+    if (blockIdx.x == 0 || (u >= before && u < before + own_units)) {
+        for (int r = r0; r < r1; ++r) {
+            const int len = a.lens[r], n = span_of(a, len).units * per;
+            if (u >= before && u < before + n) { found[0] = r; found[1] = before; found[2] = len; }
+            if (blockIdx.x == 0) a.start[r] = before;
+            before += n;
         }
-        __syncthreads();
-        if (lane == 63) scan[wave] = v;
-        __syncthreads();
-        int total = 0;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            v += w < wave ? scan[w] : 0;
-            total += scan[w];
-        }
-        v += base - n;                       // units before row r
-        if (n > 0 && u >= v && u < v + n) { found[0] = r; found[1] = v; }
-        if (blk == 0 && r < a.batch) a.start[r] = v;
-        base += total;
     }
-    if (blk == 0 && tid == 0) a.start[a.batch] = units;
+    if (blockIdx.x == 0 && tid == 0) a.start[a.batch] = units;
     __syncthreads();
     if (u >= u_end) return;
     int row = found[0], row_u = found[1];
+    Span sp = span_of(a, found[2]);
 
     while (u < u_end) {
-        Span sp = span_of(a, row);
         while (u >= row_u + sp.units * per) {
             row_u += sp.units * per;
-            sp = span_of(a, ++row);
+            sp = span_of(a, a.lens[++row]);
         }
         const int at = u - row_u, hp = at / sp.units, first = at - hp * sp.units;
         const int last = min(sp.units, first + (u_end - u));          // units [first, last) of this head
-        const int kv = hp / a.passes, pass = hp - kv * a.passes;
+        const int kvs = hp / a.passes, pass = hp - kvs * a.passes, kv = (kvs << a.wh_lg) + side;
         const int nh = min(a.gmax, a.group - pass * a.gmax);          // query heads of this pass
         const int h0 = kv * a.group + pass * a.gmax;
         u += last - first;
 
+        const char *kb = a.k + kv * a.c_sh + grp * 16, *vb = a.v + kv * a.c_sh;
+        const int32_t *table = a.table + row * a.table_stride;
+        const int t_end = min(sp.hi, sp.lo + last * T::UNIT);
+        int t0 = sp.lo + first * T::UNIT + wave * T::NT;
+
+        // A lane's token of a tile: its page (-1: not the row's), and its place in the cache
+        // in 16 bytes.  Tokens that are not the row's read the cache's first row, and are masked.
+        auto page_of = [&](int tile) {
+            const int t = tile + (lane & (T::NT - 1));
+            return t < sp.hi && tile < t_end ? table[(uint32_t)t / (uint32_t)a.page_size] : -1;
+        };
+        auto place_of = [&](int tile, int page) {
+            const uint32_t t = (uint32_t)(tile + (lane & (T::NT - 1)));
+            return (uint32_t)page < (uint32_t)a.n_pages ? (uint32_t)page * a.c_sp16 + t % (uint32_t)a.page_size * a.c_st16 : 0u;
+        };
+        auto tokens_of = [&](int page) {
+            return (uint64_t)__ballot((uint32_t)page < (uint32_t)a.n_pages) & T::ALL;
+        };
+        // The pipeline: while a tile's scores are formed its V rows are on their way, while its
+        // output is, the next tile's K rows; the page after that is asked for a tile earlier.
+        int page = page_of(t0);
+        uint64_t ok = tokens_of(page);
+        uint32_t off = place_of(t0, page);
+        KRows<CT, DP> kf;
+        load_k<CT, DP, EXACT>(kf, kb, off, col, grp, a.d);
+        page = page_of(t0 + T::UNIT);
+
         // q, as the scores' second operand
-        u32x4 qf[T::KC * T::QW];
+        u32x4 qf[T::QLDS ? 1 : T::KC * T::QW];
+        if (T::QLDS) __syncthreads();        // readers of the piece before
 #pragma unroll
-        for (int c = 0; c < T::KC; ++c)
-#pragma unroll
-            for (int w = 0; w < T::QW; ++w) {
-                const int dim = c * 4 * T::KD + grp * T::KD + w * 8;
-                u32x4 x = {0, 0, 0, 0};
-                if (col < nh && (EXACT || dim < a.d))
-                    x = *(const u32x4 *)(a.q + row * a.q_sr + (h0 + col) * a.q_sh + dim * (CT == KF32 ? 4 : 2));
-                qf[c * T::QW + w] = x;
-            }
+        for (int i = 0; i < T::KC * T::QW; ++i) {
+            if (T::QLDS && i % W != wave) continue;
+            const int dim = i / T::QW * 4 * T::KD + grp * T::KD + i % T::QW * 8;
+            u32x4 x = {0, 0, 0, 0};
+            if (col < nh && (EXACT || dim < a.d))
+                x = *(const u32x4 *)(a.q + row * a.q_sr + (h0 + col) * a.q_sh + dim * (CT == KF32 ? 4 : 2));
+            if constexpr (T::QLDS) q_lds[i * 64 + lane] = x;
+            else qf[i] = x;
+        }
+        if (T::QLDS) __syncthreads();
 
         float m = -INFINITY, l = 0.0f;       // of head col; l over this lane's tokens only
         f32x4 acc[VB][VD];
@@ -216,66 +279,45 @@ __global__ void __launch_bounds__(kNT, 2) paged_attn_kernel(Kp a) {
 #pragma unroll
             for (int i = 0; i < VD; ++i) acc[b][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 
-        const char *kb = a.k + kv * a.c_sh + grp * 16, *vb = a.v + kv * a.c_sh + col * VD * T::E;
-        const int32_t *table = a.table + row * a.table_stride;
-        const int t_end = min(sp.hi, sp.base + last * kUnit);
-        for (int t0 = sp.base + first * kUnit + wave * T::NT; t0 < t_end; t0 += kWaves * T::NT) {
-            // this lane's token of the tile: its place in the cache, in 16 bytes; rows that
-            // are not the request's are read at the cache's first row and masked
-            const int t = t0 + (lane & (T::NT - 1));
-            bool valid = t >= sp.lo && t < sp.hi;
-            uint32_t off = 0;
-            if (valid) {
-                const uint32_t p = (uint32_t)t / (uint32_t)a.page_size;
-                const int page = table[p];
-                valid = page >= 0 && page < a.n_pages;
-                if (valid) off = (uint32_t)page * a.c_sp16 + ((uint32_t)t - p * (uint32_t)a.page_size) * a.c_st16;
-            }
-            const uint32_t ok = (uint32_t)__ballot(valid);
-            const bool full = T::NT == 32 ? ok == 0xffffffffu : (ok & 0xffffu) == 0xffffu;
-
-            u32x4 kf[T::SUB][T::KC];
-#pragma unroll
-            for (int s = 0; s < T::SUB; ++s) {
-                const char *p = kb + (uint64_t)__shfl(off, 16 * s + col) * 16;
-#pragma unroll
-                for (int c = 0; c < T::KC; ++c) {
-                    kf[s][c] = (u32x4){0, 0, 0, 0};
-                    if (EXACT || (c * 4 + grp) * T::KD < a.d) kf[s][c] = *(const u32x4 *)(p + c * 64);
-                }
-            }
+        for (; t0 < t_end; t0 += T::UNIT) {
+            const bool full = ok == T::ALL;
             Words<T::VW> vf[T::VR][VB];
 #pragma unroll
             for (int j = 0; j < T::VR; ++j) {
                 const int tok = (j >> 2) * 16 + grp * 4 + (j & 3);
-                const char *p = vb + (uint64_t)__shfl(off, tok) * 16;
-                const bool have = full || (ok >> tok & 1);
+                const char *p = vb + (uint64_t)(uint32_t)__shfl((int)off, tok) * 16;
 #pragma unroll
-                for (int b = 0; b < VB; ++b) {
-#pragma unroll
-                    for (int w = 0; w < T::VW; ++w) vf[j][b].w[w] = 0;
-                    if (have && (EXACT || (b * 16 + col) * VD < a.d)) vf[j][b] = ld_words<T::VW>(p + b * 16 * VD * T::E);
+                for (int b = 0; b < VB; ++b) {       // past headdim: the row's first dims, in rows of the result that are not kept
+                    const int dim = (b * 16 + col) * VD;
+                    vf[j][b] = ld_words<T::VW>(p + (EXACT || dim < a.d ? dim * T::E : 0));
                 }
             }
 
             f32x4 s[T::SUB];
 #pragma unroll
-            for (int i = 0; i < T::SUB; ++i) {
-                s[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+            for (int i = 0; i < T::SUB; ++i) s[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int c = 0; c < T::KC; ++c) {
-                    const u32x4 k = kf[i][c];
+            for (int c = 0; c < T::KC; ++c) {
+                u32x4 q[T::QW];
+#pragma unroll
+                for (int w = 0; w < T::QW; ++w) {
+                    if constexpr (T::QLDS) q[w] = q_lds[(c * T::QW + w) * 64 + lane];
+                    else q[w] = qf[c * T::QW + w];
+                }
+#pragma unroll
+                for (int i = 0; i < T::SUB; ++i) {
+                    const u32x4 k = kf.r[i][c];
                     if constexpr (CT == KBF16) {
-                        s[i] = mfma_bf16(k, qf[c], s[i]);
+                        s[i] = mfma_bf16(k, q[0], s[i]);
                     } else if constexpr (CT == KF8) {
                         const u32x4 k0 = {widen<false>(k[0]), widen<true>(k[0]), widen<false>(k[1]), widen<true>(k[1])};
                         const u32x4 k1 = {widen<false>(k[2]), widen<true>(k[2]), widen<false>(k[3]), widen<true>(k[3])};
-                        s[i] = mfma_bf16(k0, qf[2 * c], s[i]);
-                        s[i] = mfma_bf16(k1, qf[2 * c + 1], s[i]);
+                        s[i] = mfma_bf16(k0, q[0], s[i]);
+                        s[i] = mfma_bf16(k1, q[T::QW - 1], s[i]);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            s[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k[e]), __uint_as_float(qf[c][e]), s[i], 0, 0, 0);
+                            s[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k[e]), __uint_as_float(q[0][e]), s[i], 0, 0, 0);
                     }
                 }
             }
@@ -287,6 +329,21 @@ __global__ void __launch_bounds__(kNT, 2) paged_attn_kernel(Kp a) {
                 x[j] = full || (ok >> tok & 1) ? v : -INFINITY;
                 top = fmaxf(top, x[j]);
             }
+            if (!full) {                     // 0 * what stands in a row that is not the request's
+#pragma unroll
+                for (int j = 0; j < T::VR; ++j)
+#pragma unroll
+                    for (int b = 0; b < VB; ++b)
+#pragma unroll
+                        for (int w = 0; w < T::VW; ++w)
+                            vf[j][b].w[w] = ok >> ((j >> 2) * 16 + grp * 4 + (j & 3)) & 1 ? vf[j][b].w[w] : 0u;
+            }
+            // the next tile's K
+            ok = tokens_of(page);
+            off = place_of(t0 + T::UNIT, page);
+            if (t0 + T::UNIT < t_end) load_k<CT, DP, EXACT>(kf, kb, off, col, grp, a.d);
+            page = page_of(t0 + 2 * T::UNIT);
+
             const float m_new = fmaxf(m, head_max(top));
             const float m_use = m_new == -INFINITY ? 0.0f : m_new;     // no token yet: all p are 0
             if (__any(m_new > m)) {
@@ -305,7 +362,7 @@ __global__ void __launch_bounds__(kNT, 2) paged_attn_kernel(Kp a) {
             }
             if constexpr (CT == KF32) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < T::VR; ++j)
 #pragma unroll
                     for (int b = 0; b < VB; ++b)
 #pragma unroll
@@ -313,38 +370,41 @@ __global__ void __launch_bounds__(kNT, 2) paged_attn_kernel(Kp a) {
                             acc[b][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vf[j][b].w[i]), x[j], acc[b][i], 0, 0, 0);
             } else {
                 // p as the sum of two bf16 values: one alone would double the output's error
-                u32x4 ph, pl;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    ph[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
-                    pl[j] = pack_bf16(x[2 * j] - lo_f(ph[j]), x[2 * j + 1] - hi_f(ph[j]));
-                }
+                for (int g = 0; g < T::VR; g += 8) {     // 32 tokens at a time
+                    u32x4 ph, pl;
 #pragma unroll
-                for (int b = 0; b < VB; ++b) {
-                    if constexpr (CT == KBF16) {
+                    for (int j = 0; j < 4; ++j) {
+                        ph[j] = pack_bf16(x[g + 2 * j], x[g + 2 * j + 1]);
+                        pl[j] = pack_bf16(x[g + 2 * j] - lo_f(ph[j]), x[g + 2 * j + 1] - hi_f(ph[j]));
+                    }
 #pragma unroll
-                        for (int i = 0; i < VD; ++i) {
-                            u32x4 vt;
+                    for (int b = 0; b < VB; ++b) {
+                        if constexpr (CT == KBF16) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                vt[j] = perm(vf[2 * j + 1][b].w[i / 2], vf[2 * j][b].w[i / 2], i & 1 ? 0x07060302u : 0x05040100u);
-                            acc[b][i] = mfma_bf16(vt, ph, acc[b][i]);
-                            acc[b][i] = mfma_bf16(vt, pl, acc[b][i]);
-                        }
-                    } else {
+                            for (int i = 0; i < VD; ++i) {
+                                u32x4 vt;
 #pragma unroll
-                        for (int i = 0; i < VD; i += 2) {
-                            u32x4 v0, v1;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t w = perm(vf[2 * j + 1][b].w[i / 4], vf[2 * j][b].w[i / 4], i & 2 ? 0x07030602u : 0x05010400u);
-                                v0[j] = widen<false>(w);
-                                v1[j] = widen<true>(w);
+                                for (int j = 0; j < 4; ++j)
+                                    vt[j] = perm(vf[g + 2 * j + 1][b].w[i / 2], vf[g + 2 * j][b].w[i / 2], i & 1 ? 0x07060302u : 0x05040100u);
+                                acc[b][i] = mfma_bf16(vt, ph, acc[b][i]);
+                                acc[b][i] = mfma_bf16(vt, pl, acc[b][i]);
                             }
-                            acc[b][i] = mfma_bf16(v0, ph, acc[b][i]);
-                            acc[b][i] = mfma_bf16(v0, pl, acc[b][i]);
-                            acc[b][i + 1] = mfma_bf16(v1, ph, acc[b][i + 1]);
-                            acc[b][i + 1] = mfma_bf16(v1, pl, acc[b][i + 1]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < VD; i += 2) {
+                                u32x4 v0, v1;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const uint32_t w = perm(vf[g + 2 * j + 1][b].w[i / 4], vf[g + 2 * j][b].w[i / 4], i & 2 ? 0x07030602u : 0x05010400u);
+                                    v0[j] = widen<false>(w);
+                                    v1[j] = widen<true>(w);
+                                }
+                                acc[b][i] = mfma_bf16(v0, ph, acc[b][i]);
+                                acc[b][i] = mfma_bf16(v0, pl, acc[b][i]);
+                                acc[b][i + 1] = mfma_bf16(v1, ph, acc[b][i + 1]);
+                                acc[b][i + 1] = mfma_bf16(v1, pl, acc[b][i + 1]);
+                            }
                         }
                     }
                 }
@@ -358,7 +418,7 @@ __global__ void __launch_bounds__(kNT, 2) paged_attn_kernel(Kp a) {
         __syncthreads();
         float top = wave_m[0][col];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, wave_m[w][col]);
+        for (int w = 1; w < W; ++w) top = fmaxf(top, wave_m[w][col]);
         const float f = top == -INFINITY ? 0.0f : exp2_fast(m - top);
         constexpr int PITCH = DP + 4;
         if (col < nh) {
@@ -374,19 +434,19 @@ __global__ void __launch_bounds__(kNT, 2) paged_attn_kernel(Kp a) {
         }
         __syncthreads();
         const bool whole = first == 0 && last == sp.units;
-        const int slot = 2 * blk + (first == 0 ? 1 : 0);
+        const int slot = 2 * (int)blockIdx.x + (first == 0 ? 1 : 0);
         const int d4 = a.d / 4;
-        for (int i = tid; i < nh * d4; i += kNT) {
+        for (int i = tid; i < nh * d4; i += W * 64) {
             const int h = i / d4, e = (i - h * d4) * 4;
             f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
             float ls = 0.0f, mt = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
+            for (int w = 0; w < W; ++w) {
                 v += *(const f32x4 *)(lds + (w * a.gmax + h) * PITCH + e);
                 mt = fmaxf(mt, wave_m[w][h]);
             }
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) ls += wave_l[w][h] * (mt == -INFINITY ? 0.0f : exp2_fast(wave_m[w][h] - mt));
+            for (int w = 0; w < W; ++w) ls += wave_l[w][h] * (mt == -INFINITY ? 0.0f : exp2_fast(wave_m[w][h] - mt));
             if (whole) {
                 const float n = ls > 0.0f || ls != ls ? a.v_scale / ls : 0.0f;
                 const int64_t to = ((int64_t)row * a.n_heads + h0 + h) * a.d + e;
@@ -402,85 +462,115 @@ __global__ void __launch_bounds__(kNT, 2) paged_attn_kernel(Kp a) {
 }
 
 // Joins the pieces of one (row, query head): piece i's share is scaled by
-// 2^(m_i - max m).  Rows without tokens get o = 0, lse = -inf here.
+// 2^(m_i - max m).  Rows without tokens get o = 0, lse = -inf here.  A block joins d / gridDim.z
+// dims; every wave forms the maximum and the sum for itself, so the only wait is for
+// the slices of the pieces that the block's threads add up.
 template <bool BF16>
 __global__ void __launch_bounds__(kNT) paged_attn_join_kernel(Kp a, int grid) {
-    __shared__ float red[kWaves], out[kNT * 4];
-    const int row = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int per = a.n_kv * a.passes;
-    const int kv = h / a.group, pass = (h - kv * a.group) / a.gmax, hh = h - kv * a.group - pass * a.gmax;
+    __shared__ f32x4 out[kNT];
+    const int row = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+    const int per = (a.n_kv >> a.wh_lg) * a.passes;
+    const int kv = h / a.group, side = kv & ((1 << a.wh_lg) - 1), pass = (h - kv * a.group) / a.gmax, hh = h - kv * a.group - pass * a.gmax;
     const int64_t total = a.start[a.batch];
-    const int nu = (a.start[row + 1] - a.start[row]) / per;
+    const int row_u = a.start[row], nu = (a.start[row + 1] - row_u) / per;
     const int64_t to = ((int64_t)row * a.n_heads + h) * a.d;
+    const int cols = a.d / 4 / gridDim.z, slices = kNT / cols, sl = tid / cols, e = ((int)blockIdx.z * cols + tid - sl * cols) * 4;
+    auto store = [&](f32x4 v) {
+        if constexpr (BF16) *(uint2 *)(a.o + (to + e) * 2) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        else *(f32x4 *)(a.o + (to + e) * 4) = v;
+    };
+    const bool first = tid == 0 && blockIdx.z == 0 && a.lse;
     if (nu == 0) {
-        for (int e = tid; e < a.d; e += kNT) {
-            if (BF16) ((uint16_t *)a.o)[to + e] = 0;
-            else ((float *)a.o)[to + e] = 0.0f;
-        }
-        if (tid == 0 && a.lse) a.lse[(int64_t)row * a.n_heads + h] = -INFINITY;
+        if (sl == 0) store((f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+        if (first) a.lse[(int64_t)row * a.n_heads + h] = -INFINITY;
         return;
     }
     // the blocks whose pieces hold this head's first and last unit
-    const int64_t blocks = min((int64_t)grid, total), u0 = a.start[row] + (int64_t)(kv * a.passes + pass) * nu;
+    const int64_t blocks = min((int64_t)(grid >> a.wh_lg), total), u0 = row_u + (int64_t)((kv >> a.wh_lg) * a.passes + pass) * nu;
     const int b0 = (int)(((u0 + 1) * blocks - 1) / total), b1 = (int)(((u0 + nu) * blocks - 1) / total);
     if (b0 == b1) return;                    // written whole
     const int n = b1 - b0 + 1;
     // the first block began this head (its second place); the others go on with it (their first)
-    auto place = [&](int i) { return (int64_t)(i == 0 ? 2 * b0 + 1 : 2 * (b0 + i)) * a.gmax + hh; };
-    float m = -INFINITY;
-    for (int i = tid; i < n; i += kNT) m = fmaxf(m, a.ml[place(i) * 2]);
+    auto place = [&](int i) { return ((int64_t)block_of(b0 + i, side, a.wh_lg) * 2 + (i == 0 ? 1 : 0)) * a.gmax + hh; };
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f}, part0 = v, part1 = v;
+    // the first two shares of a slice need not wait for the maximum
+    const bool in0 = sl < slices && sl < n, in1 = sl < slices && sl + slices < n;
+    if (in0) part0 = *(const f32x4 *)(a.part + place(sl) * a.d + e);
+    if (in1) part1 = *(const f32x4 *)(a.part + place(sl + slices) * a.d + e);
+    // lane i of each wave: pieces i, i + 64, ...
+    float2 mine = make_float2(-INFINITY, 0.0f);
+    if (lane < n) mine = *(const float2 *)(a.ml + place(lane) * 2);
+    float m = mine.x, l = 0.0f;
+    for (int i = lane + 64; i < n; i += 64) m = fmaxf(m, a.ml[place(i) * 2]);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    if (lane == 0) red[wave] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float m_use = m == -INFINITY ? 0.0f : m;
-    __syncthreads();
-    float l = 0.0f;
-    for (int i = tid; i < n; i += kNT) l += a.ml[place(i) * 2 + 1] * exp2_fast(a.ml[place(i) * 2] - m_use);
+    m = m == -INFINITY ? 0.0f : m;
+    const float scale = exp2_fast(mine.x - m);
+    l = mine.y * scale;
+    for (int i = lane + 64; i < n; i += 64) {
+        const float2 w = *(const float2 *)(a.ml + place(i) * 2);
+        l += w.y * exp2_fast(w.x - m);
+    }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o);
-    if (lane == 0) red[wave] = l;
-    const int d4 = a.d / 4, slices = kNT / d4, sl = tid / d4, e = (tid - sl * d4) * 4;
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (sl < slices)
-        for (int i = sl; i < n; i += slices)
-            v += *(const f32x4 *)(a.part + place(i) * a.d + e) * exp2_fast(a.ml[place(i) * 2] - m_use);
-    *(f32x4 *)(out + tid * 4) = v;
-    __syncthreads();
-    l = red[0] + red[1] + red[2] + red[3];
-    if (tid < d4) {
-        for (int s = 1; s < slices; ++s) v += *(const f32x4 *)(out + (s * d4 + tid) * 4);
-        v *= l > 0.0f || l != l ? a.v_scale / l : 0.0f;
-        if (BF16) *(uint2 *)(a.o + (to + e) * 2) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-        else *(f32x4 *)(a.o + (to + e) * 4) = v;
+    const float s0 = __shfl(scale, sl & 63), s1 = __shfl(scale, (sl + slices) & 63);
+    if (in0) v = part0 * (sl < 64 ? s0 : exp2_fast(a.ml[place(sl) * 2] - m));
+    if (in1) v += part1 * (sl + slices < 64 ? s1 : exp2_fast(a.ml[place(sl + slices) * 2] - m));
+    if (sl < slices) {
+#pragma unroll 4
+        for (int i = sl + 2 * slices; i < n; i += slices)
+            v += *(const f32x4 *)(a.part + place(i) * a.d + e) * exp2_fast(a.ml[place(i) * 2] - m);
     }
-    if (tid == 0 && a.lse) a.lse[(int64_t)row * a.n_heads + h] = m_use * kLn2 + logf(l);
+    out[tid] = v;
+    __syncthreads();
+    if (sl == 0) {
+        for (int s = 1; s < min(slices, n); ++s) v += out[s * cols + tid];
+        store(v * (l > 0.0f || l != l ? a.v_scale / l : 0.0f));
+        if (first) a.lse[(int64_t)row * a.n_heads + h] = m * kLn2 + logf(l);
+    }
 }
 
 // ------------------------------------------------------------------ host ----
 int64_t passes_of(int64_t group) { return (group + kHeads - 1) / kHeads; }
 int64_t align16(int64_t n) { return (n + 15) & ~int64_t(15); }
 
-// shared memory a block may have beyond the default needs no attribute up to 64 KiB; the
-// widest case (four waves, 16 heads, 256 dims) takes 65 KiB
-template <int CT, int DP, bool EXACT>
-hipError_t go(const Kp &k, int grid, hipStream_t stream) {
-    const size_t lds = (size_t)kWaves * k.gmax * (DP + 4) * sizeof(float);
-    if (lds > 64 * 1024 - 1024) {
-        const hipError_t e = hipFuncSetAttribute((const void *)paged_attn_kernel<CT, DP, EXACT>,
+template <int CT, int DP, bool EXACT, int W>
+hipError_t go_w(Kp &k, int &grid, hipStream_t stream) {
+    using T = Tile<CT, DP, W>;
+    k.unit = T::UNIT;
+    k.unit_lg = __builtin_ctz(T::UNIT);
+    while (k.wh_lg < 2 && (T::PER_SIMD == 1 || (k.c_sh << k.wh_lg) % 128 != 0) && (k.n_kv >> k.wh_lg) % 2 == 0) ++k.wh_lg;
+    // those that are resident at once, or one a unit if there are fewer; whole groups of heads side by side
+    const double units = (double)k.batch * k.n_kv * k.passes * ((k.max_len + T::UNIT - 1) / T::UNIT);
+    grid = (int)std::max(1.0, std::min(units, (double)(T::RES * kCUs)));
+    const int whole = 8 << k.wh_lg;
+    if (k.wh_lg > 0) grid = (grid + whole - 1) / whole * whole;
+    const size_t lds = std::max((size_t)W * k.gmax * (DP + 4) * sizeof(float), T::QLDS ? (size_t)T::KC * T::QW * 1024 : 0);
+    if (lds > 32 * 1024) {               // more than a block has unasked, from 64 KiB on
+        const hipError_t e = hipFuncSetAttribute((const void *)paged_attn_kernel<CT, DP, EXACT, W>,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((paged_attn_kernel<CT, DP, EXACT>), dim3((unsigned)grid), dim3(kNT), lds, stream, k);
+    hipLaunchKernelGGL((paged_attn_kernel<CT, DP, EXACT, W>), dim3((unsigned)grid), dim3(W * 64), lds, stream, k);
     return hipGetLastError();
 }
+// Where there is a (row, kv head) for every wave that fits the chip, a block is one wave: it
+// takes whole heads, short ones too, without waiting for others.  Else four waves share
+// the tokens of a piece, and fewer pieces are left to join.
+bool one_wave(int64_t batch, int64_t n_kv, int64_t passes, int per_simd) {
+    return batch * n_kv * passes >= per_simd * 4 * kCUs;
+}
+template <int CT, int DP, bool EXACT>
+hipError_t go(Kp &k, int &grid, hipStream_t stream) {
+    return one_wave(k.batch, k.n_kv, k.passes, Tile<CT, DP, 1>::PER_SIMD) ? go_w<CT, DP, EXACT, 1>(k, grid, stream)
+                                                                          : go_w<CT, DP, EXACT, 4>(k, grid, stream);
+}
 template <int CT, int DP>
-hipError_t go_d(const Kp &k, int grid, hipStream_t stream) {
+hipError_t go_d(Kp &k, int &grid, hipStream_t stream) {
     return k.d == DP ? go<CT, DP, true>(k, grid, stream) : go<CT, DP, false>(k, grid, stream);
 }
 template <int CT>
-hipError_t go_type(const Kp &k, int grid, hipStream_t stream) {
+hipError_t go_type(Kp &k, int &grid, hipStream_t stream) {
     if (k.d <= 64) return go_d<CT, 64>(k, grid, stream);
     if (k.d <= 128) return go_d<CT, 128>(k, grid, stream);
     if (k.d <= 192) return go_d<CT, 192>(k, grid, stream);
@@ -489,27 +579,31 @@ hipError_t go_type(const Kp &k, int grid, hipStream_t stream) {
 
 }  // namespace
 
+// (of the smallest unit, a tile of one wave)
 double paged_attn_max_units(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t max_pages, int64_t page_size) {
     const double len = (double)max_pages * (double)page_size;
-    return (double)batch * (double)n_kv_heads * (double)passes_of(n_heads / n_kv_heads) * ((len + kUnit - 1) / kUnit);
+    return (double)batch * (double)n_kv_heads * (double)passes_of(n_heads / n_kv_heads) * (len / 16 + 1.0);
 }
 
-static int64_t grid_of(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t max_pages, int64_t page_size) {
-    const double most = paged_attn_max_units(batch, n_heads, n_kv_heads, max_pages, page_size);
-    return most < kBlocks ? std::max<int64_t>(1, (int64_t)most) : kBlocks;
+// blocks of the largest grid that any cache type gives these sizes
+static int64_t most_blocks(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t headdim, int64_t max_pages,
+                           int64_t page_size) {
+    const int per_simd = headdim <= 128 ? 2 : 1;
+    const bool one = one_wave(batch, n_kv_heads, passes_of(n_heads / n_kv_heads), per_simd);
+    const double units = paged_attn_max_units(batch, n_heads, n_kv_heads, max_pages, page_size) + 32;
+    return (int64_t)std::min(units, (double)(per_simd * kCUs * (one ? 4 : 1)));
 }
 
 size_t paged_attn_workspace_bytes(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t headdim,
                                   int64_t max_pages, int64_t page_size) {
     const int64_t group = n_heads / n_kv_heads, gmax = std::min<int64_t>(group, kHeads);
-    const int64_t places = 2 * grid_of(batch, n_heads, n_kv_heads, max_pages, page_size) * gmax;
+    const int64_t places = 2 * most_blocks(batch, n_heads, n_kv_heads, headdim, max_pages, page_size) * gmax;
     return (size_t)(align16((batch + 1) * 4) + align16(places * 8) + places * headdim * 4);
 }
 
 hipError_t launch_paged_attn(const PagedAttnArgs &a, hipStream_t stream, const char **kernel_name) {
     *kernel_name = "paged_attn_kernel";
     const int e = a.kv_dtype == SSM_KV_F32 ? 4 : a.kv_dtype == SSM_KV_BF16 ? 2 : 1, qe = a.kv_dtype == SSM_KV_F32 ? 4 : 2;
-    const int64_t grid = grid_of(a.batch, a.n_heads, a.n_kv_heads, a.max_pages, a.page_size);
     Kp k = {};
     k.q = (const char *)a.q; k.k = (const char *)a.k_cache; k.v = (const char *)a.v_cache;
     k.table = a.block_table; k.lens = a.lens; k.o = (char *)a.o; k.lse = a.lse;
@@ -518,7 +612,7 @@ hipError_t launch_paged_attn(const PagedAttnArgs &a, hipStream_t stream, const c
     k.passes = (int)passes_of(k.group);
     char *ws = (char *)a.workspace;
     k.start = (int32_t *)ws; ws += align16((a.batch + 1) * 4);
-    k.ml = (float *)ws; ws += align16(2 * grid * k.gmax * 8);
+    k.ml = (float *)ws; ws += align16(2 * most_blocks(a.batch, a.n_heads, a.n_kv_heads, a.headdim, a.max_pages, a.page_size) * k.gmax * 8);
     k.part = (float *)ws;
     k.table_stride = a.table_stride; k.q_sr = a.q_sr * qe; k.q_sh = a.q_sh * qe; k.c_sh = a.c_sh * e;
     k.c_sp16 = (uint32_t)(a.c_sp * e / 16); k.c_st16 = (uint32_t)(a.c_st * e / 16);
@@ -528,14 +622,17 @@ hipError_t launch_paged_attn(const PagedAttnArgs &a, hipStream_t stream, const c
     k.window = a.window > 0 && a.window < k.max_len ? (int)a.window : 0;
     k.scale2 = a.scale * (a.kv_dtype == SSM_KV_F8E4M3 ? a.k_scale : 1.0f) * kLog2e;
     k.v_scale = a.kv_dtype == SSM_KV_F8E4M3 ? a.v_scale : 1.0f;
-    const hipError_t rc = a.kv_dtype == SSM_KV_F32 ? go_type<KF32>(k, (int)grid, stream)
-                        : a.kv_dtype == SSM_KV_BF16 ? go_type<KBF16>(k, (int)grid, stream)
-                                                    : go_type<KF8>(k, (int)grid, stream);
+    int grid = 0;
+    const hipError_t rc = a.kv_dtype == SSM_KV_F32 ? go_type<KF32>(k, grid, stream)
+                        : a.kv_dtype == SSM_KV_BF16 ? go_type<KBF16>(k, grid, stream)
+                                                    : go_type<KF8>(k, grid, stream);
     if (rc != hipSuccess) return rc;
     *kernel_name = "paged_attn_join_kernel";
-    const dim3 g((unsigned)a.batch, (unsigned)a.n_heads);
-    if (a.kv_dtype == SSM_KV_F32) hipLaunchKernelGGL((paged_attn_join_kernel<false>), g, dim3(kNT), 0, stream, k, (int)grid);
-    else hipLaunchKernelGGL((paged_attn_join_kernel<true>), g, dim3(kNT), 0, stream, k, (int)grid);
+    // few (row, head) pairs have many pieces each: more blocks a pair then, of 32 dims each
+    const int split = a.batch * a.n_heads < 2 * kCUs && a.headdim % 32 == 0 ? a.headdim / 32 : 1;
+    const dim3 g((unsigned)a.batch, (unsigned)a.n_heads, (unsigned)split);
+    if (a.kv_dtype == SSM_KV_F32) hipLaunchKernelGGL((paged_attn_join_kernel<false>), g, dim3(kNT), 0, stream, k, grid);
+    else hipLaunchKernelGGL((paged_attn_join_kernel<true>), g, dim3(kNT), 0, stream, k, grid);
     return hipGetLastError();
 }
 

@@ -120,6 +120,18 @@ CASES = [  # lens, H, Hk, d, cache, page, layout, window
     ([9000, 8000], 8, 1, 128, "f8", 64, "hnd", 4097),
     ([3001, 2000], 3, 1, 256, "f32", 16, "nhd", 0),
     ([100] * 300, 2, 2, 64, "bf16", 16, "nhd", 0),       # more rows than a block has threads
+    # kv heads side by side (their rows share cache lines, or are wide), rows over many blocks too
+    (EDGES + [3000], 8, 4, 80, "bf16", 16, "nhd", 0),
+    (EDGES + [9000], 8, 8, 64, "f8", 16, "nhd", 0),
+    ([20000, 3], 6, 6, 96, "f8", 24, "nhd", 10001),
+    ([7000, 3, 900], 8, 4, 256, "bf16", 16, "nhd", 0),
+    ([5000, 1], 6, 2, 192, "f32", 16, "nhd", 0),
+    # a (row, kv head) for every wave of the chip: blocks of one wave
+    (list(range(71)) * 16, 4, 2, 64, "bf16", 16, "nhd", 0),
+    (list(range(0, 280, 4)) * 8, 4, 4, 96, "bf16", 8, "nhd", 90),
+    (list(range(3, 143, 2)) * 8, 4, 4, 128, "f8", 64, "hnd", 0),
+    ([5, 0, 700] * 120, 6, 3, 256, "f32", 16, "nhd", 0),
+    ([2000] + [1] * 1100, 2, 2, 128, "f32", 16, "nhd", 0),
 ]
 
 

@@ -323,21 +323,21 @@ __global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_att
             }
             float x[T::VR], top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < T::VR; ++j) {
-                const int tok = (j >> 2) * 16 + grp * 4 + (j & 3);
-                const float v = s[j >> 2][j & 3] * a.scale2;
-                x[j] = full || (ok >> tok & 1) ? v : -INFINITY;
-                top = fmaxf(top, x[j]);
-            }
-            if (!full) {                     // 0 * what stands in a row that is not the request's
+            for (int j = 0; j < T::VR; ++j) x[j] = s[j >> 2][j & 3] * a.scale2;
+            if (!full) {                     // no weight, and not 0 * what stands in a row that is not the request's
+                const uint32_t bits[2] = {(uint32_t)ok >> (grp * 4), (uint32_t)(ok >> 32) >> (grp * 4)};
 #pragma unroll
-                for (int j = 0; j < T::VR; ++j)
+                for (int j = 0; j < T::VR; ++j) {
+                    const bool in = bits[j >> 3] >> ((j >> 2 & 1) * 16 + (j & 3)) & 1;
+                    x[j] = in ? x[j] : -INFINITY;
 #pragma unroll
                     for (int b = 0; b < VB; ++b)
 #pragma unroll
-                        for (int w = 0; w < T::VW; ++w)
-                            vf[j][b].w[w] = ok >> ((j >> 2) * 16 + grp * 4 + (j & 3)) & 1 ? vf[j][b].w[w] : 0u;
+                        for (int w = 0; w < T::VW; ++w) vf[j][b].w[w] = in ? vf[j][b].w[w] : 0u;
+                }
             }
+#pragma unroll
+            for (int j = 0; j < T::VR; ++j) top = fmaxf(top, x[j]);
             // the next tile's K
             ok = tokens_of(page);
             off = place_of(t0 + T::UNIT, page);
@@ -628,8 +628,9 @@ hipError_t launch_paged_attn(const PagedAttnArgs &a, hipStream_t stream, const c
                                                     : go_type<KF8>(k, grid, stream);
     if (rc != hipSuccess) return rc;
     *kernel_name = "paged_attn_join_kernel";
-    // few (row, head) pairs have many pieces each: more blocks a pair then, of 32 dims each
-    const int split = a.batch * a.n_heads < 2 * kCUs && a.headdim % 32 == 0 ? a.headdim / 32 : 1;
+    // where a head has many pieces, more blocks join it, of 32 dims each
+    const int split = (grid >> k.wh_lg) >= 64 * a.batch * (a.n_kv_heads >> k.wh_lg) * k.passes && a.headdim % 32 == 0
+                          ? a.headdim / 32 : 1;
     const dim3 g((unsigned)a.batch, (unsigned)a.n_heads, (unsigned)split);
     if (a.kv_dtype == SSM_KV_F32) hipLaunchKernelGGL((paged_attn_join_kernel<false>), g, dim3(kNT), 0, stream, k, grid);
     else hipLaunchKernelGGL((paged_attn_join_kernel<true>), g, dim3(kNT), 0, stream, k, grid);

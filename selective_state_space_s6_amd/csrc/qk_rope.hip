@@ -2,13 +2,16 @@
 // same pass, its gradients, and its form that writes k and v into a paged cache
 // (ssm_qk_norm_rope_* in include/ssm_attn.h).
 //
-// All of them move every element once and are bound by HBM.  A block takes some
-// tokens of one side (q, k or v).  It first forms the tokens' cosines and sines
-// once, into LDS (the heads of a token share them), then its lane groups take one
-// (token, head) each: a lane holds 2 V elements of the head, chosen so that both
-// halves of each rotated pair are its own, and only the norm's sums cross lanes.
+// All of them move every element once and are bound by HBM.  A wave takes a token at
+// a time (of few heads, several) of one side, q, k or v.  Its 64 lanes form the
+// token's cosines and sines, one or two each, and hand them round through a part of
+// LDS of their own; the heads of the token share them.  Then groups of lanes take one
+// head each: a lane holds 2 V elements of it, chosen so that both halves of each rotated
+// pair are its own, and only the norm's sums cross lanes.  The next heads' elements are
+// asked for before the present ones are worked on, and no wave waits for another.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <algorithm>
 
 #include "attn_launchers.hpp"
 #include "device_common.hpp"
@@ -19,8 +22,10 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kNT = 256;
-constexpr int kTabMax = 2048;       // angles of a block: 16 KiB of cosines and sines
+constexpr int kFwdWaves = 4;        // waves of a block, forward
+constexpr int kBwdWaves = 12;       // and backward: few blocks, whose shares of dw are joined after it
+constexpr int kFwdMost = 4096;      // waves of a launch: 4 on each SIMD
+constexpr int kBwdMost = 3072;      // 3 on each SIMD
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const bf16x2 r = __builtin_convertvector((f32x2){a, b}, bf16x2);   // to nearest even
@@ -29,22 +34,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// V consecutive elements, widened to fp32 and rounded back
+// V consecutive elements: as loaded, widened to fp32, and rounded back
 template <typename T, int V> struct Row;
 template <> struct Row<float, 4> {
-    __device__ __forceinline__ static void ld(const float *p, float *v) {
-        const float4 u = *(const float4 *)p;
-        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-    }
+    typedef float4 Raw;
+    __device__ __forceinline__ static void get(Raw u, float *v) { v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w; }
     __device__ __forceinline__ static void st(float *p, const float *v) { *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]); }
 };
 template <> struct Row<float, 1> {
-    __device__ __forceinline__ static void ld(const float *p, float *v) { v[0] = *p; }
+    typedef float Raw;
+    __device__ __forceinline__ static void get(Raw u, float *v) { v[0] = u; }
     __device__ __forceinline__ static void st(float *p, const float *v) { *p = v[0]; }
 };
 template <> struct Row<uint16_t, 8> {
-    __device__ __forceinline__ static void ld(const uint16_t *p, float *v) {
-        const uint4 u = *(const uint4 *)p;
+    typedef uint4 Raw;
+    __device__ __forceinline__ static void get(Raw u, float *v) {
         v[0] = lo_f(u.x); v[1] = hi_f(u.x); v[2] = lo_f(u.y); v[3] = hi_f(u.y);
         v[4] = lo_f(u.z); v[5] = hi_f(u.z); v[6] = lo_f(u.w); v[7] = hi_f(u.w);
     }
@@ -53,8 +57,8 @@ template <> struct Row<uint16_t, 8> {
     }
 };
 template <> struct Row<uint16_t, 4> {
-    __device__ __forceinline__ static void ld(const uint16_t *p, float *v) {
-        const uint2 u = *(const uint2 *)p;
+    typedef uint2 Raw;
+    __device__ __forceinline__ static void get(Raw u, float *v) {
         v[0] = lo_f(u.x); v[1] = hi_f(u.x); v[2] = lo_f(u.y); v[3] = hi_f(u.y);
     }
     __device__ __forceinline__ static void st(uint16_t *p, const float *v) {
@@ -62,7 +66,8 @@ template <> struct Row<uint16_t, 4> {
     }
 };
 template <> struct Row<uint16_t, 1> {
-    __device__ __forceinline__ static void ld(const uint16_t *p, float *v) { v[0] = lo_f(*p); }
+    typedef uint16_t Raw;
+    __device__ __forceinline__ static void get(Raw u, float *v) { v[0] = lo_f(u); }
     __device__ __forceinline__ static void st(uint16_t *p, const float *v) { *p = (uint16_t)pack_bf16(v[0], v[0]); }
 };
 
@@ -91,9 +96,9 @@ __device__ __forceinline__ void st_f8(uint8_t *p, const float *v, float scale) {
 // cos and sin of position * inv_freq.  The angle is formed and reduced in fp64, as turns:
 // a quarter-turn count and a rest of at most 1/8 turn, whose Taylor series (sine to the
 // 9th, cosine to the 10th power of at most pi/4: below 2e-9) run in fp32.
-__device__ __forceinline__ float2 cos_sin(int position, float inv_freq) {
-    constexpr double kTurn = 0.15915494309189533577;   // 1 / (2 pi)
-    const double t = (double)position * ((double)inv_freq * kTurn);
+constexpr double kTurn = 0.15915494309189533577;       // 1 / (2 pi)
+__device__ __forceinline__ float2 cos_sin(int position, double turns) {     // turns: inv_freq / (2 pi)
+    const double t = (double)position * turns;
     const double f = t - rint(t);
     const double q = rint(4.0 * f);                     // -2 .. 2
     const float y = (float)(f - 0.25 * q) * 6.28318530717958647692f;
@@ -136,14 +141,15 @@ __device__ __forceinline__ Unit unit_of(int u, int rot, int d) {
     return n;
 }
 
-// what a block works on: one of q, k, v
+// What a wave works on: one of q, k, v.  Its tokens stand in groups of `tokens` (1 where the
+// heads fill a wave's lane groups, then in `passes` steps of which a wave does `each`).
 struct Side {
     const void *x; const void *dy; void *y; const float *w; float *part;
     int64_t st, sh, dst, dsh;      // strides of x and dy: token, head
-    int heads, tb, blocks;         // tb: tokens a block takes at a time
-    uint32_t magic;                // ceil(2^32 / heads): i / heads = i * magic >> 32
-    int kind;                      // 0: normed and rotated, 1: copied
-    bool cache;                    // y is a cache
+    int heads, tokens, passes, each, splits;
+    int64_t parts;                 // (token group, split) pairs
+    int blocks;
+    bool rotate, cache;            // normed and rotated, or copied; y is a cache
 };
 struct Kp {
     Side side[3];
@@ -155,20 +161,120 @@ struct Kp {
     bool norm;
 };
 
-__device__ __forceinline__ int div_heads(int i, const Side &s) {
-    return s.heads == 1 ? i : (int)__umulhi((uint32_t)i, s.magic);
+// LDS of a wave is read by its own lanes: its instructions are in order, the compiler's
+// have to be told
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// cosines and sines of tb tokens from t0 on into cs[0 .. tb*half) and sn = cs + tb*half
-__device__ __forceinline__ void fill_table(const Kp &a, int64_t t0, int tb, float *cs) {
-    const int half = a.rot >> 1, n = tb * half;
-    for (int i = threadIdx.x; i < n; i += kNT) {
-        const int t = i / half, j = i - t * half;
-        if (t0 + t >= a.n_tokens) break;
-        const float2 v = cos_sin(a.positions[t0 + t], a.inv_freq[j]);
-        cs[i] = v.x;
-        cs[n + i] = v.y;
+// A lane's place in its wave's work, and the cosines and sines of the present token group
+template <typename T, int V, bool IL> struct Lane {
+    static constexpr int NU = V == 1 ? 2 : 1;    // units (2 only for V = 1, where 64 lanes may be too few)
+    typedef typename Row<T, V>::Raw Raw;
+    const Kp &a;
+    const Side &s;
+    float *tab;                                  // this wave's part of LDS: cosines, then sines
+    int lane, half, tok, head;                   // token of the group, head of the first pass
+    Unit un[NU];
+    double turns[2];                             // of angles lane and lane + 64 where the group is one token
+    float cs[NU][V], sn[NU][V];
+
+    __device__ __forceinline__ Lane(const Kp &a_, const Side &s_, float *tab_) : a(a_), s(s_), tab(tab_) {
+        lane = threadIdx.x & 63;
+        half = a.rot >> 1;
+        const int lanes = 1 << a.lg, group = lane >> a.lg, u0 = lane & (lanes - 1);
+        tok = s.tokens > 1 ? group / s.heads : 0;
+        head = group - tok * s.heads;
+#pragma unroll
+        for (int n = 0; n < NU; ++n) {
+            const int u = u0 + n * lanes;
+            un[n] = unit_of<V, IL>(u, a.rot, a.d);
+            un[n].in1 &= u < a.units;
+            un[n].in2 &= u < a.units;
+            un[n].turn &= u < a.units;
+#pragma unroll
+            for (int i = 0; i < V; ++i) cs[n][i] = sn[n][i] = 0.0f;     // of lanes without a token, too
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) turns[k] = lane + 64 * k < half ? (double)a.inv_freq[lane + 64 * k] * kTurn : 0.0;
     }
+    // token and head of a pass; on: there is such a one
+    struct At { int64_t t; int h, on; };
+    __device__ __forceinline__ At at(int64_t group, int pass) const {
+        At p;
+        p.t = group * s.tokens + tok;
+        p.h = head + pass * (64 >> a.lg);
+        p.on = tok < s.tokens && p.t < a.n_tokens && p.h < s.heads;
+        return p;
+    }
+    __device__ __forceinline__ void load(Raw (*r)[2], const void *x, int64_t st, int64_t sh, const At &p) const {
+        const T *xp = (const T *)x + p.t * st + p.h * sh;
+#pragma unroll
+        for (int n = 0; n < NU; ++n) {
+            r[n][0] = Raw{};
+            r[n][1] = Raw{};
+            if (p.on && un[n].in1) r[n][0] = *(const Raw *)(xp + un[n].o1);
+            if (p.on && un[n].in2) r[n][1] = *(const Raw *)(xp + un[n].o2);
+        }
+    }
+    __device__ __forceinline__ int position(const At &p) const {
+        return half > 0 && p.t < a.n_tokens && tok < s.tokens ? a.positions[p.t] : 0;
+    }
+    // cosines and sines of the group's tokens; pos: the position of this lane's own token
+    __device__ __forceinline__ void angles(int pos) {
+        if (half == 0) return;
+        const int n = s.tokens * half;
+        wave_sync();                             // readers of the group before
+        if (s.tokens == 1) {
+            pos = __builtin_amdgcn_readfirstlane(pos);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (lane + 64 * k < n) {
+                    const float2 v = cos_sin(pos, turns[k]);
+                    tab[lane + 64 * k] = v.x;
+                    tab[n + lane + 64 * k] = v.y;
+                }
+        } else {
+            for (int i0 = 0; i0 < n; i0 += 64) {
+                const int i = i0 + lane, t = min(i / half, s.tokens - 1), j = i - t * half;
+                const int p = __shfl(pos, (t * s.heads) << a.lg);
+                if (i < n) {
+                    const float2 v = cos_sin(p, (double)a.inv_freq[j] * kTurn);
+                    tab[i] = v.x;
+                    tab[n + i] = v.y;
+                }
+            }
+        }
+        wave_sync();
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
+            if (un[k].turn && tok < s.tokens) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    cs[k][i] = tab[tok * half + un[k].pair + i];
+                    sn[k][i] = tab[n + tok * half + un[k].pair + i];
+                }
+            }
+    }
+    __device__ __forceinline__ void weights(float (*w)[2 * V]) const {
+#pragma unroll
+        for (int n = 0; n < NU; ++n)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float w1 = s.w[(un[n].in1 ? un[n].o1 : 0) + i], w2 = s.w[(un[n].in2 ? un[n].o2 : 0) + i];
+                w[n][i] = un[n].in1 ? w1 : 0.0f;
+                w[n][V + i] = un[n].in2 ? w2 : 0.0f;
+            }
+    }
+};
+
+// the side of a block and the block's number in it
+__device__ __forceinline__ int side_of(const Kp &a, int &blk) {
+    int i = 0;
+    while (blk >= a.side[i].blocks) blk -= a.side[i++].blocks;
+    return i;
 }
 
 // turns the pairs of a lane's 2 V elements; SIGN -1 turns them back
@@ -183,50 +289,52 @@ __device__ __forceinline__ void turn(float *x, const float *cs, const float *sn)
     }
 }
 
-// NU units a lane (2 only for V = 1, where 64 lanes may be too few for a head)
 template <typename T, int V, bool IL, int KV>      // KV: 0 no cache, 1 a cache of type T, 2 an 8-bit cache
-__global__ void __launch_bounds__(kNT) qk_rope_kernel(Kp a) {
-    constexpr int NU = V == 1 ? 2 : 1;
+__global__ void __launch_bounds__(kFwdWaves * 64, 4) qk_rope_kernel(Kp a) {
+    typedef Lane<T, V, IL> L;
+    constexpr int NU = L::NU;
     extern __shared__ float tab[];
-    int blk = blockIdx.x, si = 0;
-    while (blk >= a.side[si].blocks) blk -= a.side[si++].blocks;     // uniform
-    const Side &s = a.side[si];
-    const int64_t t0 = (int64_t)blk * s.tb;
-    const int half = a.rot >> 1, lanes = 1 << a.lg, ng = kNT >> a.lg;
-    const int u0 = threadIdx.x & (lanes - 1);
-    const bool work = s.kind == 0, norm = work && a.norm;
-    if (work) fill_table(a, t0, s.tb, tab);
-    Unit un[NU];
+    int blk = blockIdx.x;
+    const Side &s = a.side[side_of(a, blk)];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    L me(a, s, tab + wave * s.tokens * a.rot);
+    const bool norm = s.rotate && a.norm;
     float w[NU][2 * V];
-#pragma unroll
-    for (int n = 0; n < NU; ++n) {
-        const int u = u0 + n * lanes;
-        un[n] = unit_of<V, IL>(u, a.rot, a.d);
-        un[n].in1 &= u < a.units;
-        un[n].in2 &= u < a.units;
-        if (norm) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                w[n][i] = un[n].in1 ? s.w[un[n].o1 + i] : 0.0f;
-                w[n][V + i] = un[n].in2 ? s.w[un[n].o2 + i] : 0.0f;
-            }
+    if (norm) me.weights(w);
+    const int64_t step = (int64_t)s.blocks * kFwdWaves;
+    int64_t part = (int64_t)blk * kFwdWaves + wave;
+    if (part >= s.parts) return;
+    int64_t group = part / s.splits;
+    const int pass0 = (int)(part - group * s.splits) * s.each, pass1 = min(pass0 + s.each, s.passes);
+    int pass = pass0;
+
+    typename L::Raw raw[NU][2], ahead[NU][2];
+    typename L::At p = me.at(group, pass);
+    me.load(raw, s.x, s.st, s.sh, p);
+    int pos = s.rotate ? me.position(p) : 0;
+    while (true) {
+        // what comes next is asked for first; steps over token groups keep their split (a wave
+        // has several groups only where there is one)
+        const bool turn_group = pass + 1 >= pass1;
+        const int64_t group_n = turn_group ? group + step : group;
+        const int pass_n = turn_group ? pass0 : pass + 1;
+        const bool more = turn_group ? s.splits == 1 && group_n < s.parts : true;
+        typename L::At p_n = p;
+        int pos_n = 0;
+        if (more) {
+            p_n = me.at(group_n, pass_n);
+            me.load(ahead, s.x, s.st, s.sh, p_n);
+            if (turn_group && s.rotate) pos_n = me.position(p_n);
         }
-    }
-    __syncthreads();
-    const int items = s.tb * s.heads;
-    for (int it = threadIdx.x >> a.lg; it < items; it += ng) {
-        const int tok = div_heads(it, s), h = it - tok * s.heads;
-        const int64_t t = t0 + tok;
-        if (t >= a.n_tokens) break;
-        const T *xp = (const T *)s.x + t * s.st + h * s.sh;
-        float x[NU][2 * V];
-        float ss = 0.0f;
+        int64_t slot = 0;
+        if (KV != 0 && s.cache && p.on) slot = a.slots[p.t];
+        if (s.rotate && pass == pass0) me.angles(pos);
+
+        float x[NU][2 * V], ss = 0.0f;
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
-#pragma unroll
-            for (int i = 0; i < 2 * V; ++i) x[n][i] = 0.0f;
-            if (un[n].in1) Row<T, V>::ld(xp + un[n].o1, x[n]);
-            if (un[n].in2) Row<T, V>::ld(xp + un[n].o2, x[n] + V);
+            Row<T, V>::get(raw[n][0], x[n]);
+            Row<T, V>::get(raw[n][1], x[n] + V);
 #pragma unroll
             for (int i = 0; i < 2 * V; ++i) ss = fmaf(x[n][i], x[n][i], ss);
         }
@@ -237,91 +345,95 @@ __global__ void __launch_bounds__(kNT) qk_rope_kernel(Kp a) {
 #pragma unroll
                 for (int i = 0; i < 2 * V; ++i) x[n][i] = x[n][i] * r * w[n][i];
         }
-        int64_t row;
-        bool keep = true;
+        int64_t row = (p.t * s.heads + p.h) * a.d;
+        bool keep = p.on != 0;
         if (KV != 0 && s.cache) {
-            const int64_t slot = a.slots[t];
-            keep = slot >= 0 && slot < (int64_t)a.n_slots;
+            keep = keep && slot >= 0 && slot < (int64_t)a.n_slots;
             const uint32_t sl = keep ? (uint32_t)slot : 0u, page = sl / a.page_size;
-            row = page * a.c_sp + (sl - page * a.page_size) * a.c_st + h * a.c_sh;
-        } else {
-            row = (t * s.heads + h) * a.d;
+            row = page * a.c_sp + (sl - page * a.page_size) * a.c_st + p.h * a.c_sh;
         }
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
-            if (work && un[n].turn && un[n].in1)
-                turn<V, IL, 1>(x[n], tab + tok * half + un[n].pair, tab + (s.tb + tok) * half + un[n].pair);
+            if (s.rotate && me.un[n].turn) turn<V, IL, 1>(x[n], me.cs[n], me.sn[n]);
             if (KV == 2 && s.cache) {
-                const float scale = work ? a.k_scale : a.v_scale;
+                const float scale = s.rotate ? a.k_scale : a.v_scale;
                 uint8_t *yp = (uint8_t *)s.y + row;
-                if (keep && un[n].in1) st_f8<V>(yp + un[n].o1, x[n], scale);
-                if (keep && un[n].in2) st_f8<V>(yp + un[n].o2, x[n] + V, scale);
+                if (keep && me.un[n].in1) st_f8<V>(yp + me.un[n].o1, x[n], scale);
+                if (keep && me.un[n].in2) st_f8<V>(yp + me.un[n].o2, x[n] + V, scale);
             } else {
                 T *yp = (T *)s.y + row;
-                if (keep && un[n].in1) Row<T, V>::st(yp + un[n].o1, x[n]);
-                if (keep && un[n].in2) Row<T, V>::st(yp + un[n].o2, x[n] + V);
+                if (keep && me.un[n].in1) Row<T, V>::st(yp + me.un[n].o1, x[n]);
+                if (keep && me.un[n].in2) Row<T, V>::st(yp + me.un[n].o2, x[n] + V);
             }
         }
+        if (!more) break;
+        p = p_n;
+        group = group_n;
+        pass = pass_n;
+        if (turn_group) pos = pos_n;
+#pragma unroll
+        for (int n = 0; n < NU; ++n) { raw[n][0] = ahead[n][0]; raw[n][1] = ahead[n][1]; }
     }
 }
 
-// The gradients.  A block walks its side's token groups blk, blk + blocks, ... and keeps
-// its share of dw in registers (a lane's elements are the same in every head); the
-// shares of its lane groups are joined in LDS at the end.
+// The gradients.  A wave keeps its share of dw in registers (a lane's elements are the same
+// in every head); the shares of its lane groups are joined across lanes at the end, those of
+// the block's waves in LDS.
 template <typename T, int V, bool IL>
-__global__ void __launch_bounds__(kNT) qk_rope_bwd_kernel(Kp a) {
-    constexpr int NU = V == 1 ? 2 : 1;
+__global__ void __launch_bounds__(kBwdWaves * 64, 3) qk_rope_bwd_kernel(Kp a) {
+    typedef Lane<T, V, IL> L;
+    constexpr int NU = L::NU;
     extern __shared__ float tab[];
-    int blk = blockIdx.x, si = 0;
-    while (blk >= a.side[si].blocks) blk -= a.side[si++].blocks;     // uniform
-    const Side &s = a.side[si];
-    const int half = a.rot >> 1, lanes = 1 << a.lg, ng = kNT >> a.lg;
-    const int u0 = threadIdx.x & (lanes - 1);
-    Unit un[NU];
+    int blk = blockIdx.x;
+    const Side &s = a.side[side_of(a, blk)];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    L me(a, s, tab + wave * s.tokens * a.rot);
     float w[NU][2 * V], dw[NU][2 * V];
 #pragma unroll
-    for (int n = 0; n < NU; ++n) {
-        const int u = u0 + n * lanes;
-        un[n] = unit_of<V, IL>(u, a.rot, a.d);
-        un[n].in1 &= u < a.units;
-        un[n].in2 &= u < a.units;
+    for (int n = 0; n < NU; ++n)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            w[n][i] = a.norm && un[n].in1 ? s.w[un[n].o1 + i] : 0.0f;
-            w[n][V + i] = a.norm && un[n].in2 ? s.w[un[n].o2 + i] : 0.0f;
-            dw[n][i] = 0.0f;
-            dw[n][V + i] = 0.0f;
-        }
-    }
-    const int items = s.tb * s.heads;
-    const int64_t step = (int64_t)s.blocks * s.tb;
-    for (int64_t t0 = (int64_t)blk * s.tb; t0 < a.n_tokens; t0 += step) {
-        __syncthreads();                               // the table's last readers
-        fill_table(a, t0, s.tb, tab);
-        __syncthreads();
-        for (int it = threadIdx.x >> a.lg; it < items; it += ng) {
-            const int tok = div_heads(it, s), h = it - tok * s.heads;
-            const int64_t t = t0 + tok;
-            if (t >= a.n_tokens) break;
-            const T *xp = (const T *)s.x + t * s.st + h * s.sh;
-            const T *gp = (const T *)s.dy + t * s.dst + h * s.dsh;
-            T *yp = (T *)s.y + (t * s.heads + h) * a.d;
-            float x[NU][2 * V], g[NU][2 * V];
-            float ss = 0.0f, sg = 0.0f;
+        for (int i = 0; i < 2 * V; ++i) { w[n][i] = 0.0f; dw[n][i] = 0.0f; }
+    if (a.norm) me.weights(w);
+    const int64_t step = (int64_t)s.blocks * kBwdWaves;
+    const int64_t part = (int64_t)blk * kBwdWaves + wave;
+    if (part < s.parts) {
+        int64_t group = part / s.splits;
+        const int pass0 = (int)(part - group * s.splits) * s.each, pass1 = min(pass0 + s.each, s.passes);
+        int pass = pass0;
+        typename L::Raw raw[NU][2], raw_g[NU][2], ahead[NU][2], ahead_g[NU][2];
+        typename L::At p = me.at(group, pass);
+        me.load(raw_g, s.dy, s.dst, s.dsh, p);
+        if (a.norm) me.load(raw, s.x, s.st, s.sh, p);
+        int pos = me.position(p);
+        while (true) {
+            const bool turn_group = pass + 1 >= pass1;
+            const int64_t group_n = turn_group ? group + step : group;
+            const int pass_n = turn_group ? pass0 : pass + 1;
+            const bool more = turn_group ? s.splits == 1 && group_n < s.parts : true;
+            typename L::At p_n = p;
+            int pos_n = 0;
+            if (more) {
+                p_n = me.at(group_n, pass_n);
+                me.load(ahead_g, s.dy, s.dst, s.dsh, p_n);
+                if (a.norm) me.load(ahead, s.x, s.st, s.sh, p_n);
+                if (turn_group) pos_n = me.position(p_n);
+            }
+            if (pass == pass0) me.angles(pos);
+
+            float x[NU][2 * V], g[NU][2 * V], ss = 0.0f, sg = 0.0f;
 #pragma unroll
             for (int n = 0; n < NU; ++n) {
+                Row<T, V>::get(raw_g[n][0], g[n]);
+                Row<T, V>::get(raw_g[n][1], g[n] + V);
+                if (me.un[n].turn) turn<V, IL, -1>(g[n], me.cs[n], me.sn[n]);
+                if (a.norm) {
+                    Row<T, V>::get(raw[n][0], x[n]);
+                    Row<T, V>::get(raw[n][1], x[n] + V);
 #pragma unroll
-                for (int i = 0; i < 2 * V; ++i) { x[n][i] = 0.0f; g[n][i] = 0.0f; }
-                if (un[n].in1) Row<T, V>::ld(gp + un[n].o1, g[n]);
-                if (un[n].in2) Row<T, V>::ld(gp + un[n].o2, g[n] + V);
-                if (a.norm && un[n].in1) Row<T, V>::ld(xp + un[n].o1, x[n]);
-                if (a.norm && un[n].in2) Row<T, V>::ld(xp + un[n].o2, x[n] + V);
-                if (un[n].turn && un[n].in1)
-                    turn<V, IL, -1>(g[n], tab + tok * half + un[n].pair, tab + (s.tb + tok) * half + un[n].pair);
-#pragma unroll
-                for (int i = 0; i < 2 * V; ++i) {
-                    ss = fmaf(x[n][i], x[n][i], ss);
-                    sg = fmaf(x[n][i], w[n][i] * g[n][i], sg);
+                    for (int i = 0; i < 2 * V; ++i) {
+                        ss = fmaf(x[n][i], x[n][i], ss);
+                        sg = fmaf(x[n][i], w[n][i] * g[n][i], sg);
+                    }
                 }
             }
             if (a.norm) {
@@ -335,45 +447,65 @@ __global__ void __launch_bounds__(kNT) qk_rope_bwd_kernel(Kp a) {
                         g[n][i] = r * fmaf(w[n][i], g[n][i], -x[n][i] * c);
                     }
             }
+            T *yp = (T *)s.y + (p.t * s.heads + p.h) * a.d;
 #pragma unroll
             for (int n = 0; n < NU; ++n) {
-                if (un[n].in1) Row<T, V>::st(yp + un[n].o1, g[n]);
-                if (un[n].in2) Row<T, V>::st(yp + un[n].o2, g[n] + V);
+                if (p.on && me.un[n].in1) Row<T, V>::st(yp + me.un[n].o1, g[n]);
+                if (p.on && me.un[n].in2) Row<T, V>::st(yp + me.un[n].o2, g[n] + V);
             }
+            if (!more) break;
+            p = p_n;
+            group = group_n;
+            pass = pass_n;
+            if (turn_group) pos = pos_n;
+#pragma unroll
+            for (int n = 0; n < NU; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) { raw[n][i] = ahead[n][i]; raw_g[n][i] = ahead_g[n][i]; }
         }
     }
     if (!a.norm) return;
-    __syncthreads();
-    const int group = threadIdx.x >> a.lg;
+    __syncthreads();                             // the angles' last readers
 #pragma unroll
     for (int n = 0; n < NU; ++n)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (un[n].in1) tab[group * a.d + un[n].o1 + i] = dw[n][i];
-            if (un[n].in2) tab[group * a.d + un[n].o2 + i] = dw[n][V + i];
-        }
+        for (int i = 0; i < 2 * V; ++i)
+            for (int o = 1 << a.lg; o < 64; o <<= 1) dw[n][i] += __shfl_xor(dw[n][i], o);
+    if (me.lane < 1 << a.lg) {
+#pragma unroll
+        for (int n = 0; n < NU; ++n)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (me.un[n].in1) tab[wave * a.d + me.un[n].o1 + i] = dw[n][i];
+                if (me.un[n].in2) tab[wave * a.d + me.un[n].o2 + i] = dw[n][V + i];
+            }
+    }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.d; e += kNT) {
+    for (int e = threadIdx.x; e < a.d; e += kBwdWaves * 64) {
         float v = 0.0f;
-        for (int k = 0; k < ng; ++k) v += tab[k * a.d + e];
+#pragma unroll
+        for (int k = 0; k < kBwdWaves; ++k) v += tab[k * a.d + e];
         s.part[(int64_t)blk * a.d + e] = v;
     }
 }
 
-// dw = sum of the blocks' shares in fp64: 16 elements a block, 16 slices of the shares
-__global__ void __launch_bounds__(kNT) qk_rope_dw_kernel(const float *pq, const float *pk, float *dwq, float *dwk,
+// dw = sum of the blocks' shares in fp64: 8 elements a block, 32 slices of the shares
+__global__ void __launch_bounds__(256) qk_rope_dw_kernel(const float *pq, const float *pk, float *dwq, float *dwk,
                                                          int nq, int nk, int d) {
-    __shared__ double sum[16][17];
-    const int e = blockIdx.x * 16 + (threadIdx.x & 15), sl = threadIdx.x >> 4;
+    __shared__ double sum[32][9];
+    const int i = threadIdx.x & 7, e = blockIdx.x * 8 + i, sl = threadIdx.x >> 3;
     const float *p = blockIdx.y ? pk : pq;
     const int n = blockIdx.y ? nk : nq;
     double v = 0.0;
-    if (e < d)
-        for (int i = sl; i < n; i += 16) v += (double)p[(int64_t)i * d + e];
-    sum[sl][threadIdx.x & 15] = v;
+    if (e < d) {
+#pragma unroll 8
+        for (int b = sl; b < n; b += 32) v += (double)p[(int64_t)b * d + e];
+    }
+    sum[sl][i] = v;
     __syncthreads();
     if (sl == 0 && e < d) {
-        for (int i = 1; i < 16; ++i) v += sum[i][threadIdx.x & 15];
+#pragma unroll
+        for (int k = 1; k < 32; ++k) v += sum[k][i];
         (blockIdx.y ? dwk : dwq)[e] = (float)v;
     }
 }
@@ -400,29 +532,43 @@ void set_geometry(Kp &k, int v, int d, int rot) {
     k.inv_d = 1.0f / (float)d;
 }
 
-// tokens of a block: two (token, head) items a lane group, fewer where that leaves the
-// chip's 256 compute units without a block, and no more angles than the table holds
-void set_tokens(Side &s, const Kp &k, int64_t n_tokens) {
-    const int ng = kNT >> k.lg, half = k.rot / 2;
-    int64_t tb = 2 * ng / s.heads;
-    if (tb > n_tokens / 256) tb = n_tokens / 256;
-    if (half > 0 && tb > kTabMax / half) tb = kTabMax / half;
-    s.tb = (int)(tb < 1 ? 1 : tb);
-    s.blocks = (int)((n_tokens + s.tb - 1) / s.tb);
-    s.magic = s.heads > 1 ? (uint32_t)(((uint64_t(1) << 32) + s.heads - 1) / s.heads) : 0;
+// blocks that a side may have: its share of the launch's, by heads
+int blocks_of(int64_t heads, int64_t all_heads, int waves) {
+    const int most = (waves == kFwdWaves ? kFwdMost : kBwdMost) / waves;
+    return (int)std::max<int64_t>(1, most * heads / all_heads);
 }
 
-size_t table_bytes(const Kp &k) {
+// Waves of a side: a token group each, or several where that is more than the chip holds
+// at once; where it is fewer, the passes over a token's heads are split between waves.
+void set_work(Side &s, const Kp &k, int64_t n_tokens, int64_t all_heads, int waves) {
+    const int groups = 64 >> k.lg;
+    s.tokens = std::max(1, groups / s.heads);
+    s.passes = (s.heads + groups - 1) / groups;
+    const int64_t token_groups = (n_tokens + s.tokens - 1) / s.tokens;
+    const int64_t most = (int64_t)blocks_of(s.heads, all_heads, waves) * waves;
+    s.splits = (int)std::min<int64_t>(s.passes, std::max<int64_t>(1, most / std::max<int64_t>(1, token_groups)));
+    s.each = (s.passes + s.splits - 1) / s.splits;
+    s.splits = (s.passes + s.each - 1) / s.each;
+    s.parts = token_groups * s.splits;
+    int64_t used = s.parts;
+    if (used > most) {                           // the same number of groups for each wave
+        const int64_t per = (used + most - 1) / most;
+        used = (used + per - 1) / per;
+    }
+    s.blocks = (int)((used + waves - 1) / waves);
+}
+
+size_t table_bytes(const Kp &k, int waves) {
     size_t most = 0;
     for (const Side &s : k.side)
-        if (s.blocks > 0) most = std::max(most, (size_t)s.tb * k.rot * sizeof(float));
+        if (s.blocks > 0 && s.rotate) most = std::max(most, (size_t)waves * s.tokens * k.rot * sizeof(float));
     return most;
 }
 
 template <typename T, int V, int KV>
 void fwd_go(const Kp &k, unsigned blocks, size_t lds, bool il, hipStream_t stream) {
-    if (il) hipLaunchKernelGGL((qk_rope_kernel<T, V, true, KV>), dim3(blocks), dim3(kNT), lds, stream, k);
-    else hipLaunchKernelGGL((qk_rope_kernel<T, V, false, KV>), dim3(blocks), dim3(kNT), lds, stream, k);
+    if (il) hipLaunchKernelGGL((qk_rope_kernel<T, V, true, KV>), dim3(blocks), dim3(kFwdWaves * 64), lds, stream, k);
+    else hipLaunchKernelGGL((qk_rope_kernel<T, V, false, KV>), dim3(blocks), dim3(kFwdWaves * 64), lds, stream, k);
 }
 template <int KV>
 void fwd_type(const Kp &k, unsigned blocks, size_t lds, bool bf16, int v, bool il, hipStream_t stream) {
@@ -434,13 +580,6 @@ void fwd_type(const Kp &k, unsigned blocks, size_t lds, bool bf16, int v, bool i
         if (v == 4) fwd_go<float, 4, KV>(k, blocks, lds, il, stream);
         else fwd_go<float, 1, KV>(k, blocks, lds, il, stream);
     }
-}
-
-// blocks of the backward's sides: at most 1024 in all, in proportion to the heads
-void bwd_blocks(int64_t n_tokens, int64_t nq, int64_t nk, int &bq, int &bk) {
-    const double share = 1024.0 / (double)(nq + nk);
-    bq = (int)std::min<int64_t>(n_tokens, std::max<int64_t>(1, (int64_t)(share * (double)nq)));
-    bk = nk > 0 ? (int)std::min<int64_t>(n_tokens, std::max<int64_t>(1, (int64_t)(share * (double)nk))) : 0;
 }
 
 }  // namespace
@@ -470,14 +609,17 @@ hipError_t launch_qk_rope(const QkRopeArgs &a, hipStream_t stream, const char **
     k.page_size = (uint32_t)a.page_size; k.n_slots = (uint32_t)(a.n_pages * a.page_size);
     k.eps = a.eps; k.k_scale = a.k_scale; k.v_scale = a.v_scale;
     k.norm = (a.flags & SSM_QK_NO_NORM) == 0;
-    k.side[0] = {a.q, nullptr, a.q_out, a.wq, nullptr, a.q_st, a.q_sh, 0, 0, (int)a.n_heads, 0, 0, 0, 0, false};
-    k.side[1] = {a.k, nullptr, a.k_out, a.wk, nullptr, a.k_st, a.k_sh, 0, 0, (int)a.n_kv_heads, 0, 0, 0, 0, cache};
-    k.side[2] = {a.v, nullptr, a.v_cache, nullptr, nullptr, a.v_st, a.v_sh, 0, 0, (int)a.n_kv_heads, 0, 0, 0, 1, cache};
-    set_tokens(k.side[0], k, a.n_tokens);
-    if (a.n_kv_heads > 0) set_tokens(k.side[1], k, a.n_tokens);
-    if (cache) set_tokens(k.side[2], k, a.n_tokens);
+    auto side = [&](int i, const void *x, void *y, const float *w, int64_t st, int64_t sh, int64_t heads, bool rotate, bool to_cache) {
+        Side &s = k.side[i];
+        s.x = x; s.y = y; s.w = w; s.st = st; s.sh = sh;
+        s.heads = (int)heads; s.rotate = rotate; s.cache = to_cache;
+        set_work(s, k, a.n_tokens, a.n_heads + (cache ? 2 : 1) * a.n_kv_heads, kFwdWaves);
+    };
+    side(0, a.q, a.q_out, a.wq, a.q_st, a.q_sh, a.n_heads, true, false);
+    if (a.n_kv_heads > 0) side(1, a.k, a.k_out, a.wk, a.k_st, a.k_sh, a.n_kv_heads, true, cache);
+    if (cache) side(2, a.v, a.v_cache, nullptr, a.v_st, a.v_sh, a.n_kv_heads, false, true);
     const unsigned blocks = (unsigned)(k.side[0].blocks + k.side[1].blocks + k.side[2].blocks);
-    const size_t lds = table_bytes(k);
+    const size_t lds = table_bytes(k, kFwdWaves);
     const bool il = (a.flags & SSM_ROPE_INTERLEAVED) != 0;
     if (f8) fwd_type<2>(k, blocks, lds, a.bf16, v, il, stream);
     else if (cache) fwd_type<1>(k, blocks, lds, a.bf16, v, il, stream);
@@ -488,9 +630,11 @@ hipError_t launch_qk_rope(const QkRopeArgs &a, hipStream_t stream, const char **
 size_t qk_rope_bwd_workspace_bytes(int64_t n_tokens, int64_t n_heads, int64_t n_kv_heads, int64_t headdim,
                                    uint32_t flags) {
     if (flags & SSM_QK_NO_NORM) return 0;
-    int bq, bk;
-    bwd_blocks(n_tokens, n_heads, n_kv_heads, bq, bk);
-    return (size_t)(bq + bk) * (size_t)headdim * sizeof(float);
+    const int64_t all = n_heads + n_kv_heads;
+    auto blocks = [&](int64_t heads) {           // each wave has a (token, head) at least
+        return std::min<int64_t>(n_tokens * heads / kBwdWaves + 1, blocks_of(heads, all, kBwdWaves));
+    };
+    return (size_t)(blocks(n_heads) + (n_kv_heads > 0 ? blocks(n_kv_heads) : 0)) * (size_t)headdim * sizeof(float);
 }
 
 hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const char **kernel_name) {
@@ -504,27 +648,25 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
     set_geometry(k, v, a.headdim, a.rot_dim);
     k.inv_freq = a.inv_freq; k.positions = a.positions;
     k.n_tokens = a.n_tokens; k.eps = a.eps; k.norm = norm;
-    k.side[0] = {a.q, a.dq_out, a.dq, a.wq, nullptr, a.q_st, a.q_sh, a.dq_st, a.dq_sh, (int)a.n_heads, 0, 0, 0, 0, false};
-    k.side[1] = {a.k, a.dk_out, a.dk, a.wk, nullptr, a.k_st, a.k_sh, a.dk_st, a.dk_sh, (int)a.n_kv_heads, 0, 0, 0, 0, false};
-    int bq, bk;
-    bwd_blocks(a.n_tokens, a.n_heads, a.n_kv_heads, bq, bk);
-    set_tokens(k.side[0], k, a.n_tokens);
-    k.side[0].blocks = std::min(k.side[0].blocks, bq);
-    if (has_k) {
-        set_tokens(k.side[1], k, a.n_tokens);
-        k.side[1].blocks = std::min(k.side[1].blocks, bk);
-    }
+    auto side = [&](int i, const void *x, const void *dy, void *y, const float *w, int64_t st, int64_t sh, int64_t dst,
+                    int64_t dsh, int64_t heads) {
+        Side &s = k.side[i];
+        s.x = x; s.dy = dy; s.y = y; s.w = w; s.st = st; s.sh = sh; s.dst = dst; s.dsh = dsh;
+        s.heads = (int)heads; s.rotate = true;
+        set_work(s, k, a.n_tokens, a.n_heads + a.n_kv_heads, kBwdWaves);
+    };
+    side(0, a.q, a.dq_out, a.dq, a.wq, a.q_st, a.q_sh, a.dq_st, a.dq_sh, a.n_heads);
+    if (has_k) side(1, a.k, a.dk_out, a.dk, a.wk, a.k_st, a.k_sh, a.dk_st, a.dk_sh, a.n_kv_heads);
     float *ws = (float *)a.workspace;
     k.side[0].part = ws;
     k.side[1].part = norm ? ws + (int64_t)k.side[0].blocks * a.headdim : nullptr;
-    // the joining of dw takes 2 V floats of every thread
-    const size_t lds = std::max(table_bytes(k), norm ? (size_t)kNT * (size_t)(v == 1 ? 4 : 2 * v) * sizeof(float) : 0);
+    const size_t lds = std::max(table_bytes(k, kBwdWaves), norm ? (size_t)kBwdWaves * a.headdim * sizeof(float) : 0);
     const unsigned blocks = (unsigned)(k.side[0].blocks + k.side[1].blocks);
     const bool il = (a.flags & SSM_ROPE_INTERLEAVED) != 0;
 #define SSM_BWD(T, V)                                                                                           \
     do {                                                                                                        \
-        if (il) hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, true>), dim3(blocks), dim3(kNT), lds, stream, k);  \
-        else hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, false>), dim3(blocks), dim3(kNT), lds, stream, k);    \
+        if (il) hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, true>), dim3(blocks), dim3(kBwdWaves * 64), lds, stream, k);  \
+        else hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, false>), dim3(blocks), dim3(kBwdWaves * 64), lds, stream, k);    \
     } while (0)
     if (blocks > 0) {
         if (a.bf16) {
@@ -540,7 +682,7 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !norm) return e;
     *kernel_name = "qk_rope_dw_kernel";
-    hipLaunchKernelGGL(qk_rope_dw_kernel, dim3((unsigned)((a.headdim + 15) / 16), has_k ? 2 : 1), dim3(kNT), 0, stream,
+    hipLaunchKernelGGL(qk_rope_dw_kernel, dim3((unsigned)((a.headdim + 7) / 8), has_k ? 2 : 1), dim3(256), 0, stream,
                        k.side[0].part, k.side[1].part, a.dwq, a.dwk, k.side[0].blocks, k.side[1].blocks, a.headdim);
     return hipGetLastError();
 }

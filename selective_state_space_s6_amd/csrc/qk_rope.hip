@@ -110,6 +110,12 @@ __device__ __forceinline__ float2 cos_sin(int position, double turns) {     // t
     return make_float2((n == 1 || n == 2) ? -cc : cc, n >= 2 ? -ss : ss);
 }
 
+// 1 / sqrt(v): the instruction, within an ulp, on a v that it does not flush to zero
+__device__ __forceinline__ float inv_sqrt(float v) {
+    const bool tiny = v < 0x1p-96f;
+    return __builtin_amdgcn_rsqf(tiny ? v * 0x1p96f : v) * (tiny ? 0x1p48f : 1.0f);
+}
+
 // sum over the 2^lg lanes of a group (lg is the same in the whole launch); every lane
 // gets it
 __device__ __forceinline__ float group_sum(float v, int lg) {
@@ -262,10 +268,22 @@ template <typename T, int V, bool IL> struct Lane {
 #pragma unroll
         for (int n = 0; n < NU; ++n)
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float w1 = s.w[(un[n].in1 ? un[n].o1 : 0) + i], w2 = s.w[(un[n].in2 ? un[n].o2 : 0) + i];
-                w[n][i] = un[n].in1 ? w1 : 0.0f;
-                w[n][V + i] = un[n].in2 ? w2 : 0.0f;
+            for (int h = 0; h < 2; ++h) {
+                const bool in = h ? un[n].in2 : un[n].in1;
+                const float *p = s.w + (in ? (h ? un[n].o2 : un[n].o1) : 0);
+                if constexpr (V == 1) {
+                    const float u = *p;
+                    w[n][h] = in ? u : 0.0f;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; i += 4) {
+                        const float4 u = *(const float4 *)(p + i);
+                        w[n][h * V + i] = in ? u.x : 0.0f;
+                        w[n][h * V + i + 1] = in ? u.y : 0.0f;
+                        w[n][h * V + i + 2] = in ? u.z : 0.0f;
+                        w[n][h * V + i + 3] = in ? u.w : 0.0f;
+                    }
+                }
             }
     }
 };
@@ -339,7 +357,7 @@ __global__ void __launch_bounds__(kFwdWaves * 64, 4) qk_rope_kernel(Kp a) {
             for (int i = 0; i < 2 * V; ++i) ss = fmaf(x[n][i], x[n][i], ss);
         }
         if (norm) {
-            const float r = 1.0f / sqrtf(fmaf(group_sum(ss, a.lg), a.inv_d, a.eps));
+            const float r = inv_sqrt(fmaf(group_sum(ss, a.lg), a.inv_d, a.eps));
 #pragma unroll
             for (int n = 0; n < NU; ++n)
 #pragma unroll
@@ -437,7 +455,7 @@ __global__ void __launch_bounds__(kBwdWaves * 64, 3) qk_rope_bwd_kernel(Kp a) {
                 }
             }
             if (a.norm) {
-                const float r = 1.0f / sqrtf(fmaf(group_sum(ss, a.lg), a.inv_d, a.eps));
+                const float r = inv_sqrt(fmaf(group_sum(ss, a.lg), a.inv_d, a.eps));
                 const float c = group_sum(sg, a.lg) * a.inv_d * r * r;
 #pragma unroll
                 for (int n = 0; n < NU; ++n)
@@ -513,7 +531,9 @@ __global__ void __launch_bounds__(256) qk_rope_dw_kernel(const float *pq, const 
 // ------------------------------------------------------------------ host ----
 // Widest V whose unit of 2 V elements fits the rotation's halves, what follows it, and
 // every address: 16 bytes where possible.  V = 1 fits everything.
-int pick_v(const void *const *ptr, const int64_t *stride, int np, int ns, int d, int rot, int esize) {
+int pick_v(const void *const *ptr, const int64_t *stride, int np, int ns, int d, int rot, int esize,
+           const float *wq, const float *wk) {
+    if ((((uintptr_t)wq | (uintptr_t)wk) & 15) != 0) return 1;     // weights are loaded by fours
     for (int v = 16 / esize; v >= 4; v >>= 1) {
         bool ok = (rot / 2) % v == 0 && (d - rot) % (2 * v) == 0;
         for (int i = 0; i < np; ++i) ok &= ((uintptr_t)ptr[i] & (uintptr_t)(v * esize - 1)) == 0;
@@ -550,12 +570,7 @@ void set_work(Side &s, const Kp &k, int64_t n_tokens, int64_t all_heads, int wav
     s.each = (s.passes + s.splits - 1) / s.splits;
     s.splits = (s.passes + s.each - 1) / s.each;
     s.parts = token_groups * s.splits;
-    int64_t used = s.parts;
-    if (used > most) {                           // the same number of groups for each wave
-        const int64_t per = (used + most - 1) / most;
-        used = (used + per - 1) / per;
-    }
-    s.blocks = (int)((used + waves - 1) / waves);
+    s.blocks = (int)((std::min(s.parts, most) + waves - 1) / waves);
 }
 
 size_t table_bytes(const Kp &k, int waves) {
@@ -590,7 +605,7 @@ hipError_t launch_qk_rope(const QkRopeArgs &a, hipStream_t stream, const char **
     const int esize = a.bf16 ? 2 : 4;
     const void *ptr[] = {a.q, a.q_out, a.k, a.k_out, a.v};
     const int64_t stride[] = {a.q_st, a.q_sh, a.k_st, a.k_sh, a.v_st, a.v_sh, (int64_t)a.headdim};
-    int v = pick_v(ptr, stride, cache ? 5 : a.n_kv_heads > 0 ? 4 : 2, 7, a.headdim, a.rot_dim, esize);
+    int v = pick_v(ptr, stride, cache ? 5 : a.n_kv_heads > 0 ? 4 : 2, 7, a.headdim, a.rot_dim, esize, a.wq, a.wk);
     if (cache) {   // the cache's own addresses: V elements of 1, 2 or 4 bytes
         const void *cp[] = {a.k_out, a.v_cache};
         const int64_t cs[] = {a.c_sp, a.c_st, a.c_sh};
@@ -643,7 +658,7 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
     const void *ptr[] = {a.q, a.dq_out, a.dq, a.k, a.dk_out, a.dk};
     const int64_t stride[] = {a.q_st, a.q_sh, a.dq_st, a.dq_sh, (int64_t)a.headdim, a.k_st, a.k_sh, a.dk_st, a.dk_sh};
     const bool has_k = a.n_kv_heads > 0, norm = (a.flags & SSM_QK_NO_NORM) == 0;
-    const int v = pick_v(ptr, stride, has_k ? 6 : 3, has_k ? 9 : 5, a.headdim, a.rot_dim, esize);
+    const int v = pick_v(ptr, stride, has_k ? 6 : 3, has_k ? 9 : 5, a.headdim, a.rot_dim, esize, a.wq, a.wk);
     Kp k = {};
     set_geometry(k, v, a.headdim, a.rot_dim);
     k.inv_freq = a.inv_freq; k.positions = a.positions;

@@ -1,4 +1,5 @@
-"""Build libssmscan.so (gfx950) from the HIP sources in csrc/.
+"""Build libssmscan.so (gfx950) from the HIP sources in csrc/, and _attn_bind.so, the
+compiled part of the Python binding (host code only, against torch's headers).
 
 Usage: python selective_state_space_s6_amd/build.py   (or __graft_entry__.build())
 Each source is compiled to an object in parallel, then linked into a shared
@@ -16,6 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libssmscan.so")
+BIND = os.path.join(HERE, "_attn_bind.so")
 SOURCES = ["abi.hip", "s6_scan.hip", "s6_seg.hip", "s6_fused.hip", "s6_decode.hip", "s6_bwd.hip", "ssd_scan.hip", "ssd_decode.hip", "ssd_bwd.hip", "cssd_scan.hip",
            "trap_rotate.hip", "conv1d.hip", "s6_grouped.hip", "scratch.hip",
            "abi_attn.hip", "kv_pages.hip", "qk_rope.hip", "paged_attn.hip"]
@@ -43,20 +45,48 @@ def _compile(src: str, obj: str) -> None:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stdout}\n{r.stderr}")
 
 
+def _compile_bind(obj: str) -> None:
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", "/opt/rocm/include",
+           "-I", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "bind_attn.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for bind_attn.cpp:\n{r.stdout}\n{r.stderr}")
+
+
+def _link_bind(obj: str) -> None:
+    import torch
+    cmd = ["g++", "-shared", "-o", BIND + ".tmp", obj, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+           "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-L", HERE, "-l:libssmscan.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _attn_bind.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(BIND + ".tmp", BIND)
+
+
 def build(verbose: bool = True) -> str:
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     objs = [os.path.join(objdir, s.replace(".hip", ".o")) for s in SOURCES]
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    bind_obj = os.path.join(objdir, "bind_attn.o")
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        bind = ex.submit(_compile_bind, bind_obj)
         list(ex.map(lambda so: _compile(*so), zip(SOURCES, objs)))
+        bind.result()
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_bind(bind_obj)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB}, {BIND}")
     return LIB
 
 

@@ -22,7 +22,19 @@ def m():
 
 @pytest.fixture(scope="module")
 def lib(m):
-    return m._lib
+    L = ctypes.CDLL(m.LIB_PATH)
+    I, P, Z, F, D, U = (ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float, ctypes.c_int, ctypes.c_uint32)
+    L.ssm_last_error.restype = ctypes.c_char_p
+    L.ssm_kv_pages_step.argtypes = [P] * 12 + [I] * 6 + [P]
+    L.ssm_qk_norm_rope_fwd.argtypes = [P] * 8 + [I] * 9 + [F, D, U, P]
+    L.ssm_qk_norm_rope_bwd.argtypes = [P] * 12 + [I] * 13 + [F, D, U, P, Z, P]
+    L.ssm_qk_norm_rope_bwd_workspace_size.argtypes = [I] * 4 + [U]
+    L.ssm_qk_norm_rope_bwd_workspace_size.restype = Z
+    L.ssm_qk_norm_rope_cache_fwd.argtypes = [P] * 11 + [I] * 16 + [F] * 3 + [D, D, U, P]
+    L.ssm_paged_attn_decode_fwd.argtypes = [P] * 7 + [I] * 13 + [F, I, F, F, D, D, P, Z, P]
+    L.ssm_paged_attn_decode_fwd_workspace_size.argtypes = [I] * 6
+    L.ssm_paged_attn_decode_fwd_workspace_size.restype = Z
+    return L
 
 
 def _p(i):

@@ -177,9 +177,20 @@ PyObject *pages_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
         auto *p_ring = (const int32_t *)c.whole(a[4], "ring", i32, {2});
         const hipStream_t stream = c.stream();
         const int64_t room = tokens > 0 ? tokens : 0;
-        const Tensor ring_out = c.make(i32, {2}), len = c.make(i32, {batch}), starts = c.make(i32, {batch + 1}),
-                     denied = c.make(i32, {1}), request = c.make(i32, {room}), positions = c.make(i32, {room}),
-                     slots = c.make(ScalarType::Long, {room});
+        // the outputs share one allocation, each from a multiple of 16 bytes on
+        auto up = [](int64_t words) { return (words + 3) / 4 * 4; };
+        const Tensor all = c.make(i32, {4 * up(room) + up(batch) + up(batch + 1) + 8});
+        int64_t word = 0;
+        auto part = [&](ScalarType dtype, int64_t words, int64_t size) {
+            Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(dtype));
+            t.unsafeGetTensorImpl()->set_storage_offset(dtype == ScalarType::Long ? word / 2 : word);
+            t.unsafeGetTensorImpl()->set_sizes_contiguous({size});
+            word += up(words);
+            return t;
+        };
+        const Tensor slots = part(ScalarType::Long, 2 * up(room), room), request = part(i32, room, room),
+                     positions = part(i32, room, room), len = part(i32, batch, batch), starts = part(i32, batch + 1, batch + 1),
+                     ring_out = part(i32, 2, 2), denied = part(i32, 1, 1);
         const int rc = ssm_kv_pages_step(
             p_old, p_new, p_table, p_free, p_ring, (int32_t *)ring_out.data_ptr(), (int32_t *)len.data_ptr(),
             (int32_t *)starts.data_ptr(), (int32_t *)request.data_ptr(), (int32_t *)positions.data_ptr(),

@@ -3,14 +3,18 @@
 // request, position and slot (ssm_kv_pages_step in include/ssm_attn.h).
 //
 // Everything follows from three running sums over the requests (pages needed,
-// pages given back, tokens), and the pages a request takes are consecutive
-// entries of the ring.  So every block forms the sums for itself (a few thousand
-// additions at most, out of cache) and then works on its own share of the
-// tokens and moved pages: one launch, no workspace, and no order between
-// blocks.  Nothing that one block reads is written by another: a token's page is
-// read from the table where its request held it before, and else from the ring
+// pages given back, new tokens), and the pages that requests take are consecutive
+// entries of the ring: request r takes up to place min(sum of the needs up to it, T),
+// where T is the largest such sum that the free pages cover.  So every block forms the
+// sums for itself (one pass over the lengths, a scan in registers and one wait) and then
+// works on its own share of the tokens and moved pages: one launch, no workspace, and no
+// order between blocks.  Nothing that one block reads is written by another: a token's
+// page is read from the table where its request held it before, and else from the ring
 // entry that it is taken from; taken entries lie in [head, head + free) of the
 // ring, given-back ones behind it.
+//
+// Bound: latency (lengths -> sums -> table or ring -> stores), and the 16 bytes stored
+// a token for long prompts.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -19,23 +23,32 @@
 namespace ssm {
 namespace {
 
-constexpr int kNT = 512;            // threads of a block
+constexpr int kNT = 256;            // threads of a block
 constexpr int kWaves = kNT / 64;
 constexpr int kTok = 4;             // consecutive tokens of a thread: one 16-byte store of each 32-bit output
+
+// x / page size, by a shift where that is a power of two
+struct Pages {
+    uint32_t size;
+    int shift;                      // -1: none
+    __device__ __forceinline__ explicit Pages(uint32_t n) : size(n), shift((n & (n - 1)) == 0 ? 31 - __clz(n) : -1) {}
+    __device__ __forceinline__ int of(uint32_t x) const { return (int)(shift >= 0 ? x >> shift : x / size); }
+    __device__ __forceinline__ int to_hold(int len) const { return of((uint32_t)len + size - 1); }
+};
 
 struct Need {
     int have, want;                 // pages held and wanted
     int grow;                       // new tokens
     bool over;                      // wanted pages do not fit the table's row
+    __device__ __forceinline__ int take() const { return over ? 0 : max(want - have, 0); }
+    __device__ __forceinline__ int give() const { return max(have - want, 0); }
 };
 
-__device__ __forceinline__ int pages_of(int len, uint32_t ps) { return (int)(((uint32_t)len + ps - 1) / ps); }
-
-__device__ __forceinline__ Need need_of(const KvPagesArgs &a, int r) {
+__device__ __forceinline__ Need need_of(const KvPagesArgs &a, const Pages &pages, int r) {
     const int lo = max(a.len_old[r], 0), hi = max(a.len_new[r], 0);
     Need n;
-    n.have = min(pages_of(lo, a.page_size), a.max_pages);     // a longer row has no entries to read
-    n.want = pages_of(hi, a.page_size);
+    n.have = min(pages.to_hold(lo), a.max_pages);     // a longer row has no entries to read
+    n.want = pages.to_hold(hi);
     n.grow = max(hi - lo, 0);
     n.over = n.want > a.max_pages;
     return n;
@@ -44,27 +57,23 @@ __device__ __forceinline__ Need need_of(const KvPagesArgs &a, int r) {
 // place i < 2 n of a ring of n entries
 __device__ __forceinline__ int wrap(uint32_t i, uint32_t n) { return (int)(i >= n ? i - n : i); }
 
-// inclusive sums over the block's threads; `total` (every thread) is the block's sum
+// inclusive sums over a wave: within rows of 16 lanes, then the rows' last lanes onward
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ int dpp_i(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, true); }
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ int64_t dpp_i(int64_t v) {
+    const uint32_t lo = (uint32_t)dpp_i<CTRL, ROWS>((int)(uint32_t)v), hi = (uint32_t)dpp_i<CTRL, ROWS>((int)(v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
 template <typename T>
-__device__ __forceinline__ T block_scan(T v, T *part, T &total) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const T u = __shfl_up(v, o);
-        if (lane >= o) v += u;
-    }
-    if (lane == 63) part[wave] = v;
-    __syncthreads();
-    T before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        const T p = part[w];
-        before += w < wave ? p : 0;
-        total += p;
-    }
-    __syncthreads();
-    return v + before;
+__device__ __forceinline__ T wave_scan(T v) {
+    v += dpp_i<0x111>(v);
+    v += dpp_i<0x112>(v);
+    v += dpp_i<0x114>(v);
+    v += dpp_i<0x118>(v);
+    v += dpp_i<0x142, 0xa>(v);
+    v += dpp_i<0x143, 0xc>(v);
+    return v;
 }
 
 // first i with end[i] > x (n if none): the request that item x belongs to
@@ -79,78 +88,118 @@ __device__ __forceinline__ int owner_of(const int *end, int n, int x) {
 
 __global__ void __launch_bounds__(kNT) kv_pages_kernel(KvPagesArgs a) {
     extern __shared__ int lds[];                       // three running sums of batch entries
-    __shared__ int64_t part[kWaves];
+    __shared__ int sum_need[kWaves], sum_give[kWaves], most[kWaves], refusals;
+    __shared__ int64_t sum_grow[kWaves];
     int *tok_end = lds, *take_end = lds + a.batch, *give_end = take_end + a.batch;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const Pages pages((uint32_t)a.page_size);
     const int total = a.n_pages;
     int head = a.ring[0] % total;
     head += head < 0 ? total : 0;
     const int free = min(max(a.ring[1], 0), total);
     const bool first = blockIdx.x == 0;
 
-    int64_t needed = 0, grown = 0;                     // sums over the requests before this chunk
-    int taken = 0, given = 0, denied = 0;
-    for (int r0 = 0; r0 < a.batch; r0 += kNT) {
-        const int r = r0 + (int)threadIdx.x;
-        Need n = {0, 0, 0, false};
-        if (r < a.batch) n = need_of(a, r);
-        const int need = n.over ? 0 : max(n.want - n.have, 0);
-        int64_t s_need, s_grow, s_take, s_give, s_deny;
-        const int64_t upto = needed + block_scan<int64_t>(need, part, s_need);
-        const bool refused = n.over || (need > 0 && upto > free);
-        const int take = refused ? 0 : need;
-        const int64_t ends = grown + block_scan<int64_t>(n.grow, part, s_grow);
-        // sums below 2^31: taken <= free, given <= batch * max_pages
-        const int t_end = taken + (int)block_scan<int64_t>(take, part, s_take);
-        const int g_end = given + (int)block_scan<int64_t>(max(n.have - n.want, 0), part, s_give);
-        block_scan<int64_t>(refused ? 1 : 0, part, s_deny);
-        if (r < a.batch) {
-            const int e = (int)min(ends, (int64_t)0x7fffffff);
-            tok_end[r] = e;
-            take_end[r] = t_end;
-            give_end[r] = g_end;
-            if (first) {
-                a.len_out[r] = max(refused ? a.len_old[r] : a.len_new[r], 0);
-                a.starts[r + 1] = e;
-            }
-        }
-        needed += s_need; grown += s_grow;
-        taken += (int)s_take; given += (int)s_give; denied += (int)s_deny;
+    // a thread's requests [r0, r1), their sums, and the sums before them
+    const int mine = (a.batch + kNT - 1) / kNT, r0 = tid * mine, r1 = min(r0 + mine, a.batch);
+    int need = 0, give = 0;                            // below 2^31: at most batch * max_pages
+    int64_t grow = 0;
+    for (int r = r0; r < r1; ++r) {
+        const Need n = need_of(a, pages, r);
+        need += n.take();
+        give += n.give();
+        grow += n.grow;
     }
+    int need_upto = wave_scan(need), give_upto = wave_scan(give);
+    int64_t grow_upto = wave_scan(grow);
+    if (lane == 63) { sum_need[wave] = need_upto; sum_give[wave] = give_upto; sum_grow[wave] = grow_upto; }
+    if (tid == 0) refusals = 0;
+    __syncthreads();
+    need_upto -= need; give_upto -= give; grow_upto -= grow;
+    int needed = 0, given = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) { need_upto += sum_need[w]; give_upto += sum_give[w]; grow_upto += sum_grow[w]; }
+        needed += sum_need[w];
+        given += sum_give[w];
+    }
+    int taken = needed;
+    if (needed > free) {                               // the same in the whole block: some are refused
+        int top = 0, upto = need_upto;
+        for (int r = r0; r < r1; ++r) {
+            upto += need_of(a, pages, r).take();
+            top = upto <= free ? upto : top;
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) top = max(top, __shfl_xor(top, o));
+        if (lane == 0) most[wave] = top;
+        __syncthreads();
+        taken = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) taken = max(taken, most[w]);
+    }
+    int denied = 0;
+    for (int r = r0; r < r1; ++r) {
+        const Need n = need_of(a, pages, r);
+        need_upto += n.take();
+        give_upto += n.give();
+        grow_upto += n.grow;
+        const int e = (int)min(grow_upto, (int64_t)0x7fffffff);
+        tok_end[r] = e;
+        take_end[r] = min(need_upto, taken);
+        give_end[r] = give_upto;
+        if (first) {
+            const bool refused = n.over || (n.take() > 0 && need_upto > free);
+            denied += refused;
+            a.len_out[r] = max(refused ? a.len_old[r] : a.len_new[r], 0);
+            a.starts[r + 1] = e;
+        }
+    }
+    if (first && denied > 0) atomicAdd(&refusals, denied);
+    __syncthreads();
     given = min(given, total - free);                  // no more than the ring has places for
-    if (first && threadIdx.x == 0) {
+    if (first && tid == 0) {
         a.starts[0] = 0;
         a.ring_out[0] = wrap((uint32_t)head + taken, total);
         a.ring_out[1] = free - taken + given;
-        a.denied[0] = denied;
+        a.denied[0] = refusals;
     }
-    __syncthreads();
-    const int tokens = a.batch > 0 ? tok_end[a.batch - 1] : 0;
-    const uint32_t ps = (uint32_t)a.page_size;
-    const int step = (int)gridDim.x * kNT, me = (int)blockIdx.x * kNT + (int)threadIdx.x;
+    const int tokens = tok_end[a.batch - 1];
+    const int step = (int)gridDim.x * kNT, me = (int)blockIdx.x * kNT + tid;
 
     // the new tokens
     for (int64_t t0 = (int64_t)me * kTok; t0 < a.n_tokens; t0 += (int64_t)step * kTok) {
         int rq[kTok], po[kTok];
         int64_t sl[kTok];
-        int r = t0 < tokens ? owner_of(tok_end, a.batch, (int)t0) : a.batch;
+        int r = t0 < tokens ? owner_of(tok_end, a.batch, (int)t0) : a.batch, end = 0;
+        int old = 0, start = 0, have = 0, from = 0;    // of request r: its length and first token; its
+        bool granted = false;                          // pages and first taken one; not refused
+        const int32_t *table = nullptr;
 #pragma unroll
         for (int i = 0; i < kTok; ++i) {
             const int t = (int)t0 + i;
-            while (r < a.batch && tok_end[r] <= t) ++r;
             rq[i] = -1; po[i] = -1; sl[i] = -1;
-            if (r < a.batch) {
-                const Need n = need_of(a, r);
-                const int before = r > 0 ? take_end[r - 1] : 0;
-                rq[i] = r;
-                po[i] = max(a.len_old[r], 0) + (t - (r > 0 ? tok_end[r - 1] : 0));
-                const int c = (int)((uint32_t)po[i] / ps);
-                // a request that wants more pages than it holds and takes none was refused
-                if (c < n.have || take_end[r] > before) {
-                    const int page = c < n.have ? a.block_table[r * a.table_stride + c]
-                                                : a.free_ring[wrap((uint32_t)head + (before + c - n.have), total)];
-                    sl[i] = (int64_t)page * ps + ((uint32_t)po[i] - (uint32_t)c * ps);
+            if (r < a.batch && t >= end) {             // the next request with new tokens
+                while (r < a.batch && tok_end[r] <= t) ++r;
+                if (r < a.batch) {
+                    const Need n = need_of(a, pages, r);
+                    end = tok_end[r];
+                    start = r > 0 ? tok_end[r - 1] : 0;
+                    from = r > 0 ? take_end[r - 1] : 0;
+                    old = max(a.len_old[r], 0);
+                    have = n.have;
+                    // one that wants more pages than it holds and takes none was refused
+                    granted = n.want <= n.have || take_end[r] > from;
+                    table = a.block_table + r * a.table_stride;
                 }
-                if (n.want > n.have && take_end[r] == before) sl[i] = -1;
+            }
+            if (r < a.batch) {
+                rq[i] = r;
+                po[i] = old + (t - start);
+                if (granted) {
+                    const int c = pages.of((uint32_t)po[i]);
+                    const int page = c < have ? table[c] : a.free_ring[wrap((uint32_t)head + (from + c - have), total)];
+                    sl[i] = (int64_t)page * pages.size + ((uint32_t)po[i] - (uint32_t)c * pages.size);
+                }
             }
         }
         if (t0 + kTok <= a.n_tokens) {
@@ -166,17 +215,18 @@ __global__ void __launch_bounds__(kNT) kv_pages_kernel(KvPagesArgs a) {
             }
         }
     }
-    // pages taken, into the table
-    for (int j = me; j < taken; j += step) {
+    // pages taken, into the table (by the last threads first: where there is little to do,
+    // these moves and the tokens are at work at the same time)
+    for (int j = step - 1 - me; j < taken; j += step) {
         const int r = owner_of(take_end, a.batch, j);
-        const Need n = need_of(a, r);
+        const Need n = need_of(a, pages, r);
         const int c = n.have + j - (r > 0 ? take_end[r - 1] : 0);
         a.block_table[r * a.table_stride + c] = a.free_ring[wrap((uint32_t)head + j, total)];
     }
     // pages given back, behind the ring's last entry
-    for (int j = me; j < given; j += step) {
+    for (int j = me < step / 2 ? me + step / 2 : me - step / 2; j < given; j += step) {
         const int r = owner_of(give_end, a.batch, j);
-        const int c = need_of(a, r).want + j - (r > 0 ? give_end[r - 1] : 0);
+        const int c = need_of(a, pages, r).want + j - (r > 0 ? give_end[r - 1] : 0);
         a.free_ring[wrap((uint32_t)head + (free + j), total)] = a.block_table[r * a.table_stride + c];
     }
 }

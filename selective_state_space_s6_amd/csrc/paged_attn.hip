@@ -188,35 +188,55 @@ __global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_att
     // ---- this block's piece [u, u_end) of the line of units, and the row that u is in
     const int per = (a.n_kv >> a.wh_lg) * a.passes;      // (kv heads side by side, pass) of a row
     const int blk = worker_of(blockIdx.x, a.wh_lg), side = side_of(blockIdx.x, a.wh_lg);
-    const int mine = (a.batch + W * 64 - 1) / (W * 64), r0 = tid * mine, r1 = min(r0 + mine, a.batch);   // a thread's rows
-    int own_units = 0;
-    for (int r = r0; r < r1; ++r) own_units += span_of(a, a.lens[r]).units * per;
-    int before = wave_scan(own_units), units = 0;
-    if (lane == 63) scan[wave] = before;
-    __syncthreads();
-    before -= own_units;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        before += w < wave ? scan[w] : 0;
-        units += scan[w];
-    }
-    const int blocks = min((int)gridDim.x >> a.wh_lg, units);
-    if (blk > 0 && blk >= blocks) return;
-    int u = blocks ? (int)((int64_t)blk * units / blocks) : 0;
-    const int u_end = blocks ? (int)((int64_t)(blk + 1) * units / blocks) : 0;
-    if (blockIdx.x == 0 || (u >= before && u < before + own_units)) {
-        for (int r = r0; r < r1; ++r) {
-            const int len = a.lens[r], n = span_of(a, len).units * per;
-            if (u >= before && u < before + n) { found[0] = r; found[1] = before; found[2] = len; }
-            if (blockIdx.x == 0) a.start[r] = before;
-            before += n;
+    int units = 0, u, u_end, row, row_u, row_len;
+    if (a.batch <= 64) {                    // each wave for itself: row `lane`
+        const int len = lane < a.batch ? a.lens[lane] : 0, own_units = span_of(a, len).units * per;
+        const int upto = wave_scan(own_units), before = upto - own_units;
+        units = __builtin_amdgcn_readlane(upto, 63);
+        if (blockIdx.x == 0 && wave == 0) {
+            if (lane < a.batch) a.start[lane] = before;
+            if (lane == 0) a.start[a.batch] = units;
         }
+        const int blocks = min((int)gridDim.x >> a.wh_lg, units);
+        if (blk >= blocks) return;
+        u = (int)((int64_t)blk * units / blocks);
+        u_end = (int)((int64_t)(blk + 1) * units / blocks);
+        row = __builtin_ctzll(__ballot(u >= before && u < upto));
+        row_u = __builtin_amdgcn_readlane(before, row);
+        row_len = __builtin_amdgcn_readlane(len, row);
+    } else {                                // a thread's rows: [r0, r1)
+        const int mine = (a.batch + W * 64 - 1) / (W * 64), r0 = tid * mine, r1 = min(r0 + mine, a.batch);
+        int own_units = 0;
+        for (int r = r0; r < r1; ++r) own_units += span_of(a, a.lens[r]).units * per;
+        int before = wave_scan(own_units);
+        if (lane == 63) scan[wave] = before;
+        __syncthreads();
+        before -= own_units;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            before += w < wave ? scan[w] : 0;
+            units += scan[w];
+        }
+        const int blocks = min((int)gridDim.x >> a.wh_lg, units);
+        if (blockIdx.x > 0 && blk >= blocks) return;
+        u = blocks ? (int)((int64_t)blk * units / blocks) : 0;
+        u_end = blocks ? (int)((int64_t)(blk + 1) * units / blocks) : 0;
+        if (blockIdx.x == 0 || (u >= before && u < before + own_units)) {
+            for (int r = r0; r < r1; ++r) {
+                const int len = a.lens[r], n = span_of(a, len).units * per;
+                if (u >= before && u < before + n) { found[0] = r; found[1] = before; found[2] = len; }
+                if (blockIdx.x == 0) a.start[r] = before;
+                before += n;
+            }
+        }
+        if (blockIdx.x == 0 && tid == 0) a.start[a.batch] = units;
+        __syncthreads();
+        if (u >= u_end) return;
+        row = found[0];
+        row_u = found[1];
+        row_len = found[2];
     }
-    if (blockIdx.x == 0 && tid == 0) a.start[a.batch] = units;
-    __syncthreads();
-    if (u >= u_end) return;
-    int row = found[0], row_u = found[1];
-    Span sp = span_of(a, found[2]);
+    Span sp = span_of(a, row_len);
 
     while (u < u_end) {
         while (u >= row_u + sp.units * per) {

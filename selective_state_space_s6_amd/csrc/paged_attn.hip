@@ -481,72 +481,101 @@ __global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_att
     }
 }
 
-// Joins the pieces of one (row, query head): piece i's share is scaled by
-// 2^(m_i - max m).  Rows without tokens get o = 0, lse = -inf here.  A block joins d / gridDim.z
-// dims; every wave forms the maximum and the sum for itself, so the only wait is for
-// the slices of the pieces that the block's threads add up.
-template <bool BF16>
+// Joins the pieces of a (row, query head): piece i's share is scaled by
+// 2^(m_i - max m).  Rows without tokens get o = 0, lse = -inf here.  A block has HB heads of
+// a row.  Where a head has few pieces, a wave joins it alone; else the whole block does,
+// d / gridDim.z dims of it, head after head.
+template <bool BF16, int HB>
 __global__ void __launch_bounds__(kNT) paged_attn_join_kernel(Kp a, int grid) {
     __shared__ f32x4 out[kNT];
-    const int row = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int per = (a.n_kv >> a.wh_lg) * a.passes;
-    const int kv = h / a.group, side = kv & ((1 << a.wh_lg) - 1), pass = (h - kv * a.group) / a.gmax, hh = h - kv * a.group - pass * a.gmax;
     const int64_t total = a.start[a.batch];
     const int row_u = a.start[row], nu = (a.start[row + 1] - row_u) / per;
-    const int64_t to = ((int64_t)row * a.n_heads + h) * a.d;
-    const int cols = a.d / 4 / gridDim.z, slices = kNT / cols, sl = tid / cols, e = ((int)blockIdx.z * cols + tid - sl * cols) * 4;
-    auto store = [&](f32x4 v) {
-        if constexpr (BF16) *(uint2 *)(a.o + (to + e) * 2) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-        else *(f32x4 *)(a.o + (to + e) * 4) = v;
+    const int64_t blocks = min((int64_t)(grid >> a.wh_lg), total);
+    const int d4 = a.d / 4;
+    auto store = [&](int h, int e, f32x4 v) {
+        const int64_t to = ((int64_t)row * a.n_heads + h) * a.d + e;
+        if constexpr (BF16) *(uint2 *)(a.o + to * 2) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        else *(f32x4 *)(a.o + to * 4) = v;
     };
-    const bool first = tid == 0 && blockIdx.z == 0 && a.lse;
-    if (nu == 0) {
-        if (sl == 0) store((f32x4){0.0f, 0.0f, 0.0f, 0.0f});
-        if (first) a.lse[(int64_t)row * a.n_heads + h] = -INFINITY;
+    // The threads of a head: slice sl of its pieces, dims e..e+3; the caller adds up the slices.
+    // Every wave forms the maximum and the sum for itself: lane i has pieces i, i + 64, ...
+    // n: pieces (1: the head was written whole); scale, lse: of the sum
+    struct Joined { f32x4 v; int n; float scale, lse; };
+    auto join = [&](int h, int sl, int slices, int e) {
+        Joined r = {{0.0f, 0.0f, 0.0f, 0.0f}, 1, 0.0f, -INFINITY};
+        const int kv = h / a.group, side = kv & ((1 << a.wh_lg) - 1), pass = (h - kv * a.group) / a.gmax;
+        const int hh = h - kv * a.group - pass * a.gmax;
+        // the blocks whose pieces hold this head's first and last unit
+        const int64_t u0 = row_u + (int64_t)((kv >> a.wh_lg) * a.passes + pass) * nu;
+        const int b0 = (int)(((u0 + 1) * blocks - 1) / total), n = (int)(((u0 + nu) * blocks - 1) / total) - b0 + 1;
+        if (n == 1) return r;
+        r.n = n;
+        // the first block began this head (its second place); the others go on with it (their first)
+        auto place = [&](int i) { return ((int64_t)block_of(b0 + i, side, a.wh_lg) * 2 + (i == 0 ? 1 : 0)) * a.gmax + hh; };
+        f32x4 part0 = r.v, part1 = r.v;
+        // the first two shares of a slice need not wait for the maximum
+        const bool in0 = sl < slices && sl < n, in1 = sl < slices && sl + slices < n;
+        if (in0) part0 = *(const f32x4 *)(a.part + place(sl) * a.d + e);
+        if (in1) part1 = *(const f32x4 *)(a.part + place(sl + slices) * a.d + e);
+        float2 own = make_float2(-INFINITY, 0.0f);
+        if (lane < n) own = *(const float2 *)(a.ml + place(lane) * 2);
+        float m = own.x;
+        for (int i = lane + 64; i < n; i += 64) m = fmaxf(m, a.ml[place(i) * 2]);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+        m = m == -INFINITY ? 0.0f : m;
+        const float scale = exp2_fast(own.x - m);
+        float l = own.y * scale;
+        for (int i = lane + 64; i < n; i += 64) {
+            const float2 w = *(const float2 *)(a.ml + place(i) * 2);
+            l += w.y * exp2_fast(w.x - m);
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o);
+        const float s0 = __shfl(scale, sl & 63), s1 = __shfl(scale, (sl + slices) & 63);
+        if (in0) r.v = part0 * (sl < 64 ? s0 : exp2_fast(a.ml[place(sl) * 2] - m));
+        if (in1) r.v += part1 * (sl + slices < 64 ? s1 : exp2_fast(a.ml[place(sl + slices) * 2] - m));
+        if (sl < slices) {
+#pragma unroll 4
+            for (int i = sl + 2 * slices; i < n; i += slices)
+                r.v += *(const f32x4 *)(a.part + place(i) * a.d + e) * exp2_fast(a.ml[place(i) * 2] - m);
+        }
+        r.scale = l > 0.0f || l != l ? a.v_scale / l : 0.0f;
+        r.lse = m * kLn2 + logf(l);
+        return r;
+    };
+    const int h0 = (int)blockIdx.y * HB, h1 = min(h0 + HB, a.n_heads);
+    // (a head's pieces lie within nu units, a block's share is total / blocks of them)
+    if (HB > 1 && (nu == 0 || nu * blocks / total + 2 <= 16)) {
+        const int h = h0 + wave, slices = 64 / d4, sl = lane / d4, e = (lane - sl * d4) * 4;
+        if (h >= h1) return;
+        Joined r = {{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0.0f, -INFINITY};
+        if (nu > 0) r = join(h, sl, slices, e);
+        if (r.n == 1) return;
+        f32x4 v = r.v;
+        for (int s = 1; s < min(slices, r.n); ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += __shfl(r.v[i], lane + s * d4);
+        if (sl == 0) store(h, e, v * r.scale);
+        if (lane == 0 && a.lse) a.lse[(int64_t)row * a.n_heads + h] = r.lse;
         return;
     }
-    // the blocks whose pieces hold this head's first and last unit
-    const int64_t blocks = min((int64_t)(grid >> a.wh_lg), total), u0 = row_u + (int64_t)((kv >> a.wh_lg) * a.passes + pass) * nu;
-    const int b0 = (int)(((u0 + 1) * blocks - 1) / total), b1 = (int)(((u0 + nu) * blocks - 1) / total);
-    if (b0 == b1) return;                    // written whole
-    const int n = b1 - b0 + 1;
-    // the first block began this head (its second place); the others go on with it (their first)
-    auto place = [&](int i) { return ((int64_t)block_of(b0 + i, side, a.wh_lg) * 2 + (i == 0 ? 1 : 0)) * a.gmax + hh; };
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f}, part0 = v, part1 = v;
-    // the first two shares of a slice need not wait for the maximum
-    const bool in0 = sl < slices && sl < n, in1 = sl < slices && sl + slices < n;
-    if (in0) part0 = *(const f32x4 *)(a.part + place(sl) * a.d + e);
-    if (in1) part1 = *(const f32x4 *)(a.part + place(sl + slices) * a.d + e);
-    // lane i of each wave: pieces i, i + 64, ...
-    float2 mine = make_float2(-INFINITY, 0.0f);
-    if (lane < n) mine = *(const float2 *)(a.ml + place(lane) * 2);
-    float m = mine.x, l = 0.0f;
-    for (int i = lane + 64; i < n; i += 64) m = fmaxf(m, a.ml[place(i) * 2]);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    m = m == -INFINITY ? 0.0f : m;
-    const float scale = exp2_fast(mine.x - m);
-    l = mine.y * scale;
-    for (int i = lane + 64; i < n; i += 64) {
-        const float2 w = *(const float2 *)(a.ml + place(i) * 2);
-        l += w.y * exp2_fast(w.x - m);
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o);
-    const float s0 = __shfl(scale, sl & 63), s1 = __shfl(scale, (sl + slices) & 63);
-    if (in0) v = part0 * (sl < 64 ? s0 : exp2_fast(a.ml[place(sl) * 2] - m));
-    if (in1) v += part1 * (sl + slices < 64 ? s1 : exp2_fast(a.ml[place(sl + slices) * 2] - m));
-    if (sl < slices) {
-#pragma unroll 4
-        for (int i = sl + 2 * slices; i < n; i += slices)
-            v += *(const f32x4 *)(a.part + place(i) * a.d + e) * exp2_fast(a.ml[place(i) * 2] - m);
-    }
-    out[tid] = v;
-    __syncthreads();
-    if (sl == 0) {
-        for (int s = 1; s < min(slices, n); ++s) v += out[s * cols + tid];
-        store(v * (l > 0.0f || l != l ? a.v_scale / l : 0.0f));
-        if (first) a.lse[(int64_t)row * a.n_heads + h] = m * kLn2 + logf(l);
+    const int cols = d4 / gridDim.z, slices = kNT / cols, sl = tid / cols, e = ((int)blockIdx.z * cols + tid - sl * cols) * 4;
+    for (int h = h0; h < h1; ++h) {
+        Joined r = {{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0.0f, -INFINITY};
+        if (nu > 0) r = join(h, sl, slices, e);
+        if (r.n == 1) continue;                  // the same in the whole block
+        out[tid] = r.v;
+        __syncthreads();
+        if (sl == 0) {
+            f32x4 v = r.v;
+            for (int s = 1; s < min(slices, r.n); ++s) v += out[s * cols + tid];
+            store(h, e, v * r.scale);
+        }
+        if (tid == 0 && blockIdx.z == 0 && a.lse) a.lse[(int64_t)row * a.n_heads + h] = r.lse;
+        __syncthreads();
     }
 }
 
@@ -648,12 +677,15 @@ hipError_t launch_paged_attn(const PagedAttnArgs &a, hipStream_t stream, const c
                                                     : go_type<KF8>(k, grid, stream);
     if (rc != hipSuccess) return rc;
     *kernel_name = "paged_attn_join_kernel";
-    // where a head has many pieces, more blocks join it, of 32 dims each
-    const int split = (grid >> k.wh_lg) >= 64 * a.batch * (a.n_kv_heads >> k.wh_lg) * k.passes && a.headdim % 32 == 0
-                          ? a.headdim / 32 : 1;
-    const dim3 g((unsigned)a.batch, (unsigned)a.n_heads, (unsigned)split);
-    if (a.kv_dtype == SSM_KV_F32) hipLaunchKernelGGL((paged_attn_join_kernel<false>), g, dim3(kNT), 0, stream, k, grid);
-    else hipLaunchKernelGGL((paged_attn_join_kernel<true>), g, dim3(kNT), 0, stream, k, grid);
+    // where a head has many pieces, a block joins it, or several of 32 dims each; else its waves a head each
+    const int64_t pieces = (grid >> k.wh_lg) / (a.batch * (a.n_kv_heads >> k.wh_lg) * k.passes);
+    const int split = pieces >= 64 && a.headdim % 32 == 0 ? a.headdim / 32 : 1, hb = pieces >= 8 ? 1 : 4;
+    const dim3 g((unsigned)a.batch, (unsigned)((a.n_heads + hb - 1) / hb), (unsigned)split);
+    const bool bf16 = a.kv_dtype != SSM_KV_F32;
+    if (hb == 1 && bf16) hipLaunchKernelGGL((paged_attn_join_kernel<true, 1>), g, dim3(kNT), 0, stream, k, grid);
+    else if (hb == 1) hipLaunchKernelGGL((paged_attn_join_kernel<false, 1>), g, dim3(kNT), 0, stream, k, grid);
+    else if (bf16) hipLaunchKernelGGL((paged_attn_join_kernel<true, 4>), g, dim3(kNT), 0, stream, k, grid);
+    else hipLaunchKernelGGL((paged_attn_join_kernel<false, 4>), g, dim3(kNT), 0, stream, k, grid);
     return hipGetLastError();
 }
 

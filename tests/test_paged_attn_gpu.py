@@ -248,16 +248,17 @@ def test_a_cache_past_4_gib(cuda_device):
     _compare("attn 5 GiB", got, q, kc[last], vc[last], np.array([[0, 1, 2, 3, 4]]), [77], 0.09, 1.0)
 
 
-def test_in_a_graph_with_lens_and_table_changing(cuda_device):
+@pytest.mark.parametrize("H,Hk,d", [(8, 2, 128), (16, 1, 256)])     # the second: 65 KiB of LDS a block
+def test_in_a_graph_with_lens_and_table_changing(cuda_device, H, Hk, d):
     """Captured once; lens, table and q change in place between replays.  The grid depends on
     the table's size alone, so every replay has to equal the eager call."""
     import torch
     m = lib()
-    q, kc, vc, table, lens, s = _make(cuda_device, 11, [600, 20, 333, 1], 8, 2, 128, "bf16", 16, "nhd", nan=False)
+    q, kc, vc, table, lens, s = _make(cuda_device, 11, [600, 20, 333, 1], H, Hk, d, "bf16", 16, "nhd", nan=False)
     t = torch.tensor(table, dtype=torch.int32, device=cuda_device)
     n = torch.tensor(lens, dtype=torch.int32, device=cuda_device)
-    o, lse = torch.empty_like(q), torch.empty((4, 8), device=cuda_device)
-    ws = torch.empty(m.ssm_paged_attn_decode_fwd_workspace_size(4, 8, 2, 128, t.shape[1], 16), dtype=torch.uint8, device=cuda_device)
+    o, lse = torch.empty_like(q), torch.empty((4, H), device=cuda_device)
+    ws = torch.empty(m.ssm_paged_attn_decode_fwd_workspace_size(4, H, Hk, d, t.shape[1], 16), dtype=torch.uint8, device=cuda_device)
     call = lambda: m.ssm_paged_attn_decode_fwd(q, kc, vc, t, n, scale=0.09, o=o, lse=lse, workspace=ws)  # noqa: E731
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())

@@ -15,8 +15,10 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <array>
 #include <initializer_list>
 #include <string>
+#include <tuple>
 
 #include "../../include/ssm_attn.h"
 
@@ -94,6 +96,27 @@ struct Call {
     Tensor make(ScalarType dtype, std::initializer_list<int64_t> shape) const {
         if (!gpu()) refuse(PyExc_ValueError, "tensors are on " + dev.str() + ", expected a GPU");
         return at::empty(IntArrayRef(shape.begin(), shape.size()), options.dtype(dtype));
+    }
+    // new outputs in one allocation, each from a multiple of 16 bytes on: an allocation costs
+    // more than the rest of a small call's checks
+    struct Wanted { ScalarType dtype; std::initializer_list<int64_t> shape; };
+    template <size_t N> std::array<Tensor, N> make_together(const Wanted (&want)[N]) const {
+        int64_t at[N], bytes = 0;
+        for (size_t i = 0; i < N; ++i) {
+            at[i] = bytes;
+            int64_t n = (int64_t)c10::elementSize(want[i].dtype);
+            for (int64_t d : want[i].shape) n *= d;
+            bytes += (n + 15) / 16 * 16;
+        }
+        const Tensor all = make(ScalarType::Byte, {bytes});
+        std::array<Tensor, N> r;
+        for (size_t i = 0; i < N; ++i) {
+            r[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                            c10::scalarTypeToTypeMeta(want[i].dtype));
+            r[i].unsafeGetTensorImpl()->set_storage_offset(at[i] / (int64_t)c10::elementSize(want[i].dtype));
+            r[i].unsafeGetTensorImpl()->set_sizes_contiguous(IntArrayRef(want[i].shape.begin(), want[i].shape.size()));
+        }
+        return r;
     }
     Tensor workspace(PyObject *o, size_t need) const {
         if (o == Py_None) return make(ScalarType::Byte, {(int64_t)need});
@@ -177,20 +200,8 @@ PyObject *pages_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
         auto *p_ring = (const int32_t *)c.whole(a[4], "ring", i32, {2});
         const hipStream_t stream = c.stream();
         const int64_t room = tokens > 0 ? tokens : 0;
-        // the outputs share one allocation, each from a multiple of 16 bytes on
-        auto up = [](int64_t words) { return (words + 3) / 4 * 4; };
-        const Tensor all = c.make(i32, {4 * up(room) + up(batch) + up(batch + 1) + 8});
-        int64_t word = 0;
-        auto part = [&](ScalarType dtype, int64_t words, int64_t size) {
-            Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(dtype));
-            t.unsafeGetTensorImpl()->set_storage_offset(dtype == ScalarType::Long ? word / 2 : word);
-            t.unsafeGetTensorImpl()->set_sizes_contiguous({size});
-            word += up(words);
-            return t;
-        };
-        const Tensor slots = part(ScalarType::Long, 2 * up(room), room), request = part(i32, room, room),
-                     positions = part(i32, room, room), len = part(i32, batch, batch), starts = part(i32, batch + 1, batch + 1),
-                     ring_out = part(i32, 2, 2), denied = part(i32, 1, 1);
+        const auto [slots, request, positions, len, starts, ring_out, denied] = c.make_together<7>(
+            {{ScalarType::Long, {room}}, {i32, {room}}, {i32, {room}}, {i32, {batch}}, {i32, {batch + 1}}, {i32, {2}}, {i32, {1}}});
         const int rc = ssm_kv_pages_step(
             p_old, p_new, p_table, p_free, p_ring, (int32_t *)ring_out.data_ptr(), (int32_t *)len.data_ptr(),
             (int32_t *)starts.data_ptr(), (int32_t *)request.data_ptr(), (int32_t *)positions.data_ptr(),
@@ -286,8 +297,14 @@ PyObject *rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
         const Tensor dq = r.c.out(a[10], "dq", r.type, {r.T, r.H, r.d});
         const Tensor dk = has_k ? r.c.out(a[11], "dk", r.type, {r.T, r.Hk, r.d}) : Tensor();
-        const Tensor dwq = r.norm ? r.c.out(a[12], "dwq", ScalarType::Float, {r.d}) : Tensor();
-        const Tensor dwk = r.norm && has_k ? r.c.out(a[13], "dwk", ScalarType::Float, {r.d}) : Tensor();
+        Tensor dwq, dwk;
+        if (r.norm && has_k && a[12] == Py_None && a[13] == Py_None) {
+            const auto f32 = ScalarType::Float;
+            std::tie(dwq, dwk) = std::tuple_cat(r.c.make_together<2>({{f32, {r.d}}, {f32, {r.d}}}));
+        } else if (r.norm) {
+            dwq = r.c.out(a[12], "dwq", ScalarType::Float, {r.d});
+            if (has_k) dwk = r.c.out(a[13], "dwk", ScalarType::Float, {r.d});
+        }
         const Tensor ws = r.c.workspace(a[14], ssm_qk_norm_rope_bwd_workspace_size(r.T, r.H, r.Hk, r.d, flags));
         auto at_ = [](const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
         const int rc = ssm_qk_norm_rope_bwd(r.q, r.k, r.wq, r.wk, r.inv_freq, r.positions, pgq, pgk, at_(dq), at_(dk),
@@ -369,9 +386,14 @@ PyObject *attn_decode_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
         auto *pl = (const int32_t *)c.whole(a[4], "lens", ScalarType::Int, {B});
         const float scale = number(a[5], "scale"), k_scale = number(a[7], "k_scale"), v_scale = number(a[8], "v_scale");
         const int64_t window = whole_number(a[6], "window");
-        const Tensor o = c.out(a[10], "o", type, {B, H, d});
         const bool want_lse = a[11] != Py_None || PyObject_IsTrue(a[9]) == 1;
-        const Tensor lse = want_lse ? c.out(a[11], "lse", ScalarType::Float, {B, H}) : Tensor();
+        Tensor o, lse;
+        if (want_lse && a[10] == Py_None && a[11] == Py_None) {
+            std::tie(o, lse) = std::tuple_cat(c.make_together<2>({{type, {B, H, d}}, {ScalarType::Float, {B, H}}}));
+        } else {
+            o = c.out(a[10], "o", type, {B, H, d});
+            if (want_lse) lse = c.out(a[11], "lse", ScalarType::Float, {B, H});
+        }
         const Tensor ws = c.workspace(a[12], ssm_paged_attn_decode_fwd_workspace_size(B, H, k.Hk, d, cols, k.page_size));
         const int rc = ssm_paged_attn_decode_fwd(
             pq, k.k, k.v, pt, pl, o.data_ptr(), want_lse ? (float *)lse.data_ptr() : nullptr, B, H, k.Hk, d, cols,

@@ -203,8 +203,15 @@ template <typename T, int V, bool IL> struct Lane {
 #pragma unroll
             for (int i = 0; i < V; ++i) cs[n][i] = sn[n][i] = 0.0f;     // of lanes without a token, too
         }
+    }
+    // loads that the first elements need not wait for
+    __device__ __forceinline__ void frequencies() {
+        if (half == 0) return;
+        float f[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) turns[k] = lane + 64 * k < half ? (double)a.inv_freq[lane + 64 * k] * kTurn : 0.0;
+        for (int k = 0; k < 2; ++k) f[k] = a.inv_freq[min(lane + 64 * k, half - 1)];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) turns[k] = (double)f[k] * kTurn;
     }
     // token and head of a pass; on: there is such a one
     struct At { int64_t t; int h, on; };
@@ -318,7 +325,6 @@ __global__ void __launch_bounds__(kFwdWaves * 64, 4) qk_rope_kernel(Kp a) {
     L me(a, s, tab + wave * s.tokens * a.rot);
     const bool norm = s.rotate && a.norm;
     float w[NU][2 * V];
-    if (norm) me.weights(w);
     const int64_t step = (int64_t)s.blocks * kFwdWaves;
     int64_t part = (int64_t)blk * kFwdWaves + wave;
     if (part >= s.parts) return;
@@ -330,6 +336,8 @@ __global__ void __launch_bounds__(kFwdWaves * 64, 4) qk_rope_kernel(Kp a) {
     typename L::At p = me.at(group, pass);
     me.load(raw, s.x, s.st, s.sh, p);
     int pos = s.rotate ? me.position(p) : 0;
+    if (norm) me.weights(w);
+    if (s.rotate) me.frequencies();
     while (true) {
         // what comes next is asked for first; steps over token groups keep their split (a wave
         // has several groups only where there is one)
@@ -410,8 +418,7 @@ __global__ void __launch_bounds__(kBwdWaves * 64, 3) qk_rope_bwd_kernel(Kp a) {
 #pragma unroll
     for (int n = 0; n < NU; ++n)
 #pragma unroll
-        for (int i = 0; i < 2 * V; ++i) { w[n][i] = 0.0f; dw[n][i] = 0.0f; }
-    if (a.norm) me.weights(w);
+        for (int i = 0; i < 2 * V; ++i) dw[n][i] = 0.0f;
     const int64_t step = (int64_t)s.blocks * kBwdWaves;
     const int64_t part = (int64_t)blk * kBwdWaves + wave;
     if (part < s.parts) {
@@ -423,6 +430,8 @@ __global__ void __launch_bounds__(kBwdWaves * 64, 3) qk_rope_bwd_kernel(Kp a) {
         me.load(raw_g, s.dy, s.dst, s.dsh, p);
         if (a.norm) me.load(raw, s.x, s.st, s.sh, p);
         int pos = me.position(p);
+        if (a.norm) me.weights(w);
+        me.frequencies();
         while (true) {
             const bool turn_group = pass + 1 >= pass1;
             const int64_t group_n = turn_group ? group + step : group;

@@ -22,10 +22,16 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kFwdWaves = 4;        // waves of a block, forward
-constexpr int kBwdWaves = 12;       // and backward: few blocks, whose shares of dw are joined after it
-constexpr int kFwdMost = 4096;      // waves of a launch: 4 on each SIMD
-constexpr int kBwdMost = 3072;      // 3 on each SIMD
+constexpr int kCUs = 256;
+constexpr int kFwdWaves = 4;        // waves of a block, forward: 4 on each SIMD of 4 blocks
+constexpr int kFwdBlocks = 4 * kCUs;
+// Backward: one block on a compute unit, so that few shares of dw are joined after it, with
+// the waves that its registers let run at once, 3 or 4 on a SIMD, by the bytes of one of a
+// lane's loads: 16 bf16 elements a lane take 150 registers, 8 take 102.  8 fp32 elements take
+// 118, which 4 waves would fit, but run faster on 3 (8k tokens of 16 + 4 heads of 128: 50.5
+// against 54.8 us).
+constexpr int bwd_waves(int bytes) { return bytes == 16 ? 12 : 16; }
+constexpr int kBwdBlocks = kCUs;
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const bf16x2 r = __builtin_convertvector((f32x2){a, b}, bf16x2);   // to nearest even
@@ -154,7 +160,7 @@ struct Side {
     int64_t st, sh, dst, dsh;      // strides of x and dy: token, head
     int heads, tokens, passes, each, splits;
     int64_t parts;                 // (token group, split) pairs
-    int blocks;
+    int blocks, stride, groups_on, splits_on;      // waves of the side, and what they add to a part
     bool rotate, cache;            // normed and rotated, or copied; y is a cache
 };
 struct Kp {
@@ -295,6 +301,31 @@ template <typename T, int V, bool IL> struct Lane {
     }
 };
 
+// The parts of a wave: (token group, split) pairs, as many apart as the side has waves, and
+// the passes of the group's heads that a split has.
+struct Walk {
+    int64_t part, group;
+    int split, pass0, pass1;
+    __device__ __forceinline__ Walk(const Side &s, uint32_t first) : part(first) {
+        const uint32_t g = first / (uint32_t)s.splits;
+        group = g;
+        split = (int)(first - g * (uint32_t)s.splits);
+        passes(s);
+    }
+    __device__ __forceinline__ void passes(const Side &s) {
+        pass0 = split * s.each;
+        pass1 = min(pass0 + s.each, s.passes);
+    }
+    __device__ __forceinline__ bool next(const Side &s) {
+        part += s.stride;
+        group += s.groups_on;
+        split += s.splits_on;
+        if (split >= s.splits) { split -= s.splits; ++group; }
+        passes(s);
+        return part < s.parts;
+    }
+};
+
 // the side of a block and the block's number in it
 __device__ __forceinline__ int side_of(const Kp &a, int &blk) {
     int i = 0;
@@ -325,36 +356,33 @@ __global__ void __launch_bounds__(kFwdWaves * 64, 4) qk_rope_kernel(Kp a) {
     L me(a, s, tab + wave * s.tokens * a.rot);
     const bool norm = s.rotate && a.norm;
     float w[NU][2 * V];
-    const int64_t step = (int64_t)s.blocks * kFwdWaves;
-    int64_t part = (int64_t)blk * kFwdWaves + wave;
-    if (part >= s.parts) return;
-    int64_t group = part / s.splits;
-    const int pass0 = (int)(part - group * s.splits) * s.each, pass1 = min(pass0 + s.each, s.passes);
-    int pass = pass0;
+    Walk at(s, (uint32_t)(blk * kFwdWaves + wave));
+    if (at.part >= s.parts) return;
+    int pass = at.pass0;
 
     typename L::Raw raw[NU][2], ahead[NU][2];
-    typename L::At p = me.at(group, pass);
+    typename L::At p = me.at(at.group, pass);
     me.load(raw, s.x, s.st, s.sh, p);
     int pos = s.rotate ? me.position(p) : 0;
+    bool turn_group = true;             // the present step is the first of its group
     if (norm) me.weights(w);
     if (s.rotate) me.frequencies();
     while (true) {
-        // what comes next is asked for first; steps over token groups keep their split (a wave
-        // has several groups only where there is one)
-        const bool turn_group = pass + 1 >= pass1;
-        const int64_t group_n = turn_group ? group + step : group;
-        const int pass_n = turn_group ? pass0 : pass + 1;
-        const bool more = turn_group ? s.splits == 1 && group_n < s.parts : true;
+        // what comes next is asked for first
+        const bool new_group = turn_group;
+        turn_group = pass + 1 >= at.pass1;
+        const bool more = turn_group ? at.next(s) : true;
+        const int pass_n = turn_group ? at.pass0 : pass + 1;
         typename L::At p_n = p;
         int pos_n = 0;
         if (more) {
-            p_n = me.at(group_n, pass_n);
+            p_n = me.at(at.group, pass_n);
             me.load(ahead, s.x, s.st, s.sh, p_n);
             if (turn_group && s.rotate) pos_n = me.position(p_n);
         }
         int64_t slot = 0;
         if (KV != 0 && s.cache && p.on) slot = a.slots[p.t];
-        if (s.rotate && pass == pass0) me.angles(pos);
+        if (s.rotate && new_group) me.angles(pos);
 
         float x[NU][2 * V], ss = 0.0f;
 #pragma unroll
@@ -394,7 +422,6 @@ __global__ void __launch_bounds__(kFwdWaves * 64, 4) qk_rope_kernel(Kp a) {
         }
         if (!more) break;
         p = p_n;
-        group = group_n;
         pass = pass_n;
         if (turn_group) pos = pos_n;
 #pragma unroll
@@ -406,7 +433,8 @@ __global__ void __launch_bounds__(kFwdWaves * 64, 4) qk_rope_kernel(Kp a) {
 // in every head); the shares of its lane groups are joined across lanes at the end, those of
 // the block's waves in LDS.
 template <typename T, int V, bool IL>
-__global__ void __launch_bounds__(kBwdWaves * 64, 3) qk_rope_bwd_kernel(Kp a) {
+__global__ void __launch_bounds__(bwd_waves(V * sizeof(T)) * 64, bwd_waves(V * sizeof(T)) / 4) qk_rope_bwd_kernel(Kp a) {
+    constexpr int WAVES = bwd_waves(V * sizeof(T));
     typedef Lane<T, V, IL> L;
     constexpr int NU = L::NU;
     extern __shared__ float tab[];
@@ -419,33 +447,31 @@ __global__ void __launch_bounds__(kBwdWaves * 64, 3) qk_rope_bwd_kernel(Kp a) {
     for (int n = 0; n < NU; ++n)
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) dw[n][i] = 0.0f;
-    const int64_t step = (int64_t)s.blocks * kBwdWaves;
-    const int64_t part = (int64_t)blk * kBwdWaves + wave;
-    if (part < s.parts) {
-        int64_t group = part / s.splits;
-        const int pass0 = (int)(part - group * s.splits) * s.each, pass1 = min(pass0 + s.each, s.passes);
-        int pass = pass0;
+    Walk at(s, (uint32_t)(blk * WAVES + wave));
+    if (at.part < s.parts) {
+        int pass = at.pass0;
         typename L::Raw raw[NU][2], raw_g[NU][2], ahead[NU][2], ahead_g[NU][2];
-        typename L::At p = me.at(group, pass);
+        typename L::At p = me.at(at.group, pass);
         me.load(raw_g, s.dy, s.dst, s.dsh, p);
         if (a.norm) me.load(raw, s.x, s.st, s.sh, p);
         int pos = me.position(p);
+        bool turn_group = true;         // the present step is the first of its group
         if (a.norm) me.weights(w);
         me.frequencies();
         while (true) {
-            const bool turn_group = pass + 1 >= pass1;
-            const int64_t group_n = turn_group ? group + step : group;
-            const int pass_n = turn_group ? pass0 : pass + 1;
-            const bool more = turn_group ? s.splits == 1 && group_n < s.parts : true;
+            const bool new_group = turn_group;
+            turn_group = pass + 1 >= at.pass1;
+            const bool more = turn_group ? at.next(s) : true;
+            const int pass_n = turn_group ? at.pass0 : pass + 1;
             typename L::At p_n = p;
             int pos_n = 0;
             if (more) {
-                p_n = me.at(group_n, pass_n);
+                p_n = me.at(at.group, pass_n);
                 me.load(ahead_g, s.dy, s.dst, s.dsh, p_n);
                 if (a.norm) me.load(ahead, s.x, s.st, s.sh, p_n);
                 if (turn_group) pos_n = me.position(p_n);
             }
-            if (pass == pass0) me.angles(pos);
+            if (new_group) me.angles(pos);
 
             float x[NU][2 * V], g[NU][2 * V], ss = 0.0f, sg = 0.0f;
 #pragma unroll
@@ -482,7 +508,6 @@ __global__ void __launch_bounds__(kBwdWaves * 64, 3) qk_rope_bwd_kernel(Kp a) {
             }
             if (!more) break;
             p = p_n;
-            group = group_n;
             pass = pass_n;
             if (turn_group) pos = pos_n;
 #pragma unroll
@@ -508,10 +533,10 @@ __global__ void __launch_bounds__(kBwdWaves * 64, 3) qk_rope_bwd_kernel(Kp a) {
             }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.d; e += kBwdWaves * 64) {
+    for (int e = threadIdx.x; e < a.d; e += WAVES * 64) {
         float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kBwdWaves; ++k) v += tab[k * a.d + e];
+        for (int k = 0; k < WAVES; ++k) v += tab[k * a.d + e];
         s.part[(int64_t)blk * a.d + e] = v;
     }
 }
@@ -562,24 +587,34 @@ void set_geometry(Kp &k, int v, int d, int rot) {
 }
 
 // blocks that a side may have: its share of the launch's, by heads
-int blocks_of(int64_t heads, int64_t all_heads, int waves) {
-    const int most = (waves == kFwdWaves ? kFwdMost : kBwdMost) / waves;
+int blocks_of(int64_t heads, int64_t all_heads, int most) {
     return (int)std::max<int64_t>(1, most * heads / all_heads);
 }
 
-// Waves of a side: a token group each, or several where that is more than the chip holds
-// at once; where it is fewer, the passes over a token's heads are split between waves.
-void set_work(Side &s, const Kp &k, int64_t n_tokens, int64_t all_heads, int waves) {
+// Parts of a side's work, (token group, split of its passes) pairs dealt to the waves that
+// the chip holds at once.  A group is split where that evens the waves' steps out, or gives more of
+// them one (4096 tokens of 64 + 8 heads of 128: 34.3 us in whole groups, 30.7 split); a part costs
+// about half a step more, for its angles.
+void set_work(Side &s, const Kp &k, int64_t n_tokens, int64_t all_heads, int waves, int blocks) {
     const int groups = 64 >> k.lg;
     s.tokens = std::max(1, groups / s.heads);
     s.passes = (s.heads + groups - 1) / groups;
     const int64_t token_groups = (n_tokens + s.tokens - 1) / s.tokens;
-    const int64_t most = (int64_t)blocks_of(s.heads, all_heads, waves) * waves;
-    s.splits = (int)std::min<int64_t>(s.passes, std::max<int64_t>(1, most / std::max<int64_t>(1, token_groups)));
-    s.each = (s.passes + s.splits - 1) / s.splits;
-    s.splits = (s.passes + s.each - 1) / s.each;
+    const int64_t most = (int64_t)blocks_of(s.heads, all_heads, blocks) * waves;
+    int64_t best = INT64_MAX;
+    for (int t = 1; t <= std::min(s.passes, 64); ++t) {
+        const int each = (s.passes + t - 1) / t, splits = (s.passes + each - 1) / each;
+        const int64_t steps = (token_groups * splits + most - 1) / most * (2 * each + 1);
+        if (steps >= best) continue;
+        best = steps;
+        s.each = each;
+        s.splits = splits;
+    }
     s.parts = token_groups * s.splits;
     s.blocks = (int)((std::min(s.parts, most) + waves - 1) / waves);
+    s.stride = s.blocks * waves;
+    s.groups_on = s.stride / s.splits;
+    s.splits_on = s.stride % s.splits;
 }
 
 size_t table_bytes(const Kp &k, int waves) {
@@ -637,7 +672,7 @@ hipError_t launch_qk_rope(const QkRopeArgs &a, hipStream_t stream, const char **
         Side &s = k.side[i];
         s.x = x; s.y = y; s.w = w; s.st = st; s.sh = sh;
         s.heads = (int)heads; s.rotate = rotate; s.cache = to_cache;
-        set_work(s, k, a.n_tokens, a.n_heads + (cache ? 2 : 1) * a.n_kv_heads, kFwdWaves);
+        set_work(s, k, a.n_tokens, a.n_heads + (cache ? 2 : 1) * a.n_kv_heads, kFwdWaves, kFwdBlocks);
     };
     side(0, a.q, a.q_out, a.wq, a.q_st, a.q_sh, a.n_heads, true, false);
     if (a.n_kv_heads > 0) side(1, a.k, a.k_out, a.wk, a.k_st, a.k_sh, a.n_kv_heads, true, cache);
@@ -656,7 +691,7 @@ size_t qk_rope_bwd_workspace_bytes(int64_t n_tokens, int64_t n_heads, int64_t n_
     if (flags & SSM_QK_NO_NORM) return 0;
     const int64_t all = n_heads + n_kv_heads;
     auto blocks = [&](int64_t heads) {           // each wave has a (token, head) at least
-        return std::min<int64_t>(n_tokens * heads / kBwdWaves + 1, blocks_of(heads, all, kBwdWaves));
+        return std::min<int64_t>(n_tokens * heads / bwd_waves(16) + 1, blocks_of(heads, all, kBwdBlocks));
     };
     return (size_t)(blocks(n_heads) + (n_kv_heads > 0 ? blocks(n_kv_heads) : 0)) * (size_t)headdim * sizeof(float);
 }
@@ -667,7 +702,12 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
     const void *ptr[] = {a.q, a.dq_out, a.dq, a.k, a.dk_out, a.dk};
     const int64_t stride[] = {a.q_st, a.q_sh, a.dq_st, a.dq_sh, (int64_t)a.headdim, a.k_st, a.k_sh, a.dk_st, a.dk_sh};
     const bool has_k = a.n_kv_heads > 0, norm = (a.flags & SSM_QK_NO_NORM) == 0;
-    const int v = pick_v(ptr, stride, has_k ? 6 : 3, has_k ? 9 : 5, a.headdim, a.rot_dim, esize, a.wq, a.wk);
+    int v = pick_v(ptr, stride, has_k ? 6 : 3, has_k ? 9 : 5, a.headdim, a.rot_dim, esize, a.wq, a.wk);
+    // 8 elements a lane save instructions and cost a quarter of the waves (150 registers against
+    // 102): 16k tokens of 16 + 4 heads of 128 67 us against 63 with 4, of 64 + 8 heads the same;
+    // 8k tokens of heads of 256 55 against 63
+    if (v == 8 && a.headdim <= 128) v = 4;
+    const int waves = bwd_waves(v * esize);
     Kp k = {};
     set_geometry(k, v, a.headdim, a.rot_dim);
     k.inv_freq = a.inv_freq; k.positions = a.positions;
@@ -677,20 +717,20 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
         Side &s = k.side[i];
         s.x = x; s.dy = dy; s.y = y; s.w = w; s.st = st; s.sh = sh; s.dst = dst; s.dsh = dsh;
         s.heads = (int)heads; s.rotate = true;
-        set_work(s, k, a.n_tokens, a.n_heads + a.n_kv_heads, kBwdWaves);
+        set_work(s, k, a.n_tokens, a.n_heads + a.n_kv_heads, waves, kBwdBlocks);
     };
     side(0, a.q, a.dq_out, a.dq, a.wq, a.q_st, a.q_sh, a.dq_st, a.dq_sh, a.n_heads);
     if (has_k) side(1, a.k, a.dk_out, a.dk, a.wk, a.k_st, a.k_sh, a.dk_st, a.dk_sh, a.n_kv_heads);
     float *ws = (float *)a.workspace;
     k.side[0].part = ws;
     k.side[1].part = norm ? ws + (int64_t)k.side[0].blocks * a.headdim : nullptr;
-    const size_t lds = std::max(table_bytes(k, kBwdWaves), norm ? (size_t)kBwdWaves * a.headdim * sizeof(float) : 0);
+    const size_t lds = std::max(table_bytes(k, waves), norm ? (size_t)waves * a.headdim * sizeof(float) : 0);
     const unsigned blocks = (unsigned)(k.side[0].blocks + k.side[1].blocks);
     const bool il = (a.flags & SSM_ROPE_INTERLEAVED) != 0;
 #define SSM_BWD(T, V)                                                                                           \
     do {                                                                                                        \
-        if (il) hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, true>), dim3(blocks), dim3(kBwdWaves * 64), lds, stream, k);  \
-        else hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, false>), dim3(blocks), dim3(kBwdWaves * 64), lds, stream, k);    \
+        if (il) hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, true>), dim3(blocks), dim3(waves * 64), lds, stream, k);  \
+        else hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, false>), dim3(blocks), dim3(waves * 64), lds, stream, k);    \
     } while (0)
     if (blocks > 0) {
         if (a.bf16) {

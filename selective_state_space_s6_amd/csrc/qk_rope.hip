@@ -107,7 +107,7 @@ __device__ __forceinline__ float2 cos_sin(int position, double turns) {     // t
     const double t = (double)position * turns;
     const double f = t - rint(t);
     const double q = rint(4.0 * f);                     // -2 .. 2
-    const float y = (float)(f - 0.25 * q) * 6.28318530717958647692f;
+    const float y = (float)((f - 0.25 * q) * 6.28318530717958647692);
     const float z = y * y;
     const float s = fmaf(y * z, fmaf(z, fmaf(z, fmaf(z, 2.75573192e-6f, -1.98412698e-4f), 8.33333333e-3f), -1.66666667e-1f), y);
     const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.75573192e-7f, 2.48015873e-5f), -1.38888889e-3f), 4.16666667e-2f), -0.5f), 1.0f);
@@ -116,10 +116,19 @@ __device__ __forceinline__ float2 cos_sin(int position, double turns) {     // t
     return make_float2((n == 1 || n == 2) ? -cc : cc, n >= 2 ? -ss : ss);
 }
 
-// 1 / sqrt(v): the instruction, within an ulp, on a v that it does not flush to zero
+// 1 / sqrt(v): the instruction, within an ulp, on a v that it does not flush to zero; for
+// fp32 elements with a Newton step (bf16 rounds to 2^-9 afterwards), which leaves an
+// infinite v's 0 and a zero's infinity alone
+template <typename T>
 __device__ __forceinline__ float inv_sqrt(float v) {
     const bool tiny = v < 0x1p-96f;
-    return __builtin_amdgcn_rsqf(tiny ? v * 0x1p96f : v) * (tiny ? 0x1p48f : 1.0f);
+    const float u = tiny ? v * 0x1p96f : v;
+    float r = __builtin_amdgcn_rsqf(u);
+    if constexpr (sizeof(T) == 4) {
+        const float e = fmaf(-u * r, r, 1.0f);
+        r = fabsf(e) < 0.5f ? fmaf(0.5f * r, e, r) : r;
+    }
+    return r * (tiny ? 0x1p48f : 1.0f);
 }
 
 // sum over the 2^lg lanes of a group (lg is the same in the whole launch); every lane
@@ -393,7 +402,7 @@ __global__ void __launch_bounds__(kFwdWaves * 64, 4) qk_rope_kernel(Kp a) {
             for (int i = 0; i < 2 * V; ++i) ss = fmaf(x[n][i], x[n][i], ss);
         }
         if (norm) {
-            const float r = inv_sqrt(fmaf(group_sum(ss, a.lg), a.inv_d, a.eps));
+            const float r = inv_sqrt<T>(fmaf(group_sum(ss, a.lg), a.inv_d, a.eps));
 #pragma unroll
             for (int n = 0; n < NU; ++n)
 #pragma unroll
@@ -490,7 +499,7 @@ __global__ void __launch_bounds__(bwd_waves(V * sizeof(T)) * 64, bwd_waves(V * s
                 }
             }
             if (a.norm) {
-                const float r = inv_sqrt(fmaf(group_sum(ss, a.lg), a.inv_d, a.eps));
+                const float r = inv_sqrt<T>(fmaf(group_sum(ss, a.lg), a.inv_d, a.eps));
                 const float c = group_sum(sg, a.lg) * a.inv_d * r * r;
 #pragma unroll
                 for (int n = 0; n < NU; ++n)

@@ -236,7 +236,11 @@ __global__ void __launch_bounds__(kNT) kv_pages_kernel(KvPagesArgs a) {
 hipError_t launch_kv_pages(const KvPagesArgs &a, hipStream_t stream, const char **kernel_name) {
     *kernel_name = "kv_pages_kernel";
     const int64_t work = (a.n_tokens + kTok - 1) / kTok;
+    // a thread for 4 tokens; a block a request, for the pages that it may give back or take, of
+    // which the host does not know how many there are: 256 requests with 86 of 125 pages each
+    // ending 10.4 us on 8 blocks, 6.5 us on 256
     int64_t blocks = (work + kNT - 1) / kNT;
+    blocks = blocks < a.batch ? a.batch : blocks;
     blocks = blocks < 8 ? 8 : blocks > 512 ? 512 : blocks;
     hipLaunchKernelGGL(kv_pages_kernel, dim3((unsigned)blocks), dim3(kNT), (size_t)a.batch * 3 * sizeof(int), stream, a);
     return hipGetLastError();

@@ -2,6 +2,10 @@
 // same pass, its gradients, and its form that writes k and v into a paged cache
 // (ssm_qk_norm_rope_* in include/ssm_attn.h).
 //
+// Forward: n = x r w with r = 1 / sqrt(mean x^2 + eps), and each pair (a, b) of the first
+// rot_dim elements turned by its angle, position * inv_freq: (a c - b s, b c + a s).
+// Backward: g = dy turned back, dx = r (w g - x r^2 mean(x w g)), dw = sum of g x r.
+//
 // All of them move every element once and are bound by HBM.  A wave takes a token at
 // a time (of few heads, several) of one side, q, k or v.  Its 64 lanes form the
 // token's cosines and sines, one or two each, and hand them round through a part of
@@ -9,6 +13,12 @@
 // head each: a lane holds 2 V elements of it, chosen so that both halves of each rotated
 // pair are its own, and only the norm's sums cross lanes.  The next heads' elements are
 // asked for before the present ones are worked on, and no wave waits for another.
+//
+// Measured, kernels alone, 16384 tokens of 16 + 4 heads of 128 in bf16: forward 168 MB 41 us (4.1
+// TB/s; the same kernel without norm and rotation 35, a strided copy 35 to 37), backward 252
+// MB 60 us (4.2 TB/s) and 4.7 us to join dw.  8192 tokens of 32 + 8 + 8 heads into an 8-bit cache
+// 185 MB 47 us.  64 tokens into a cache 4.3 us, 1021 fp32 tokens of 6 + 3 heads of 72 5.0 us:
+// a chain of loads.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <algorithm>
@@ -573,7 +583,8 @@ __global__ void __launch_bounds__(256) qk_rope_dw_kernel(const float *pq, const 
 
 // ------------------------------------------------------------------ host ----
 // Widest V whose unit of 2 V elements fits the rotation's halves, what follows it, and
-// every address: 16 bytes where possible.  V = 1 fits everything.
+// every address: 16 bytes where possible.  V = 1 fits everything.  (Forward, bf16, V = 8 against 4:
+// 16k tokens of 16 + 4 heads of 128 39.9 and 42.4 us, of 64 19.7 and 21.8, 8k of 256 33.5 and 39.8.)
 int pick_v(const void *const *ptr, const int64_t *stride, int np, int ns, int d, int rot, int esize,
            const float *wq, const float *wk) {
     if ((((uintptr_t)wq | (uintptr_t)wk) & 15) != 0) return 1;     // weights are loaded by fours

@@ -1,4 +1,4 @@
-"""ssm_kv_pages_step on the GPU against the fp64-free list oracle: whole numbers, so every
+"""ssm_kv_pages_step on the GPU against the oracle's lists: whole numbers, so every
 output has to be equal."""
 import numpy as np
 import pytest

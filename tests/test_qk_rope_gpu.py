@@ -74,6 +74,7 @@ SHAPES = [  # T, H, Hk, d, rot, dtype, interleaved, norm
     (6, 40, 1, 8, 8, "f32", False, True),
     (3, 2, 1, 1, 0, "f32", False, True),
     (700, 300, 7, 64, 64, "bf16", False, True),     # more heads than a block has lane groups
+    (2000, 20, 4, 128, 64, "bf16", False, True),    # a token's heads in parts, more of them than waves
 ]
 _id = lambda c: "T%d-H%d-%d-d%d-r%d-%s-%d%d" % c  # noqa: E731
 

@@ -25,7 +25,7 @@
 //    it are the lane's own.
 // 8-bit elements widen to bf16 exactly.  Scores, maxima, sums and outputs are fp32.
 //
-// Measured (both kernels): 64 rows of up to 8192 tokens, 32 + 8 heads of 128, bf16, 1.07 GB of
+// Measured (both kernels): 64 rows of up to 8192 tokens, 32 + 8 heads of 128, bf16, 1.06 GB of
 // cache 205 us (5.2 TB/s; the counters show those bytes fetched and no others); 16 rows of 65536,
 // 64 + 8 heads of 128, 8 bits, 2.15 GB 370 us (5.8 TB/s); 48 rows of up to 5000 tokens, 5 + 1
 // heads of 256, fp32, 234 MB 62 us (3.8 TB/s, 6 of it the join); one row of 2047 tokens 10 us, two

@@ -509,7 +509,9 @@ __global__ void __launch_bounds__(bwd_waves(V * sizeof(T)) * 64, bwd_waves(V * s
                 }
             }
             if (a.norm) {
-                const float r = inv_sqrt<T>(fmaf(group_sum(ss, a.lg), a.inv_d, a.eps));
+                // (lanes without a head: with eps = 0 their 1/0 would turn all of dw into NaN)
+                const float mean = fmaf(group_sum(ss, a.lg), a.inv_d, a.eps);
+                const float r = p.on ? inv_sqrt<T>(mean) : 0.0f;
                 const float c = group_sum(sg, a.lg) * a.inv_d * r * r;
 #pragma unroll
                 for (int n = 0; n < NU; ++n)

@@ -154,6 +154,24 @@ def test_backward_against_differences(cuda_device):
         assert abs(want - have) <= bound
 
 
+@pytest.mark.parametrize("case", [(33, 3, 1, 128, 64, "bf16", False, True), (5, 6, 3, 72, 24, "f32", True, True),
+                                  (7, 1, 1, 31, 10, "f32", False, True)], ids=_id)
+def test_backward_without_an_eps(cuda_device, case):
+    """eps = 0 where heads do not fill a wave's lanes: the idle lanes' 1/0 stays out of dw.
+    Bounds as above."""
+    T, H, Hk, d, rot, dtype, il, norm = case
+    q, k, v, w, f, pos, g, flags = _make(case, cuda_device, 12)
+    got = lib().ssm_qk_norm_rope_bwd(q, k, w[0], w[1], f, pos, g[0], g[1], eps=0.0, flags=flags)
+    for n, x, wx, gx in (("q", q, w[0], g[0]), ("k", k, w[1], g[1])):
+        dx, dw = paged.qk_norm_rope_bwd(_n(x), _n(wx), _n(f), _n(pos), _n(gx), eps=0.0, interleaved=il)
+        r = 1.0 / np.sqrt((_n(x) ** 2).mean(-1, keepdims=True))
+        size = _pair(np.abs(_n(gx)), rot, il)
+        wg, nx = np.abs(_n(wx)) * size, np.abs(_n(x)) * r
+        _check("rope eps 0 dw%s %s" % (n, case), got["dw" + n], dw, (40 + 128) * U * (size * nx).sum((0, 1)))
+        size = r * (wg + nx * (wg * nx).mean(-1, keepdims=True))
+        _check("rope eps 0 d%s %s" % (n, case), got["d" + n], dx, 64 * U * size + (2.0 ** -8 * np.abs(dx) if dtype == "bf16" else 0))
+
+
 def test_in_place_q_alone_and_odd_views(cuda_device):
     import torch
     m = lib()

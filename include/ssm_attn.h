@@ -189,7 +189,10 @@ int ssm_qk_norm_rope_cache_fwd(const void *q, const void *k, const void *v, cons
  * times the passes).
  * The cache is read once per 16 query heads of a kv head.  Work is cut by
  * length, not by row, into equal shares over the chip, whatever the lengths
- * are, and the shares of a row are joined by their maxima and sums.
+ * are, and the shares of a row are joined by their maxima and sums; where the
+ * table or the window keeps every row short, a row's head is one share (one
+ * launch instead of two).  Which of the two follows from the arguments, not
+ * from lens.  An infinite v gives NaN where the formula may give an infinity.
  * Workspace: ssm_paged_attn_decode_fwd_workspace_size() bytes, 16-byte aligned
  * (the rows' places in the work, and the unjoined shares). */
 size_t ssm_paged_attn_decode_fwd_workspace_size(int64_t batch, int64_t n_heads, int64_t n_kv_heads,

@@ -10,7 +10,8 @@
 // all rows stand in one line, and each resident block takes an equal piece of it,
 // whatever the rows' lengths are.  A piece that does not hold a whole (row, kv head) leaves
 // its unnormalised output, maximum and sum in the workspace, and a second kernel joins those,
-// in an order that the lengths alone decide.
+// in an order that the lengths alone decide.  Where rows cannot be long (a short table, or a window), a
+// block takes a whole (row, kv head) instead, and the call is one launch.
 //
 // Inside a block every wave walks tiles of its own with a running maximum and sum, and
 // takes its operands from global memory straight into the matrix instructions' registers:
@@ -62,6 +63,7 @@ struct Kp {
     int batch, n_heads, n_kv, group, passes, gmax;   // group: query heads a kv head; passes of gmax <= 16 of them
     int d, n_pages, page_size, max_len, window, unit, unit_lg;
     int wh_lg;                      // 2^wh_lg kv heads side by side (worker_of)
+    bool whole;                     // a block for each (row, kv head, pass), and nothing to join
     float scale2, v_scale;          // scale2: score -> log2 units
 };
 
@@ -201,7 +203,25 @@ __global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_att
     const int per = (a.n_kv >> a.wh_lg) * a.passes;      // (kv heads side by side, pass) of a row
     const int blk = worker_of(blockIdx.x, a.wh_lg), side = side_of(blockIdx.x, a.wh_lg);
     int units = 0, u, u_end, row, row_u, row_len;
-    if (a.batch <= 64) {                    // each wave for itself: row `lane`
+    if (a.whole) {                          // the units of its own row alone, from 0 on
+        row = (int)((uint32_t)blk / (uint32_t)per);
+        if (row >= a.batch) return;
+        const int hp = blk - row * per;
+        row_u = 0;
+        row_len = a.lens[row];
+        units = span_of(a, row_len).units;
+        u = hp * units;
+        u_end = u + units;
+        if (units == 0) {                   // no token: o = 0, lse = -inf
+            const int kvs = hp / a.passes, pass = hp - kvs * a.passes, kv = (kvs << a.wh_lg) + side;
+            const int nh = min(a.gmax, a.group - pass * a.gmax);
+            const int64_t h = (int64_t)row * a.n_heads + kv * a.group + pass * a.gmax;
+            constexpr int OE = CT == KF32 ? 4 : 2;
+            for (int i = tid; i < nh * a.d * OE / 16; i += W * 64) *(u32x4 *)(a.o + h * a.d * OE + i * 16) = (u32x4){0, 0, 0, 0};
+            if (a.lse && tid < nh) a.lse[h + tid] = -INFINITY;
+            return;
+        }
+    } else if (a.batch <= 64) {                    // each wave for itself: row `lane`
         const int len = lane < a.batch ? a.lens[lane] : 0, own_units = span_of(a, len).units * per;
         const int upto = wave_scan(own_units), before = upto - own_units;
         units = __builtin_amdgcn_readlane(upto, 63);
@@ -595,17 +615,20 @@ __global__ void __launch_bounds__(kNT) paged_attn_join_kernel(Kp a, int grid) {
 int64_t passes_of(int64_t group) { return (group + kHeads - 1) / kHeads; }
 int64_t align16(int64_t n) { return (n + 15) & ~int64_t(15); }
 
+// waves of the largest grid that are resident at once
+constexpr int64_t waves_of(int per_simd) { return per_simd * 4 * kCUs; }
+
 template <int CT, int DP, bool EXACT, int W>
 hipError_t go_w(Kp &k, int &grid, hipStream_t stream) {
     using T = Tile<CT, DP, W>;
     k.unit = T::UNIT;
     k.unit_lg = __builtin_ctz(T::UNIT);
     while (k.wh_lg < 2 && (T::PER_SIMD == 1 || (k.c_sh << k.wh_lg) % 128 != 0) && (k.n_kv >> k.wh_lg) % 2 == 0) ++k.wh_lg;
-    // those that are resident at once, or one a unit if there are fewer; whole groups of heads side by side
+    // the blocks that are resident at once, or one a unit if there are fewer; whole groups of heads side by side
     const double units = (double)k.batch * k.n_kv * k.passes * ((k.max_len + T::UNIT - 1) / T::UNIT);
-    grid = (int)std::max(1.0, std::min(units, (double)(T::RES * kCUs)));
-    const int whole = 8 << k.wh_lg;
-    if (k.wh_lg > 0) grid = (grid + whole - 1) / whole * whole;
+    grid = k.whole ? k.batch * k.n_kv * k.passes : (int)std::max(1.0, std::min(units, (double)(T::RES * kCUs)));
+    const int group = 8 << k.wh_lg;
+    if (k.wh_lg > 0) grid = (grid + group - 1) / group * group;
     const size_t lds = std::max((size_t)W * k.gmax * (DP + 4) * sizeof(float), T::QLDS ? (size_t)T::KC * T::QW * 1024 : 0);
     if (lds > 32 * 1024) {               // more than a block has unasked, from 64 KiB on
         const hipError_t e = hipFuncSetAttribute((const void *)paged_attn_kernel<CT, DP, EXACT, W>,
@@ -615,19 +638,25 @@ hipError_t go_w(Kp &k, int &grid, hipStream_t stream) {
     hipLaunchKernelGGL((paged_attn_kernel<CT, DP, EXACT, W>), dim3((unsigned)grid), dim3(W * 64), lds, stream, k);
     return hipGetLastError();
 }
-// Where there is a (row, kv head) for every wave that fits the chip, or none is longer than
-// two tiles, a block is one wave: it takes whole heads, short ones too, without waiting for
-// others.  Else four waves share the tokens of a piece, and fewer pieces are left to join.
-// One wave against four: 256 rows x 8 heads of up to 200 tokens 46.6 against 50.7 us, one row of
-// 100000 tokens 32.8 against 23.1 us.
-bool one_wave(int64_t batch, int64_t n_kv, int64_t passes, int per_simd, int64_t max_len, int tile) {
-    return batch * n_kv * passes >= per_simd * 4 * kCUs || max_len <= 2 * tile;
-}
+// Blocks of one wave or of four, and whole (row, kv head)s or equal pieces.  A whole one saves the second
+// launch and the search for a piece, and makes a block work for as long as its row is, so it is taken
+// where rows reach few tiles, more of them if there are many rows to even the blocks out.  One wave
+// takes a head where every wave of the chip has one or nearly so.  us, bf16 heads of 128, 8 kv heads, all rows
+// of the length (whole in one wave, whole in four, pieces):
+//   1 row of 32 tokens 5.7, 5.7, 8.2; 300: 12.0, 7.7, 9.6; 600: 19.8, 10.5, 10.0; 2400: 67, 28, 10.6
+//   64 rows of 128 tokens 10.3, 9.2, 12.1; 600: 36.9, 29.6, 32.9; up to 1200: 59, 39, 39; up to 2400: 118, 78, 71
+//   256 rows of 128 tokens 24.4, 29.0, 30.2; up to 300: 32.8, 38.9, 43.5; up to 1200: 132, 130, 136; up to 2400: 255, 248, 244
+// and of 4 and 3 kv heads in 8 and 32 bits, heads of 64 and 256 the same way.  In pieces, four waves share the
+// tokens of one, and fewer pieces are left to join; one row of 100000 tokens 32.8 us by waves, 23.1 by fours.
 template <int CT, int DP, bool EXACT>
 hipError_t go(Kp &k, int &grid, hipStream_t stream) {
     using T = Tile<CT, DP, 1>;
-    return one_wave(k.batch, k.n_kv, k.passes, T::PER_SIMD, k.max_len, T::NT) ? go_w<CT, DP, EXACT, 1>(k, grid, stream)
-                                                                              : go_w<CT, DP, EXACT, 4>(k, grid, stream);
+    const int64_t heads = (int64_t)k.batch * k.n_kv * k.passes, waves = waves_of(T::PER_SIMD);
+    const int tiles = ((k.window > 0 ? k.window : k.max_len) + T::NT - 1) / T::NT;
+    const bool by_wave = tiles <= 1 || (heads >= waves / 2 && tiles <= (heads >= waves ? 32 : 16));
+    const bool by_block = tiles <= (heads >= waves / 4 ? 40 : heads >= waves / 8 ? 20 : 12);
+    k.whole = (by_wave || by_block) && heads < (1 << 22);      // (a grid's threads are counted in 32 bits)
+    return (k.whole ? by_wave : heads >= waves) ? go_w<CT, DP, EXACT, 1>(k, grid, stream) : go_w<CT, DP, EXACT, 4>(k, grid, stream);
 }
 template <int CT, int DP>
 hipError_t go_d(Kp &k, int &grid, hipStream_t stream) {
@@ -653,9 +682,9 @@ double paged_attn_max_units(int64_t batch, int64_t n_heads, int64_t n_kv_heads, 
 static int64_t most_blocks(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t headdim, int64_t max_pages,
                            int64_t page_size) {
     const int per_simd = headdim <= 128 ? 2 : 1;
-    const bool one = one_wave(batch, n_kv_heads, passes_of(n_heads / n_kv_heads), per_simd, max_pages * page_size, 64);
+    const bool one = batch * n_kv_heads * passes_of(n_heads / n_kv_heads) >= waves_of(per_simd);
     const double units = paged_attn_max_units(batch, n_heads, n_kv_heads, max_pages, page_size) + 32;
-    return (int64_t)std::min(units, (double)(per_simd * kCUs * (one ? 4 : 1)));
+    return (int64_t)std::min(units, (double)(waves_of(per_simd) / (one ? 1 : 4)));
 }
 
 size_t paged_attn_workspace_bytes(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t headdim,
@@ -690,7 +719,7 @@ hipError_t launch_paged_attn(const PagedAttnArgs &a, hipStream_t stream, const c
     const hipError_t rc = a.kv_dtype == SSM_KV_F32 ? go_type<KF32>(k, grid, stream)
                         : a.kv_dtype == SSM_KV_BF16 ? go_type<KBF16>(k, grid, stream)
                                                     : go_type<KF8>(k, grid, stream);
-    if (rc != hipSuccess) return rc;
+    if (rc != hipSuccess || k.whole) return rc;
     *kernel_name = "paged_attn_join_kernel";
     // Where a head has many pieces, a block joins it, or several of 32 dims each; else its waves a head
     // each.  One row of 100000 tokens 22.7 us with, 46 without the split; 256 rows of up to 60

@@ -132,6 +132,17 @@ CASES = [  # lens, H, Hk, d, cache, page, layout, window
     (list(range(3, 143, 2)) * 8, 4, 4, 128, "f8", 64, "hnd", 0),
     ([5, 0, 700] * 120, 6, 3, 256, "f32", 16, "nhd", 0),
     ([2000] + [1] * 1100, 2, 2, 128, "f32", 16, "nhd", 0),
+    # short rows, a block for each (row, kv head): by the window alone, in two passes, side by side
+    (EDGES + [7000], 4, 2, 128, "bf16", 16, "nhd", 300),
+    (EDGES + [7000], 34, 2, 128, "bf16", 24, "hnd", 300),
+    (EDGES, 6, 6, 80, "bf16", 7, "nhd", 257),
+    ([100, 0, 31, 384], 40, 1, 128, "bf16", 16, "nhd", 0),
+    (EDGES, 8, 4, 192, "f32", 16, "nhd", 150),
+    (list(range(0, 600, 5)) * 2, 2, 1, 72, "bf16", 1, "nhd", 0),
+    (list(range(40, 440)) + [0], 6, 3, 256, "bf16", 16, "nhd", 0),
+    # and rows too long for that, on blocks of one wave
+    ([2100] + [7] * 1050, 2, 2, 64, "bf16", 16, "hnd", 0),
+    ([0, 2100, 64] * 350, 4, 2, 128, "f8", 16, "nhd", 0),
 ]
 
 
@@ -248,7 +259,7 @@ def test_a_cache_past_4_gib(cuda_device):
     _compare("attn 5 GiB", got, q, kc[last], vc[last], np.array([[0, 1, 2, 3, 4]]), [77], 0.09, 1.0)
 
 
-@pytest.mark.parametrize("H,Hk,d", [(8, 2, 128), (16, 1, 256)])     # the second: 65 KiB of LDS a block
+@pytest.mark.parametrize("H,Hk,d", [(8, 2, 128), (16, 1, 256), (4, 2, 64)])     # 65 KiB of LDS a block; a block a head
 def test_in_a_graph_with_lens_and_table_changing(cuda_device, H, Hk, d):
     """Captured once; lens, table and q change in place between replays.  The grid depends on
     the table's size alone, so every replay has to equal the eager call."""

@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kNT = 256;            // threads of a block
 constexpr int kWaves = kNT / 64;
+constexpr int kKeep = 2;            // requests of a thread whose lengths stay in registers
 constexpr int kTok = 4;             // consecutive tokens of a thread: one 16-byte store of each 32-bit output
 
 // x / page size, by a shift where that is a power of two
@@ -45,14 +46,16 @@ struct Need {
     __device__ __forceinline__ int give() const { return max(have - want, 0); }
 };
 
-__device__ __forceinline__ Need need_of(const KvPagesArgs &a, const Pages &pages, int r) {
-    const int lo = max(a.len_old[r], 0), hi = max(a.len_new[r], 0);
+__device__ __forceinline__ Need need_of(const KvPagesArgs &a, const Pages &pages, int lo, int hi) {
     Need n;
     n.have = min(pages.to_hold(lo), a.max_pages);     // a longer row has no entries to read
     n.want = pages.to_hold(hi);
     n.grow = max(hi - lo, 0);
     n.over = n.want > a.max_pages;
     return n;
+}
+__device__ __forceinline__ Need need_of(const KvPagesArgs &a, const Pages &pages, int r) {
+    return need_of(a, pages, max(a.len_old[r], 0), max(a.len_new[r], 0));
 }
 
 // place i < 2 n of a ring of n entries
@@ -76,6 +79,16 @@ __device__ __forceinline__ T wave_scan(T v) {
     v += dpp_i<0x143, 0xc>(v);
     return v;
 }
+// the largest of a wave's values >= 0, in lane 63
+__device__ __forceinline__ int wave_max(int v) {
+    v = max(v, dpp_i<0x111>(v));
+    v = max(v, dpp_i<0x112>(v));
+    v = max(v, dpp_i<0x114>(v));
+    v = max(v, dpp_i<0x118>(v));
+    v = max(v, dpp_i<0x142, 0xa>(v));
+    v = max(v, dpp_i<0x143, 0xc>(v));
+    return v;
+}
 
 // first i with end[i] > x (n if none): the request that item x belongs to
 __device__ __forceinline__ int owner_of(const int *end, int n, int x) {
@@ -89,80 +102,92 @@ __device__ __forceinline__ int owner_of(const int *end, int n, int x) {
 
 __global__ void __launch_bounds__(kNT) kv_pages_kernel(KvPagesArgs a) {
     extern __shared__ int lds[];                       // three running sums of batch entries
-    __shared__ int sum_need[kWaves], sum_give[kWaves], most[kWaves], refusals;
+    __shared__ int sum_need[kWaves], sum_give[kWaves], most[kWaves], refusals[kWaves];
     __shared__ int64_t sum_grow[kWaves];
-    int *tok_end = lds, *take_end = lds + a.batch, *give_end = take_end + a.batch;
+    int *tok_end = lds, *need_end = lds + a.batch, *give_end = need_end + a.batch;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const Pages pages((uint32_t)a.page_size);
     const int total = a.n_pages;
-    int head = a.ring[0] % total;
-    head += head < 0 ? total : 0;
-    const int free = min(max(a.ring[1], 0), total);
     const bool first = blockIdx.x == 0;
 
     // a thread's requests [r0, r1), their sums, and the sums before them
     const int mine = (a.batch + kNT - 1) / kNT, r0 = tid * mine, r1 = min(r0 + mine, a.batch);
+    int lo[kKeep], hi[kKeep];                          // their lengths, where they are few
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+        const int r = min(r0 + i, a.batch - 1);
+        lo[i] = max(a.len_old[r], 0);
+        hi[i] = max(a.len_new[r], 0);
+    }
+    int head = a.ring[0];
+    const int free = min(max(a.ring[1], 0), total);
+    if (head < 0 || head >= total) {
+        head %= total;
+        head += head < 0 ? total : 0;
+    }
+    auto each = [&](auto f) {
+        if (mine <= kKeep) {
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i)
+                if (r0 + i < r1) f(r0 + i, lo[i], hi[i], need_of(a, pages, lo[i], hi[i]));
+        } else {
+            for (int r = r0; r < r1; ++r) {
+                const int l = max(a.len_old[r], 0), h = max(a.len_new[r], 0);
+                f(r, l, h, need_of(a, pages, l, h));
+            }
+        }
+    };
     int need = 0, give = 0;                            // below 2^31: at most batch * max_pages
     int64_t grow = 0;
-    for (int r = r0; r < r1; ++r) {
-        const Need n = need_of(a, pages, r);
+    each([&](int, int, int, const Need &n) {
         need += n.take();
         give += n.give();
         grow += n.grow;
-    }
+    });
     int need_upto = wave_scan(need), give_upto = wave_scan(give);
     int64_t grow_upto = wave_scan(grow);
     if (lane == 63) { sum_need[wave] = need_upto; sum_give[wave] = give_upto; sum_grow[wave] = grow_upto; }
-    if (tid == 0) refusals = 0;
     __syncthreads();
     need_upto -= need; give_upto -= give; grow_upto -= grow;
-    int needed = 0, given = 0;
+    int given = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
         if (w < wave) { need_upto += sum_need[w]; give_upto += sum_give[w]; grow_upto += sum_grow[w]; }
-        needed += sum_need[w];
         given += sum_give[w];
     }
-    int taken = needed;
-    if (needed > free) {                               // the same in the whole block: some are refused
-        int top = 0, upto = need_upto;
-        for (int r = r0; r < r1; ++r) {
-            upto += need_of(a, pages, r).take();
-            top = upto <= free ? upto : top;
-        }
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) top = max(top, __shfl_xor(top, o));
-        if (lane == 0) most[wave] = top;
-        __syncthreads();
-        taken = 0;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) taken = max(taken, most[w]);
-    }
-    int denied = 0;
-    for (int r = r0; r < r1; ++r) {
-        const Need n = need_of(a, pages, r);
+    int top = 0, denied = 0;                           // the largest need up to a request that is covered
+    each([&](int r, int l, int h, const Need &n) {
         need_upto += n.take();
         give_upto += n.give();
         grow_upto += n.grow;
         const int e = (int)min(grow_upto, (int64_t)0x7fffffff);
         tok_end[r] = e;
-        take_end[r] = min(need_upto, taken);
+        need_end[r] = need_upto;
         give_end[r] = give_upto;
+        top = need_upto <= free ? need_upto : top;
         if (first) {
             const bool refused = n.over || (n.take() > 0 && need_upto > free);
             denied += refused;
-            a.len_out[r] = max(refused ? a.len_old[r] : a.len_new[r], 0);
+            a.len_out[r] = refused ? l : h;
             a.starts[r + 1] = e;
         }
-    }
-    if (first && denied > 0) atomicAdd(&refusals, denied);
+    });
+    top = wave_max(top);
+    denied = wave_scan(denied);
+    if (lane == 63) { most[wave] = top; refusals[wave] = denied; }
     __syncthreads();
+    int taken = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) taken = max(taken, most[w]);
     given = min(given, total - free);                  // no more than the ring has places for
     if (first && tid == 0) {
         a.starts[0] = 0;
         a.ring_out[0] = wrap((uint32_t)head + taken, total);
         a.ring_out[1] = free - taken + given;
-        a.denied[0] = refusals;
+        int d = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) d += refusals[w];
+        a.denied[0] = d;
     }
     const int tokens = tok_end[a.batch - 1];
     const int step = (int)gridDim.x * kNT, me = (int)blockIdx.x * kNT + tid;
@@ -185,11 +210,11 @@ __global__ void __launch_bounds__(kNT) kv_pages_kernel(KvPagesArgs a) {
                     const Need n = need_of(a, pages, r);
                     end = tok_end[r];
                     start = r > 0 ? tok_end[r - 1] : 0;
-                    from = r > 0 ? take_end[r - 1] : 0;
+                    from = r > 0 ? min(need_end[r - 1], taken) : 0;
                     old = max(a.len_old[r], 0);
                     have = n.have;
                     // one that wants more pages than it holds and takes none was refused
-                    granted = n.want <= n.have || take_end[r] > from;
+                    granted = n.want <= n.have || min(need_end[r], taken) > from;
                     table = a.block_table + r * a.table_stride;
                 }
             }
@@ -219,9 +244,9 @@ __global__ void __launch_bounds__(kNT) kv_pages_kernel(KvPagesArgs a) {
     // pages taken, into the table (by the last threads first: where there is little to do,
     // these moves and the tokens are at work at the same time)
     for (int j = step - 1 - me; j < taken; j += step) {
-        const int r = owner_of(take_end, a.batch, j);
+        const int r = owner_of(need_end, a.batch, j);
         const Need n = need_of(a, pages, r);
-        const int c = n.have + j - (r > 0 ? take_end[r - 1] : 0);
+        const int c = n.have + j - (r > 0 ? need_end[r - 1] : 0);
         a.block_table[r * a.table_stride + c] = a.free_ring[wrap((uint32_t)head + j, total)];
     }
     // pages given back, behind the ring's last entry

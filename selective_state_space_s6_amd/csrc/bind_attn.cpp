@@ -118,6 +118,8 @@ struct Call {
         }
         return r;
     }
+    // few enough bytes that outputs which stay alive do not hold much of each other's memory
+    static bool few(int64_t elements) { return elements <= (1 << 18); }
     Tensor workspace(PyObject *o, size_t need) const {
         if (o == Py_None) return make(ScalarType::Byte, {(int64_t)need});
         const Tensor &t = tensor(o, "workspace");
@@ -272,8 +274,13 @@ PyObject *rope_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const float eps = number(a[6], "eps");
         const uint32_t flags = (uint32_t)whole_number(a[7], "flags");
         const Rope r(a, flags);
-        const Tensor qo = r.c.out(a[8], "q_out", r.type, {r.T, r.H, r.d});
-        const Tensor ko = a[1] != Py_None ? r.c.out(a[9], "k_out", r.type, {r.T, r.Hk, r.d}) : Tensor();
+        Tensor qo, ko;
+        if (a[1] != Py_None && a[8] == Py_None && a[9] == Py_None && r.c.few(r.T * (r.H + r.Hk) * r.d)) {
+            std::tie(qo, ko) = std::tuple_cat(r.c.make_together<2>({{r.type, {r.T, r.H, r.d}}, {r.type, {r.T, r.Hk, r.d}}}));
+        } else {
+            qo = r.c.out(a[8], "q_out", r.type, {r.T, r.H, r.d});
+            if (a[1] != Py_None) ko = r.c.out(a[9], "k_out", r.type, {r.T, r.Hk, r.d});
+        }
         const int rc = ssm_qk_norm_rope_fwd(r.q, r.k, r.wq, r.wk, r.inv_freq, r.positions, qo.data_ptr(),
                                             ko.defined() ? ko.data_ptr() : nullptr, r.T, r.H, r.Hk, r.d, r.rot, r.q_st, r.q_sh,
                                             r.k_st, r.k_sh, eps, r.dtype, flags, r.c.stream());
@@ -295,17 +302,27 @@ PyObject *rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
             pgk = r.c.view(gk, "dk_out", r.type, {r.T, r.Hk, r.d});
             gk_st = gk.stride(0); gk_sh = gk.stride(1);
         }
-        const Tensor dq = r.c.out(a[10], "dq", r.type, {r.T, r.H, r.d});
-        const Tensor dk = has_k ? r.c.out(a[11], "dk", r.type, {r.T, r.Hk, r.d}) : Tensor();
-        Tensor dwq, dwk;
-        if (r.norm && has_k && a[12] == Py_None && a[13] == Py_None) {
-            const auto f32 = ScalarType::Float;
-            std::tie(dwq, dwk) = std::tuple_cat(r.c.make_together<2>({{f32, {r.d}}, {f32, {r.d}}}));
-        } else if (r.norm) {
-            dwq = r.c.out(a[12], "dwq", ScalarType::Float, {r.d});
-            if (has_k) dwk = r.c.out(a[13], "dwk", ScalarType::Float, {r.d});
+        const size_t need = ssm_qk_norm_rope_bwd_workspace_size(r.T, r.H, r.Hk, r.d, flags);
+        const auto f32 = ScalarType::Float;
+        Tensor dq, dk, dwq, dwk, ws;
+        bool given = !has_k || !r.norm;
+        for (int i = 10; i < 15; ++i) given = given || a[i] != Py_None;
+        if (!given && r.c.few(r.T * (r.H + r.Hk) * r.d)) {
+            // (of few tokens the workspace is a part of the outputs' size)
+            std::tie(dq, dk, dwq, dwk, ws) = std::tuple_cat(
+                r.c.make_together<5>({{r.type, {r.T, r.H, r.d}}, {r.type, {r.T, r.Hk, r.d}}, {f32, {r.d}}, {f32, {r.d}},
+                                      {ScalarType::Byte, {(int64_t)need}}}));
+        } else {
+            dq = r.c.out(a[10], "dq", r.type, {r.T, r.H, r.d});
+            if (has_k) dk = r.c.out(a[11], "dk", r.type, {r.T, r.Hk, r.d});
+            if (r.norm && has_k && a[12] == Py_None && a[13] == Py_None) {
+                std::tie(dwq, dwk) = std::tuple_cat(r.c.make_together<2>({{f32, {r.d}}, {f32, {r.d}}}));
+            } else if (r.norm) {
+                dwq = r.c.out(a[12], "dwq", f32, {r.d});
+                if (has_k) dwk = r.c.out(a[13], "dwk", f32, {r.d});
+            }
+            ws = r.c.workspace(a[14], need);
         }
-        const Tensor ws = r.c.workspace(a[14], ssm_qk_norm_rope_bwd_workspace_size(r.T, r.H, r.Hk, r.d, flags));
         auto at_ = [](const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
         const int rc = ssm_qk_norm_rope_bwd(r.q, r.k, r.wq, r.wk, r.inv_freq, r.positions, pgq, pgk, at_(dq), at_(dk),
                                             (float *)at_(dwq), (float *)at_(dwk), r.T, r.H, r.Hk, r.d, r.rot, r.q_st, r.q_sh,

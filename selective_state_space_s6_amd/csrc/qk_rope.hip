@@ -739,13 +739,27 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
         Side &s = k.side[i];
         s.x = x; s.dy = dy; s.y = y; s.w = w; s.st = st; s.sh = sh; s.dst = dst; s.dsh = dsh;
         s.heads = (int)heads; s.rotate = true;
-        set_work(s, k, a.n_tokens, a.n_heads + a.n_kv_heads, waves, kBwdBlocks);
+    };
+    // steps of a wave, where the sides have `blocks` blocks together, and one each at least
+    auto deal = [&](int blocks) {
+        int64_t most = 0;
+        for (int i = 0; i < (has_k ? 2 : 1); ++i) {
+            Side &s = k.side[i];
+            set_work(s, k, a.n_tokens, a.n_heads + a.n_kv_heads, waves, blocks);
+            if (s.blocks > 0) most = std::max(most, (s.parts + s.stride - 1) / s.stride * s.each);
+        }
+        return most;
     };
     side(0, a.q, a.dq_out, a.dq, a.wq, a.q_st, a.q_sh, a.dq_st, a.dq_sh, a.n_heads);
     if (has_k) side(1, a.k, a.dk_out, a.dk, a.wk, a.k_st, a.k_sh, a.dk_st, a.dk_sh, a.n_kv_heads);
+    // Few heads: a block a side, whose share of dw is dw, and no second launch.  (16 + 4 heads of 128,
+    // us a call in one launch and in two: 8 bf16 tokens, 2 steps 7.8 and 10.5, 8 fp32 ones, 4 steps 8.6 and 11.4;
+    // 16 bf16 tokens, 4 steps 10.2 and 10.6; 32, 8 steps 16.2 and 10.5.)
+    const bool one = norm && a.n_tokens > 0 && deal(1) <= 4;
+    if (!one) deal(kBwdBlocks);
     float *ws = (float *)a.workspace;
-    k.side[0].part = ws;
-    k.side[1].part = norm ? ws + (int64_t)k.side[0].blocks * a.headdim : nullptr;
+    k.side[0].part = one ? a.dwq : ws;
+    k.side[1].part = one ? a.dwk : norm ? ws + (int64_t)k.side[0].blocks * a.headdim : nullptr;
     const size_t lds = std::max(table_bytes(k, waves), norm ? (size_t)waves * a.headdim * sizeof(float) : 0);
     const unsigned blocks = (unsigned)(k.side[0].blocks + k.side[1].blocks);
     const bool il = (a.flags & SSM_ROPE_INTERLEAVED) != 0;
@@ -766,7 +780,7 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
     }
 #undef SSM_BWD
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !norm) return e;
+    if (e != hipSuccess || !norm || one) return e;
     *kernel_name = "qk_rope_dw_kernel";
     hipLaunchKernelGGL(qk_rope_dw_kernel, dim3((unsigned)((a.headdim + 7) / 8), has_k ? 2 : 1), dim3(256), 0, stream,
                        k.side[0].part, k.side[1].part, a.dwq, a.dwk, k.side[0].blocks, k.side[1].blocks, a.headdim);

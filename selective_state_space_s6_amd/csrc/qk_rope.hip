@@ -33,8 +33,12 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kCUs = 256;
-constexpr int kFwdWaves = 4;        // waves of a block, forward: 4 on each SIMD of 4 blocks
-constexpr int kFwdBlocks = 4 * kCUs;
+constexpr int kFwdWaves = 4;        // waves of a block, forward: one on each SIMD
+// Forward: blocks of a compute unit, as many as registers let run at once: 16 elements a lane take 115
+// of them, 8 take 78 in bf16 and up to 87 in fp32 or with a cache, 2 up to 83.  (10000 bf16 tokens of 16 + 4 heads
+// of 128 with 24 turned, 8 elements a lane, on 4, 5 and 6 blocks: 22.5, 20.8, 20.3 us; into a cache 31.8, 28.7, 31.5;
+// fp32, all turned: 40.3, 38.8, 45.5.)
+constexpr int fwd_blocks(int esize, int v, bool cache) { return v == 8 ? 4 : esize == 2 && !cache ? 6 : 5; }
 // Backward: one block on a compute unit, so that few shares of dw are joined after it, with
 // the waves that its registers let run at once, 3 or 4 on a SIMD, by the bytes of one of a
 // lane's loads: 16 bf16 elements a lane take 150 registers, 8 take 102.  8 fp32 elements take
@@ -365,7 +369,7 @@ __device__ __forceinline__ void turn(float *x, const float *cs, const float *sn)
 }
 
 template <typename T, int V, bool IL, int KV>      // KV: 0 no cache, 1 a cache of type T, 2 an 8-bit cache
-__global__ void __launch_bounds__(kFwdWaves * 64, 4) qk_rope_kernel(Kp a) {
+__global__ void __launch_bounds__(kFwdWaves * 64, fwd_blocks(sizeof(T), V, KV != 0)) qk_rope_kernel(Kp a) {
     typedef Lane<T, V, IL> L;
     constexpr int NU = L::NU;
     extern __shared__ float tab[];
@@ -694,7 +698,8 @@ hipError_t launch_qk_rope(const QkRopeArgs &a, hipStream_t stream, const char **
         Side &s = k.side[i];
         s.x = x; s.y = y; s.w = w; s.st = st; s.sh = sh;
         s.heads = (int)heads; s.rotate = rotate; s.cache = to_cache;
-        set_work(s, k, a.n_tokens, a.n_heads + (cache ? 2 : 1) * a.n_kv_heads, kFwdWaves, kFwdBlocks);
+        set_work(s, k, a.n_tokens, a.n_heads + (cache ? 2 : 1) * a.n_kv_heads, kFwdWaves,
+                 kCUs * fwd_blocks(esize, v, cache));
     };
     side(0, a.q, a.q_out, a.wq, a.q_st, a.q_sh, a.n_heads, true, false);
     if (a.n_kv_heads > 0) side(1, a.k, a.k_out, a.wk, a.k_st, a.k_sh, a.n_kv_heads, true, cache);

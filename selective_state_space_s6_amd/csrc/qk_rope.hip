@@ -14,10 +14,10 @@
 // pair are its own, and only the norm's sums cross lanes.  The next heads' elements are
 // asked for before the present ones are worked on, and no wave waits for another.
 //
-// Measured, kernels alone, 16384 tokens of 16 + 4 heads of 128 in bf16: forward 168 MB 41 us (4.1
-// TB/s; the same kernel without norm and rotation 35, a strided copy 35 to 37), backward 252
-// MB 60 us (4.2 TB/s) and 4.7 us to join dw.  8192 tokens of 32 + 8 + 8 heads into an 8-bit cache
-// 185 MB 47 us.  64 tokens into a cache 4.3 us, 1021 fp32 tokens of 6 + 3 heads of 72 5.0 us:
+// Measured, kernels alone, 16384 tokens of 16 + 4 heads of 128 in bf16: forward 168 MB 38 to 41 us (4.1
+// to 4.4 TB/s; the same kernel without norm and rotation 35, a strided copy 35 to 37), backward 252
+// MB 57 us (4.4 TB/s) and 4.8 us to join dw.  8192 tokens of 32 + 8 + 8 heads into an 8-bit cache
+// 185 MB 44 us.  64 tokens into a cache 4.5 us, 1021 fp32 tokens of 6 + 3 heads of 72 5.1 us:
 // a chain of loads.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -34,11 +34,12 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kCUs = 256;
 constexpr int kFwdWaves = 4;        // waves of a block, forward: one on each SIMD
-// Forward: blocks of a compute unit, as many as registers let run at once: 16 elements a lane take 115
-// of them, 8 take 78 in bf16 and up to 87 in fp32 or with a cache, 2 up to 83.  (10000 bf16 tokens of 16 + 4 heads
-// of 128 with 24 turned, 8 elements a lane, on 4, 5 and 6 blocks: 22.5, 20.8, 20.3 us; into a cache 31.8, 28.7, 31.5;
-// fp32, all turned: 40.3, 38.8, 45.5.)
-constexpr int fwd_blocks(int esize, int v, bool cache) { return v == 8 ? 4 : esize == 2 && !cache ? 6 : 5; }
+// Forward: blocks of a compute unit, as many as registers let run at once: bf16 lanes take up to 80 of
+// them, fp32 ones up to 87 (on 6 blocks they spill: 16k tokens of 16 + 4 heads of 128 into a cache 84.1 us on
+// 5, 90.5 on 6).  16 bf16 elements a lane instead of 8, which leave room for 4 blocks, move 16k tokens of 16 + 4
+// heads of 128 in 37.5 us against 34.0, of 4 + 1 heads of 256 in 21.9 against 21.0, into a bf16 cache in 45.1 against
+// 39.1 and 26.1 against 24.1; only of 32 + 8 heads in 73.0 against 74.5.
+constexpr int fwd_blocks(int esize) { return esize == 2 ? 6 : 5; }
 // Backward: one block on a compute unit, so that few shares of dw are joined after it, with
 // the waves that its registers let run at once, 3 or 4 on a SIMD, by the bytes of one of a
 // lane's loads: 16 bf16 elements a lane take 150 registers, 8 take 102.  8 fp32 elements take
@@ -95,22 +96,17 @@ template <> struct Row<uint16_t, 1> {
 // rounded once.  The comparisons leave a NaN as it is.
 template <int V>
 __device__ __forceinline__ void st_f8(uint8_t *p, const float *v, float scale) {
-    float c[V < 4 ? 4 : V];
+    float c[4];
 #pragma unroll
-    for (int i = 0; i < (V < 4 ? 4 : V); ++i) {
+    for (int i = 0; i < 4; ++i) {
         const float x = i < V ? v[i] / scale : 0.0f;
         const float y = x > 448.0f ? 448.0f : x;
         c[i] = y < -448.0f ? -448.0f : y;
     }
-    uint32_t w[V < 4 ? 1 : V / 4];
-#pragma unroll
-    for (int i = 0; i < (V < 4 ? 1 : V / 4); ++i) {
-        int u = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i], c[4 * i + 1], 0, false);
-        w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i + 2], c[4 * i + 3], u, true);
-    }
-    if constexpr (V == 8) *(uint2 *)p = make_uint2(w[0], w[1]);
-    else if constexpr (V == 4) *(uint32_t *)p = w[0];
-    else *p = (uint8_t)w[0];
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+    const uint32_t w = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], lo, true);
+    if constexpr (V == 4) *(uint32_t *)p = w;
+    else *p = (uint8_t)w;
 }
 
 // cos and sin of position * inv_freq.  The angle is formed and reduced in fp64, as turns:
@@ -369,7 +365,7 @@ __device__ __forceinline__ void turn(float *x, const float *cs, const float *sn)
 }
 
 template <typename T, int V, bool IL, int KV>      // KV: 0 no cache, 1 a cache of type T, 2 an 8-bit cache
-__global__ void __launch_bounds__(kFwdWaves * 64, fwd_blocks(sizeof(T), V, KV != 0)) qk_rope_kernel(Kp a) {
+__global__ void __launch_bounds__(kFwdWaves * 64, fwd_blocks(sizeof(T))) qk_rope_kernel(Kp a) {
     typedef Lane<T, V, IL> L;
     constexpr int NU = L::NU;
     extern __shared__ float tab[];
@@ -588,13 +584,12 @@ __global__ void __launch_bounds__(256) qk_rope_dw_kernel(const float *pq, const 
 }
 
 // ------------------------------------------------------------------ host ----
-// Widest V whose unit of 2 V elements fits the rotation's halves, what follows it, and
-// every address: 16 bytes where possible.  V = 1 fits everything.  (Forward, bf16, V = 8 against 4:
-// 16k tokens of 16 + 4 heads of 128 39.9 and 42.4 us, of 64 19.7 and 21.8, 8k of 256 33.5 and 39.8.)
-int pick_v(const void *const *ptr, const int64_t *stride, int np, int ns, int d, int rot, int esize,
+// Widest V up to `most` whose unit of 2 V elements fits the rotation's halves, what follows it, and
+// every address.  V = 1 fits everything.
+int pick_v(int most, const void *const *ptr, const int64_t *stride, int np, int ns, int d, int rot, int esize,
            const float *wq, const float *wk) {
     if ((((uintptr_t)wq | (uintptr_t)wk) & 15) != 0) return 1;     // weights are loaded by fours
-    for (int v = 16 / esize; v >= 4; v >>= 1) {
+    for (int v = most; v >= 4; v >>= 1) {
         bool ok = (rot / 2) % v == 0 && (d - rot) % (2 * v) == 0;
         for (int i = 0; i < np; ++i) ok &= ((uintptr_t)ptr[i] & (uintptr_t)(v * esize - 1)) == 0;
         for (int i = 0; i < ns; ++i) ok &= stride[i] % v == 0;
@@ -658,8 +653,7 @@ void fwd_go(const Kp &k, unsigned blocks, size_t lds, bool il, hipStream_t strea
 template <int KV>
 void fwd_type(const Kp &k, unsigned blocks, size_t lds, bool bf16, int v, bool il, hipStream_t stream) {
     if (bf16) {
-        if (v == 8) fwd_go<uint16_t, 8, KV>(k, blocks, lds, il, stream);
-        else if (v == 4) fwd_go<uint16_t, 4, KV>(k, blocks, lds, il, stream);
+        if (v == 4) fwd_go<uint16_t, 4, KV>(k, blocks, lds, il, stream);
         else fwd_go<uint16_t, 1, KV>(k, blocks, lds, il, stream);
     } else if constexpr (KV != 2) {
         if (v == 4) fwd_go<float, 4, KV>(k, blocks, lds, il, stream);
@@ -675,17 +669,15 @@ hipError_t launch_qk_rope(const QkRopeArgs &a, hipStream_t stream, const char **
     const int esize = a.bf16 ? 2 : 4;
     const void *ptr[] = {a.q, a.q_out, a.k, a.k_out, a.v};
     const int64_t stride[] = {a.q_st, a.q_sh, a.k_st, a.k_sh, a.v_st, a.v_sh, (int64_t)a.headdim};
-    int v = pick_v(ptr, stride, cache ? 5 : a.n_kv_heads > 0 ? 4 : 2, 7, a.headdim, a.rot_dim, esize, a.wq, a.wk);
+    int v = pick_v(4, ptr, stride, cache ? 5 : a.n_kv_heads > 0 ? 4 : 2, 7, a.headdim, a.rot_dim, esize, a.wq, a.wk);
     if (cache) {   // the cache's own addresses: V elements of 1, 2 or 4 bytes
         const void *cp[] = {a.k_out, a.v_cache};
         const int64_t cs[] = {a.c_sp, a.c_st, a.c_sh};
         const int ce = f8 ? 1 : esize;
-        for (; v > 1; v = v > 4 ? v / 2 : 1) {
-            bool ok = (a.rot_dim / 2) % v == 0 && (a.headdim - a.rot_dim) % (2 * v) == 0;
-            for (const void *p : cp) ok &= ((uintptr_t)p & (uintptr_t)(v * ce - 1)) == 0;
-            for (int64_t st : cs) ok &= st % v == 0;
-            if (ok) break;
-        }
+        bool ok = true;
+        for (const void *p : cp) ok &= ((uintptr_t)p & (uintptr_t)(v * ce - 1)) == 0;
+        for (int64_t st : cs) ok &= st % v == 0;
+        if (!ok) v = 1;
     }
     Kp k = {};
     set_geometry(k, v, a.headdim, a.rot_dim);
@@ -699,7 +691,7 @@ hipError_t launch_qk_rope(const QkRopeArgs &a, hipStream_t stream, const char **
         s.x = x; s.y = y; s.w = w; s.st = st; s.sh = sh;
         s.heads = (int)heads; s.rotate = rotate; s.cache = to_cache;
         set_work(s, k, a.n_tokens, a.n_heads + (cache ? 2 : 1) * a.n_kv_heads, kFwdWaves,
-                 kCUs * fwd_blocks(esize, v, cache));
+                 kCUs * fwd_blocks(esize));
     };
     side(0, a.q, a.q_out, a.wq, a.q_st, a.q_sh, a.n_heads, true, false);
     if (a.n_kv_heads > 0) side(1, a.k, a.k_out, a.wk, a.k_st, a.k_sh, a.n_kv_heads, true, cache);
@@ -729,11 +721,11 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
     const void *ptr[] = {a.q, a.dq_out, a.dq, a.k, a.dk_out, a.dk};
     const int64_t stride[] = {a.q_st, a.q_sh, a.dq_st, a.dq_sh, (int64_t)a.headdim, a.k_st, a.k_sh, a.dk_st, a.dk_sh};
     const bool has_k = a.n_kv_heads > 0, norm = (a.flags & SSM_QK_NO_NORM) == 0;
-    int v = pick_v(ptr, stride, has_k ? 6 : 3, has_k ? 9 : 5, a.headdim, a.rot_dim, esize, a.wq, a.wk);
     // 8 elements a lane save instructions and cost a quarter of the waves (150 registers against
     // 102): 16k tokens of 16 + 4 heads of 128 67 us against 63 with 4, of 64 + 8 heads the same;
     // 8k tokens of heads of 256 55 against 63
-    if (v == 8 && a.headdim <= 128) v = 4;
+    const int most = a.bf16 && a.headdim > 128 ? 8 : 4;
+    const int v = pick_v(most, ptr, stride, has_k ? 6 : 3, has_k ? 9 : 5, a.headdim, a.rot_dim, esize, a.wq, a.wk);
     const int waves = bwd_waves(v * esize);
     Kp k = {};
     set_geometry(k, v, a.headdim, a.rot_dim);

@@ -34,19 +34,18 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kCUs = 256;
 constexpr int kFwdWaves = 4;        // waves of a block, forward: one on each SIMD
-// Forward: blocks of a compute unit, as many as registers let run at once: bf16 lanes take up to 80 of
-// them, fp32 ones up to 87 (on 6 blocks they spill: 16k tokens of 16 + 4 heads of 128 into a cache 84.1 us on
-// 5, 90.5 on 6).  16 bf16 elements a lane instead of 8, which leave room for 4 blocks, move 16k tokens of 16 + 4
-// heads of 128 in 37.5 us against 34.0, of 4 + 1 heads of 256 in 21.9 against 21.0, into a bf16 cache in 45.1 against
-// 39.1 and 26.1 against 24.1; only of 32 + 8 heads in 73.0 against 74.5.
-constexpr int fwd_blocks(int esize) { return esize == 2 ? 6 : 5; }
-// Backward: one block on a compute unit, so that few shares of dw are joined after it, with
-// the waves that its registers let run at once, 3 or 4 on a SIMD, by the bytes of one of a
-// lane's loads: 16 bf16 elements a lane take 150 registers, 8 take 102.  8 fp32 elements take
-// 118, which 4 waves would fit, but run faster on 3 (8k tokens of 16 + 4 heads of 128: 50.5
-// against 54.8 us).
-constexpr int bwd_waves(int bytes) { return bytes == 16 ? 12 : 16; }
-constexpr int kBwdBlocks = kCUs;
+// Forward: blocks of a compute unit, as many as registers let run at once: up to 66 of them without a
+// cache in bf16, 79 in fp32, 80 with a cache.  (16k tokens of 16 + 4 heads of 128, us: bf16 on 6, 7 and 8 blocks, where
+// they spill, 34.6, 33.9, 36.1; fp32 on 5, 6 and 8 71.2, 69.9, 77.5; into an 8-bit cache on 6, 7 and 8 42.5, 51.6, 59.6.
+// 16 bf16 elements a lane in place of 8, which leave room for 4 blocks: 37.5.)
+constexpr int fwd_blocks(int esize, bool cache) { return esize == 2 && !cache ? 7 : 6; }
+// Backward: up to 110 registers, 4 waves on a SIMD, in two blocks of 8: one block of 16 starts and ends
+// together and leaves half the shares of dw (16k tokens of 16 + 4 heads of 128, bf16 60.6 against 57.8 us, fp32 111.5
+// against 106.6), blocks of 4 leave twice as many (4k tokens 20.7 against 20.4 us).  16 bf16 elements a
+// lane take 149 registers and 3 waves (16k tokens of 8 + 2 heads of 256 67.5 against 58.6 us, of 8 + 8 heads of 192
+// 68.7 against 73.5).
+constexpr int kBwdWaves = 8;
+constexpr int kBwdBlocks = 2 * kCUs;
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const bf16x2 r = __builtin_convertvector((f32x2){a, b}, bf16x2);   // to nearest even
@@ -66,16 +65,6 @@ template <> struct Row<float, 1> {
     typedef float Raw;
     __device__ __forceinline__ static void get(Raw u, float *v) { v[0] = u; }
     __device__ __forceinline__ static void st(float *p, const float *v) { *p = v[0]; }
-};
-template <> struct Row<uint16_t, 8> {
-    typedef uint4 Raw;
-    __device__ __forceinline__ static void get(Raw u, float *v) {
-        v[0] = lo_f(u.x); v[1] = hi_f(u.x); v[2] = lo_f(u.y); v[3] = hi_f(u.y);
-        v[4] = lo_f(u.z); v[5] = hi_f(u.z); v[6] = lo_f(u.w); v[7] = hi_f(u.w);
-    }
-    __device__ __forceinline__ static void st(uint16_t *p, const float *v) {
-        *(uint4 *)p = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    }
 };
 template <> struct Row<uint16_t, 4> {
     typedef uint2 Raw;
@@ -209,7 +198,7 @@ template <typename T, int V, bool IL> struct Lane {
     float *tab;                                  // this wave's part of LDS: cosines, then sines
     int lane, half, tok, head;                   // token of the group, head of the first pass
     Unit un[NU];
-    double turns[2];                             // of angles lane and lane + 64 where the group is one token
+    float freq[2];                               // of angles lane and lane + 64 where the group is one token
     float cs[NU][V], sn[NU][V];
 
     __device__ __forceinline__ Lane(const Kp &a_, const Side &s_, float *tab_) : a(a_), s(s_), tab(tab_) {
@@ -232,23 +221,20 @@ template <typename T, int V, bool IL> struct Lane {
     // loads that the first elements need not wait for
     __device__ __forceinline__ void frequencies() {
         if (half == 0) return;
-        float f[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) f[k] = a.inv_freq[min(lane + 64 * k, half - 1)];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) turns[k] = (double)f[k] * kTurn;
+        for (int k = 0; k < 2; ++k) freq[k] = a.inv_freq[min(lane + 64 * k, half - 1)];
     }
     // token and head of a pass; on: there is such a one
-    struct At { int64_t t; int h, on; };
+    struct At { int t, h; bool on; };
     __device__ __forceinline__ At at(int64_t group, int pass) const {
         At p;
-        p.t = group * s.tokens + tok;
+        p.t = (int)group * s.tokens + tok;
         p.h = head + pass * (64 >> a.lg);
         p.on = tok < s.tokens && p.t < a.n_tokens && p.h < s.heads;
         return p;
     }
     __device__ __forceinline__ void load(Raw (*r)[2], const void *x, int64_t st, int64_t sh, const At &p) const {
-        const T *xp = (const T *)x + p.t * st + p.h * sh;
+        const T *xp = (const T *)x + (int64_t)p.t * st + (int64_t)p.h * sh;
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
             r[n][0] = Raw{};
@@ -270,7 +256,7 @@ template <typename T, int V, bool IL> struct Lane {
 #pragma unroll
             for (int k = 0; k < 2; ++k)
                 if (lane + 64 * k < n) {
-                    const float2 v = cos_sin(pos, turns[k]);
+                    const float2 v = cos_sin(pos, (double)freq[k] * kTurn);
                     tab[lane + 64 * k] = v.x;
                     tab[n + lane + 64 * k] = v.y;
                 }
@@ -365,7 +351,7 @@ __device__ __forceinline__ void turn(float *x, const float *cs, const float *sn)
 }
 
 template <typename T, int V, bool IL, int KV>      // KV: 0 no cache, 1 a cache of type T, 2 an 8-bit cache
-__global__ void __launch_bounds__(kFwdWaves * 64, fwd_blocks(sizeof(T))) qk_rope_kernel(Kp a) {
+__global__ void __launch_bounds__(kFwdWaves * 64, fwd_blocks(sizeof(T), KV != 0)) qk_rope_kernel(Kp a) {
     typedef Lane<T, V, IL> L;
     constexpr int NU = L::NU;
     extern __shared__ float tab[];
@@ -389,16 +375,18 @@ __global__ void __launch_bounds__(kFwdWaves * 64, fwd_blocks(sizeof(T))) qk_rope
     while (true) {
         // what comes next is asked for first
         const bool new_group = turn_group;
+        const int64_t group = at.group;
+        const int pass_now = pass;
         turn_group = pass + 1 >= at.pass1;
         const bool more = turn_group ? at.next(s) : true;
-        const int pass_n = turn_group ? at.pass0 : pass + 1;
-        typename L::At p_n = p;
+        pass = turn_group ? at.pass0 : pass + 1;
         int pos_n = 0;
         if (more) {
-            p_n = me.at(at.group, pass_n);
+            const typename L::At p_n = me.at(at.group, pass);
             me.load(ahead, s.x, s.st, s.sh, p_n);
             if (turn_group && s.rotate) pos_n = me.position(p_n);
         }
+        p = me.at(group, pass_now);
         int64_t slot = 0;
         if (KV != 0 && s.cache && p.on) slot = a.slots[p.t];
         if (s.rotate && new_group) me.angles(pos);
@@ -418,8 +406,8 @@ __global__ void __launch_bounds__(kFwdWaves * 64, fwd_blocks(sizeof(T))) qk_rope
 #pragma unroll
                 for (int i = 0; i < 2 * V; ++i) x[n][i] = x[n][i] * r * w[n][i];
         }
-        int64_t row = (p.t * s.heads + p.h) * a.d;
-        bool keep = p.on != 0;
+        int64_t row = ((int64_t)p.t * s.heads + p.h) * a.d;
+        bool keep = p.on;
         if (KV != 0 && s.cache) {
             keep = keep && slot >= 0 && slot < (int64_t)a.n_slots;
             const uint32_t sl = keep ? (uint32_t)slot : 0u, page = sl / a.page_size;
@@ -440,8 +428,6 @@ __global__ void __launch_bounds__(kFwdWaves * 64, fwd_blocks(sizeof(T))) qk_rope
             }
         }
         if (!more) break;
-        p = p_n;
-        pass = pass_n;
         if (turn_group) pos = pos_n;
 #pragma unroll
         for (int n = 0; n < NU; ++n) { raw[n][0] = ahead[n][0]; raw[n][1] = ahead[n][1]; }
@@ -452,8 +438,7 @@ __global__ void __launch_bounds__(kFwdWaves * 64, fwd_blocks(sizeof(T))) qk_rope
 // in every head); the shares of its lane groups are joined across lanes at the end, those of
 // the block's waves in LDS.
 template <typename T, int V, bool IL>
-__global__ void __launch_bounds__(bwd_waves(V * sizeof(T)) * 64, bwd_waves(V * sizeof(T)) / 4) qk_rope_bwd_kernel(Kp a) {
-    constexpr int WAVES = bwd_waves(V * sizeof(T));
+__global__ void __launch_bounds__(kBwdWaves * 64, 4) qk_rope_bwd_kernel(Kp a) {
     typedef Lane<T, V, IL> L;
     constexpr int NU = L::NU;
     extern __shared__ float tab[];
@@ -466,7 +451,7 @@ __global__ void __launch_bounds__(bwd_waves(V * sizeof(T)) * 64, bwd_waves(V * s
     for (int n = 0; n < NU; ++n)
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) dw[n][i] = 0.0f;
-    Walk at(s, (uint32_t)(blk * WAVES + wave));
+    Walk at(s, (uint32_t)(blk * kBwdWaves + wave));
     if (at.part < s.parts) {
         int pass = at.pass0;
         typename L::Raw raw[NU][2], raw_g[NU][2], ahead[NU][2], ahead_g[NU][2];
@@ -479,17 +464,19 @@ __global__ void __launch_bounds__(bwd_waves(V * sizeof(T)) * 64, bwd_waves(V * s
         me.frequencies();
         while (true) {
             const bool new_group = turn_group;
+            const int64_t group = at.group;
+            const int pass_now = pass;
             turn_group = pass + 1 >= at.pass1;
             const bool more = turn_group ? at.next(s) : true;
-            const int pass_n = turn_group ? at.pass0 : pass + 1;
-            typename L::At p_n = p;
+            pass = turn_group ? at.pass0 : pass + 1;
             int pos_n = 0;
             if (more) {
-                p_n = me.at(at.group, pass_n);
+                const typename L::At p_n = me.at(at.group, pass);
                 me.load(ahead_g, s.dy, s.dst, s.dsh, p_n);
                 if (a.norm) me.load(ahead, s.x, s.st, s.sh, p_n);
                 if (turn_group) pos_n = me.position(p_n);
             }
+            p = me.at(group, pass_now);
             if (new_group) me.angles(pos);
 
             float x[NU][2 * V], g[NU][2 * V], ss = 0.0f, sg = 0.0f;
@@ -521,15 +508,13 @@ __global__ void __launch_bounds__(bwd_waves(V * sizeof(T)) * 64, bwd_waves(V * s
                         g[n][i] = r * fmaf(w[n][i], g[n][i], -x[n][i] * c);
                     }
             }
-            T *yp = (T *)s.y + (p.t * s.heads + p.h) * a.d;
+            T *yp = (T *)s.y + ((int64_t)p.t * s.heads + p.h) * a.d;
 #pragma unroll
             for (int n = 0; n < NU; ++n) {
                 if (p.on && me.un[n].in1) Row<T, V>::st(yp + me.un[n].o1, g[n]);
                 if (p.on && me.un[n].in2) Row<T, V>::st(yp + me.un[n].o2, g[n] + V);
             }
             if (!more) break;
-            p = p_n;
-            pass = pass_n;
             if (turn_group) pos = pos_n;
 #pragma unroll
             for (int n = 0; n < NU; ++n)
@@ -554,25 +539,28 @@ __global__ void __launch_bounds__(bwd_waves(V * sizeof(T)) * 64, bwd_waves(V * s
             }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.d; e += WAVES * 64) {
+    for (int e = threadIdx.x; e < a.d; e += kBwdWaves * 64) {
         float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < WAVES; ++k) v += tab[k * a.d + e];
+        for (int k = 0; k < kBwdWaves; ++k) v += tab[k * a.d + e];
         s.part[(int64_t)blk * a.d + e] = v;
     }
 }
 
-// dw = sum of the blocks' shares in fp64: 8 elements a block, 32 slices of the shares
+// dw = sum of the blocks' shares in fp64: 8 elements a block, 32 slices of the shares, all asked for at once
 __global__ void __launch_bounds__(256) qk_rope_dw_kernel(const float *pq, const float *pk, float *dwq, float *dwk,
                                                          int nq, int nk, int d) {
     __shared__ double sum[32][9];
     const int i = threadIdx.x & 7, e = blockIdx.x * 8 + i, sl = threadIdx.x >> 3;
-    const float *p = blockIdx.y ? pk : pq;
+    const float *p = (blockIdx.y ? pk : pq) + min(e, d - 1);
     const int n = blockIdx.y ? nk : nq;
     double v = 0.0;
-    if (e < d) {
-#pragma unroll 8
-        for (int b = sl; b < n; b += 32) v += (double)p[(int64_t)b * d + e];
+    if (n > 0) {
+        float share[kBwdBlocks / 32];
+#pragma unroll
+        for (int k = 0; k < kBwdBlocks / 32; ++k) share[k] = p[min(sl + 32 * k, n - 1) * d];
+#pragma unroll
+        for (int k = 0; k < kBwdBlocks / 32; ++k) v += sl + 32 * k < n ? (double)share[k] : 0.0;
     }
     sum[sl][i] = v;
     __syncthreads();
@@ -584,18 +572,15 @@ __global__ void __launch_bounds__(256) qk_rope_dw_kernel(const float *pq, const 
 }
 
 // ------------------------------------------------------------------ host ----
-// Widest V up to `most` whose unit of 2 V elements fits the rotation's halves, what follows it, and
-// every address.  V = 1 fits everything.
-int pick_v(int most, const void *const *ptr, const int64_t *stride, int np, int ns, int d, int rot, int esize,
+// 4 where units of 2 x 4 elements fit the rotation's halves, what follows it, and every
+// address; else 1, which fits everything
+int pick_v(const void *const *ptr, const int64_t *stride, int np, int ns, int d, int rot, int esize,
            const float *wq, const float *wk) {
-    if ((((uintptr_t)wq | (uintptr_t)wk) & 15) != 0) return 1;     // weights are loaded by fours
-    for (int v = most; v >= 4; v >>= 1) {
-        bool ok = (rot / 2) % v == 0 && (d - rot) % (2 * v) == 0;
-        for (int i = 0; i < np; ++i) ok &= ((uintptr_t)ptr[i] & (uintptr_t)(v * esize - 1)) == 0;
-        for (int i = 0; i < ns; ++i) ok &= stride[i] % v == 0;
-        if (ok) return v;
-    }
-    return 1;
+    bool ok = (((uintptr_t)wq | (uintptr_t)wk) & 15) == 0;         // weights are loaded by fours
+    ok &= rot / 2 % 4 == 0 && (d - rot) % 8 == 0;
+    for (int i = 0; i < np; ++i) ok &= ((uintptr_t)ptr[i] & (uintptr_t)(4 * esize - 1)) == 0;
+    for (int i = 0; i < ns; ++i) ok &= stride[i] % 4 == 0;
+    return ok ? 4 : 1;
 }
 
 void set_geometry(Kp &k, int v, int d, int rot) {
@@ -669,7 +654,7 @@ hipError_t launch_qk_rope(const QkRopeArgs &a, hipStream_t stream, const char **
     const int esize = a.bf16 ? 2 : 4;
     const void *ptr[] = {a.q, a.q_out, a.k, a.k_out, a.v};
     const int64_t stride[] = {a.q_st, a.q_sh, a.k_st, a.k_sh, a.v_st, a.v_sh, (int64_t)a.headdim};
-    int v = pick_v(4, ptr, stride, cache ? 5 : a.n_kv_heads > 0 ? 4 : 2, 7, a.headdim, a.rot_dim, esize, a.wq, a.wk);
+    int v = pick_v(ptr, stride, cache ? 5 : a.n_kv_heads > 0 ? 4 : 2, 7, a.headdim, a.rot_dim, esize, a.wq, a.wk);
     if (cache) {   // the cache's own addresses: V elements of 1, 2 or 4 bytes
         const void *cp[] = {a.k_out, a.v_cache};
         const int64_t cs[] = {a.c_sp, a.c_st, a.c_sh};
@@ -691,7 +676,7 @@ hipError_t launch_qk_rope(const QkRopeArgs &a, hipStream_t stream, const char **
         s.x = x; s.y = y; s.w = w; s.st = st; s.sh = sh;
         s.heads = (int)heads; s.rotate = rotate; s.cache = to_cache;
         set_work(s, k, a.n_tokens, a.n_heads + (cache ? 2 : 1) * a.n_kv_heads, kFwdWaves,
-                 kCUs * fwd_blocks(esize));
+                 kCUs * fwd_blocks(esize, cache));
     };
     side(0, a.q, a.q_out, a.wq, a.q_st, a.q_sh, a.n_heads, true, false);
     if (a.n_kv_heads > 0) side(1, a.k, a.k_out, a.wk, a.k_st, a.k_sh, a.n_kv_heads, true, cache);
@@ -710,7 +695,7 @@ size_t qk_rope_bwd_workspace_bytes(int64_t n_tokens, int64_t n_heads, int64_t n_
     if (flags & SSM_QK_NO_NORM) return 0;
     const int64_t all = n_heads + n_kv_heads;
     auto blocks = [&](int64_t heads) {           // each wave has a (token, head) at least
-        return std::min<int64_t>(n_tokens * heads / bwd_waves(16) + 1, blocks_of(heads, all, kBwdBlocks));
+        return std::min<int64_t>(n_tokens * heads / kBwdWaves + 1, blocks_of(heads, all, kBwdBlocks));
     };
     return (size_t)(blocks(n_heads) + (n_kv_heads > 0 ? blocks(n_kv_heads) : 0)) * (size_t)headdim * sizeof(float);
 }
@@ -721,12 +706,8 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
     const void *ptr[] = {a.q, a.dq_out, a.dq, a.k, a.dk_out, a.dk};
     const int64_t stride[] = {a.q_st, a.q_sh, a.dq_st, a.dq_sh, (int64_t)a.headdim, a.k_st, a.k_sh, a.dk_st, a.dk_sh};
     const bool has_k = a.n_kv_heads > 0, norm = (a.flags & SSM_QK_NO_NORM) == 0;
-    // 8 elements a lane save instructions and cost a quarter of the waves (150 registers against
-    // 102): 16k tokens of 16 + 4 heads of 128 67 us against 63 with 4, of 64 + 8 heads the same;
-    // 8k tokens of heads of 256 55 against 63
-    const int most = a.bf16 && a.headdim > 128 ? 8 : 4;
-    const int v = pick_v(most, ptr, stride, has_k ? 6 : 3, has_k ? 9 : 5, a.headdim, a.rot_dim, esize, a.wq, a.wk);
-    const int waves = bwd_waves(v * esize);
+    const int v = pick_v(ptr, stride, has_k ? 6 : 3, has_k ? 9 : 5, a.headdim, a.rot_dim, esize, a.wq, a.wk);
+    constexpr int waves = kBwdWaves;
     Kp k = {};
     set_geometry(k, v, a.headdim, a.rot_dim);
     k.inv_freq = a.inv_freq; k.positions = a.positions;
@@ -749,10 +730,10 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
     };
     side(0, a.q, a.dq_out, a.dq, a.wq, a.q_st, a.q_sh, a.dq_st, a.dq_sh, a.n_heads);
     if (has_k) side(1, a.k, a.dk_out, a.dk, a.wk, a.k_st, a.k_sh, a.dk_st, a.dk_sh, a.n_kv_heads);
-    // Few heads: a block a side, whose share of dw is dw, and no second launch.  (16 + 4 heads of 128,
-    // us a call in one launch and in two: 8 bf16 tokens, 2 steps 7.8 and 10.5, 8 fp32 ones, 4 steps 8.6 and 11.4;
-    // 16 bf16 tokens, 4 steps 10.2 and 10.6; 32, 8 steps 16.2 and 10.5.)
-    const bool one = norm && a.n_tokens > 0 && deal(1) <= 4;
+    // Few heads: a block a side, whose share of dw is dw, and no second launch.  (16 + 4 heads of 128, us a
+    // call in one launch and in two: 4 tokens, 2 steps 6.2 and 8.2; 8, 4 steps 8.2 both; 16, 8 steps 12.8 and
+    // 8.2.  32 fp32 tokens of 4 + 4 heads of 64, 2 steps 7.4 and 8.4.)
+    const bool one = norm && a.n_tokens > 0 && deal(1) <= 2;
     if (!one) deal(kBwdBlocks);
     float *ws = (float *)a.workspace;
     k.side[0].part = one ? a.dwq : ws;
@@ -767,8 +748,7 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
     } while (0)
     if (blocks > 0) {
         if (a.bf16) {
-            if (v == 8) SSM_BWD(uint16_t, 8);
-            else if (v == 4) SSM_BWD(uint16_t, 4);
+            if (v == 4) SSM_BWD(uint16_t, 4);
             else SSM_BWD(uint16_t, 1);
         } else {
             if (v == 4) SSM_BWD(float, 4);

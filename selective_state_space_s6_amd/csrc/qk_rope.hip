@@ -14,11 +14,10 @@
 // pair are its own, and only the norm's sums cross lanes.  The next heads' elements are
 // asked for before the present ones are worked on, and no wave waits for another.
 //
-// Measured, kernels alone, 16384 tokens of 16 + 4 heads of 128 in bf16: forward 168 MB 38 to 41 us (4.1
-// to 4.4 TB/s; the same kernel without norm and rotation 35, a strided copy 35 to 37), backward 252
-// MB 57 us (4.4 TB/s) and 4.8 us to join dw.  8192 tokens of 32 + 8 + 8 heads into an 8-bit cache
-// 185 MB 44 us.  64 tokens into a cache 4.5 us, 1021 fp32 tokens of 6 + 3 heads of 72 5.1 us:
-// a chain of loads.
+// Measured, us a call, 16384 tokens of 16 + 4 heads of 128 in bf16: forward 168 MB 36.4 (4.6 TB/s; a strided
+// copy 35 to 37), backward 252 MB 58 (4.3 TB/s), 4 of it to join dw.  8192 tokens of 32 + 8 + 8 heads into an
+// 8-bit cache 185 MB 46.  64 tokens into a cache 5.1, 1021 fp32 tokens of 6 + 3 heads of 72 5.4: a chain
+// of loads.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <algorithm>
@@ -46,6 +45,7 @@ constexpr int fwd_blocks(int esize, bool cache) { return esize == 2 && !cache ? 
 // 68.7 against 73.5).
 constexpr int kBwdWaves = 8;
 constexpr int kBwdBlocks = 2 * kCUs;
+constexpr int kOneWaves = 16;       // of the only block of a side
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const bf16x2 r = __builtin_convertvector((f32x2){a, b}, bf16x2);   // to nearest even
@@ -437,8 +437,8 @@ __global__ void __launch_bounds__(kFwdWaves * 64, fwd_blocks(sizeof(T), KV != 0)
 // The gradients.  A wave keeps its share of dw in registers (a lane's elements are the same
 // in every head); the shares of its lane groups are joined across lanes at the end, those of
 // the block's waves in LDS.
-template <typename T, int V, bool IL>
-__global__ void __launch_bounds__(kBwdWaves * 64, 4) qk_rope_bwd_kernel(Kp a) {
+template <typename T, int V, bool IL, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64, 4) qk_rope_bwd_kernel(Kp a) {
     typedef Lane<T, V, IL> L;
     constexpr int NU = L::NU;
     extern __shared__ float tab[];
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kBwdWaves * 64, 4) qk_rope_bwd_kernel(Kp a) {
     for (int n = 0; n < NU; ++n)
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) dw[n][i] = 0.0f;
-    Walk at(s, (uint32_t)(blk * kBwdWaves + wave));
+    Walk at(s, (uint32_t)(blk * WAVES + wave));
     if (at.part < s.parts) {
         int pass = at.pass0;
         typename L::Raw raw[NU][2], raw_g[NU][2], ahead[NU][2], ahead_g[NU][2];
@@ -539,10 +539,10 @@ __global__ void __launch_bounds__(kBwdWaves * 64, 4) qk_rope_bwd_kernel(Kp a) {
             }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.d; e += kBwdWaves * 64) {
+    for (int e = threadIdx.x; e < a.d; e += WAVES * 64) {
         float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kBwdWaves; ++k) v += tab[k * a.d + e];
+        for (int k = 0; k < WAVES; ++k) v += tab[k * a.d + e];
         s.part[(int64_t)blk * a.d + e] = v;
     }
 }
@@ -646,6 +646,16 @@ void fwd_type(const Kp &k, unsigned blocks, size_t lds, bool bf16, int v, bool i
     }
 }
 
+template <typename T, int V, int WAVES>
+void bwd_waves_go(const Kp &k, unsigned blocks, bool il, size_t lds, hipStream_t stream) {
+    if (il) hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, true, WAVES>), dim3(blocks), dim3(WAVES * 64), lds, stream, k);
+    else hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, false, WAVES>), dim3(blocks), dim3(WAVES * 64), lds, stream, k);
+}
+template <typename T, int V>
+void bwd_go(const Kp &k, unsigned blocks, bool one, bool il, size_t lds, hipStream_t stream) {
+    one ? bwd_waves_go<T, V, kOneWaves>(k, blocks, il, lds, stream) : bwd_waves_go<T, V, kBwdWaves>(k, blocks, il, lds, stream);
+}
+
 }  // namespace
 
 hipError_t launch_qk_rope(const QkRopeArgs &a, hipStream_t stream, const char **kernel_name) {
@@ -707,7 +717,6 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
     const int64_t stride[] = {a.q_st, a.q_sh, a.dq_st, a.dq_sh, (int64_t)a.headdim, a.k_st, a.k_sh, a.dk_st, a.dk_sh};
     const bool has_k = a.n_kv_heads > 0, norm = (a.flags & SSM_QK_NO_NORM) == 0;
     const int v = pick_v(ptr, stride, has_k ? 6 : 3, has_k ? 9 : 5, a.headdim, a.rot_dim, esize, a.wq, a.wk);
-    constexpr int waves = kBwdWaves;
     Kp k = {};
     set_geometry(k, v, a.headdim, a.rot_dim);
     k.inv_freq = a.inv_freq; k.positions = a.positions;
@@ -719,7 +728,7 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
         s.heads = (int)heads; s.rotate = true;
     };
     // steps of a wave, where the sides have `blocks` blocks together, and one each at least
-    auto deal = [&](int blocks) {
+    auto deal = [&](int blocks, int waves) {
         int64_t most = 0;
         for (int i = 0; i < (has_k ? 2 : 1); ++i) {
             Side &s = k.side[i];
@@ -731,31 +740,21 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
     side(0, a.q, a.dq_out, a.dq, a.wq, a.q_st, a.q_sh, a.dq_st, a.dq_sh, a.n_heads);
     if (has_k) side(1, a.k, a.dk_out, a.dk, a.wk, a.k_st, a.k_sh, a.dk_st, a.dk_sh, a.n_kv_heads);
     // Few heads: a block a side, whose share of dw is dw, and no second launch.  (16 + 4 heads of 128, us a
-    // call in one launch and in two: 4 tokens, 2 steps 6.2 and 8.2; 8, 4 steps 8.2 both; 16, 8 steps 12.8 and
-    // 8.2.  32 fp32 tokens of 4 + 4 heads of 64, 2 steps 7.4 and 8.4.)
-    const bool one = norm && a.n_tokens > 0 && deal(1) <= 2;
-    if (!one) deal(kBwdBlocks);
+    // call in one launch and in two: 4 tokens, 1 step 6.4 and 9.3; 8 tokens, 2 steps 7.6 and 9.2; 16 tokens, 4
+    // steps 10.3 and 9.3.)
+    const bool one = norm && a.n_tokens > 0 && deal(1, kOneWaves) <= 2;
+    if (!one) deal(kBwdBlocks, kBwdWaves);
+    const int waves = one ? kOneWaves : kBwdWaves;
     float *ws = (float *)a.workspace;
     k.side[0].part = one ? a.dwq : ws;
     k.side[1].part = one ? a.dwk : norm ? ws + (int64_t)k.side[0].blocks * a.headdim : nullptr;
     const size_t lds = std::max(table_bytes(k, waves), norm ? (size_t)waves * a.headdim * sizeof(float) : 0);
     const unsigned blocks = (unsigned)(k.side[0].blocks + k.side[1].blocks);
     const bool il = (a.flags & SSM_ROPE_INTERLEAVED) != 0;
-#define SSM_BWD(T, V)                                                                                           \
-    do {                                                                                                        \
-        if (il) hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, true>), dim3(blocks), dim3(waves * 64), lds, stream, k);  \
-        else hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, false>), dim3(blocks), dim3(waves * 64), lds, stream, k);    \
-    } while (0)
     if (blocks > 0) {
-        if (a.bf16) {
-            if (v == 4) SSM_BWD(uint16_t, 4);
-            else SSM_BWD(uint16_t, 1);
-        } else {
-            if (v == 4) SSM_BWD(float, 4);
-            else SSM_BWD(float, 1);
-        }
+        if (a.bf16) v == 4 ? bwd_go<uint16_t, 4>(k, blocks, one, il, lds, stream) : bwd_go<uint16_t, 1>(k, blocks, one, il, lds, stream);
+        else v == 4 ? bwd_go<float, 4>(k, blocks, one, il, lds, stream) : bwd_go<float, 1>(k, blocks, one, il, lds, stream);
     }
-#undef SSM_BWD
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !norm || one) return e;
     *kernel_name = "qk_rope_dw_kernel";

@@ -118,6 +118,8 @@ __device__ __forceinline__ float head_sum(float v) {
     return v + __shfl_xor(v, 32);
 }
 
+// waves on one of a compute unit's 4 SIMDs, for heads of up to dp (why: Tile::PER_SIMD)
+constexpr int per_simd(int dp) { return dp <= 64 ? 3 : dp <= 128 ? 2 : 1; }
 // One (cache type, padded head size): register shapes of a tile
 template <int CT, int DP, int W> struct Tile {
     static constexpr int E = CT == KF32 ? 4 : CT == KBF16 ? 2 : 1;
@@ -134,8 +136,10 @@ template <int CT, int DP, int W> struct Tile {
     static constexpr int UNIT = W * NT;
     // resident blocks of a compute unit, by the registers of a tile's K, V and output (and of q,
     // which waits in LDS where those leave it no room).  Heads of 256 on 2 waves a SIMD would spill:
-    // fp32 118 us against 58.
-    static constexpr int PER_SIMD = DP <= 128 ? 2 : 1;         // waves on one of a compute unit's 4
+    // fp32 118 us against 58; of 128 on 3 do a little: 64 rows of up to 16000 tokens, 8 kv heads in 8 bits 228 us on 2
+    // and 234 on 3, of up to 2000 32 and 41; bf16 374 and 375; 59 and 60.  Heads of 64 do not: in 8 bits 16000 tokens
+    // each 222 us on 2, 201 on 3, bf16 411 and 360, fp32 713 and 675, up to 16000 bf16 224 and 212.
+    static constexpr int PER_SIMD = per_simd(DP);
     static constexpr int RES = PER_SIMD * 4 / W;
     static constexpr bool QLDS = DP > 128;
     static constexpr uint64_t ALL = NT == 64 ? ~uint64_t(0) : (uint64_t(1) << NT) - 1;
@@ -615,8 +619,8 @@ __global__ void __launch_bounds__(kNT) paged_attn_join_kernel(Kp a, int grid) {
 int64_t passes_of(int64_t group) { return (group + kHeads - 1) / kHeads; }
 int64_t align16(int64_t n) { return (n + 15) & ~int64_t(15); }
 
-// waves of the largest grid that are resident at once
-constexpr int64_t waves_of(int per_simd) { return per_simd * 4 * kCUs; }
+// (row, kv head)s that occupy the chip with a wave each
+int64_t waves_of(int64_t d) { return (d <= 128 ? 2 : 1) * 4 * kCUs; }
 
 template <int CT, int DP, bool EXACT, int W>
 hipError_t go_w(Kp &k, int &grid, hipStream_t stream) {
@@ -651,7 +655,7 @@ hipError_t go_w(Kp &k, int &grid, hipStream_t stream) {
 template <int CT, int DP, bool EXACT>
 hipError_t go(Kp &k, int &grid, hipStream_t stream) {
     using T = Tile<CT, DP, 1>;
-    const int64_t heads = (int64_t)k.batch * k.n_kv * k.passes, waves = waves_of(T::PER_SIMD);
+    const int64_t heads = (int64_t)k.batch * k.n_kv * k.passes, waves = waves_of(DP);
     const int tiles = ((k.window > 0 ? k.window : k.max_len) + T::NT - 1) / T::NT;
     const bool by_wave = tiles <= 1 || (heads >= waves / 2 && tiles <= (heads >= waves ? 32 : 16));
     const bool by_block = tiles <= (heads >= waves / 4 ? 40 : heads >= waves / 8 ? 20 : 12);
@@ -681,10 +685,9 @@ double paged_attn_max_units(int64_t batch, int64_t n_heads, int64_t n_kv_heads, 
 // blocks of the largest grid that any cache type gives these sizes
 static int64_t most_blocks(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t headdim, int64_t max_pages,
                            int64_t page_size) {
-    const int per_simd = headdim <= 128 ? 2 : 1;
-    const bool one = batch * n_kv_heads * passes_of(n_heads / n_kv_heads) >= waves_of(per_simd);
+    const bool one = batch * n_kv_heads * passes_of(n_heads / n_kv_heads) >= waves_of(headdim);
     const double units = paged_attn_max_units(batch, n_heads, n_kv_heads, max_pages, page_size) + 32;
-    return (int64_t)std::min(units, (double)(waves_of(per_simd) / (one ? 1 : 4)));
+    return (int64_t)std::min(units, (double)(per_simd((int)std::min<int64_t>(headdim, 256)) * kCUs * (one ? 4 : 1)));
 }
 
 size_t paged_attn_workspace_bytes(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t headdim,

@@ -118,8 +118,8 @@ struct Call {
         }
         return r;
     }
-    // few enough bytes that outputs which stay alive do not hold much of each other's memory
-    static bool few(int64_t elements) { return elements <= (1 << 18); }
+    // few enough (up to 4 MiB) that outputs which stay alive do not hold much of each other's memory
+    static bool few(int64_t elements) { return elements <= (1 << 20); }
     Tensor workspace(PyObject *o, size_t need) const {
         if (o == Py_None) return make(ScalarType::Byte, {(int64_t)need});
         const Tensor &t = tensor(o, "workspace");

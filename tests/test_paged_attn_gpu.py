@@ -155,6 +155,25 @@ def test_against_the_oracle(cuda_device, case):
     _compare("attn %s" % (case[1:],), got, q, kc, vc, table, lens, sc, s, window)
 
 
+@pytest.mark.parametrize("H,Hk,d,cache,layout,window", [
+    (8, 2, 128, "bf16", "nhd", 0), (2, 2, 64, "bf16", "hnd", 0), (20, 1, 80, "bf16", "nhd", 0), (8, 4, 96, "f8", "nhd", 0),
+    (8, 8, 128, "f8", "hnd", 3333), (6, 3, 128, "f32", "nhd", 0), (10, 2, 256, "f32", "nhd", 2000), (8, 4, 256, "bf16", "nhd", 0)])
+def test_one_row_in_a_wide_table(cuda_device, H, Hk, d, cache, layout, window):
+    """One request, of any length, in a table for 6400 tokens (fewer tokens than blocks, too), with a
+    workspace that holds NaN before the call: what no block wrote is not used."""
+    import torch
+    m = lib()
+    ws = torch.empty(m.ssm_paged_attn_decode_fwd_workspace_size(1, H, Hk, d, 400, 16), dtype=torch.uint8, device=cuda_device)
+    for n in (0, 1, 17, 130, 700, 3001, 6400):
+        q, kc, vc, table, lens, s = _make(cuda_device, 20 + n, [n], H, Hk, d, cache, 16, layout, cols=400)
+        ws.fill_(255)
+        got = _run(cuda_device, q, kc, vc, table, lens, d ** -0.5, s, window, workspace=ws)
+        _compare("attn one row %s" % ((n, H, Hk, d, cache, window),), got, q, kc, vc, table, lens, d ** -0.5, s, window)
+    table[0, 100:300] = -1                      # whole pieces without a page in the cache
+    got = _run(cuda_device, q, kc, vc, table, lens, d ** -0.5, s, window, workspace=ws)
+    _compare("attn one row, pages missing", got, q, kc, vc, table, lens, d ** -0.5, s, window)
+
+
 def test_twice_the_same_and_without_lse(cuda_device):
     import torch
     q, kc, vc, table, lens, s = _make(cuda_device, 3, [700, 33, 2100], 8, 2, 128, "bf16", 16, "nhd")

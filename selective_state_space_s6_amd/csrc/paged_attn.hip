@@ -125,8 +125,10 @@ constexpr int per_simd(int dp) { return dp <= 64 ? 3 : dp <= 128 ? 2 : 1; }
 // One (cache type, padded head size): register shapes of a tile
 template <int CT, int DP, int W> struct Tile {
     static constexpr int E = CT == KF32 ? 4 : CT == KBF16 ? 2 : 1;
-    // tokens: about 8 KiB of K (and of V), so that a wave has that much on its way at any time
-    static constexpr int NT = CT == KF32 ? (DP <= 64 ? 32 : 16) : CT == KBF16 ? (DP <= 64 ? 64 : 32) : 64;
+    // tokens: about 8 KiB of K (and of V), so that a wave has that much on its way at any time.  (8-bit heads of
+    // 256 in tiles of 64 and of 32 tokens: 1 row of 600 15.1 and 11.4 us, 78 rows of up to 600 25.0 and 18.5, 10 of
+    // 16000 73.9 and 77.3.)
+    static constexpr int NT = CT == KF32 ? (DP <= 64 ? 32 : 16) : CT == KBF16 ? (DP <= 64 ? 64 : 32) : DP > 128 ? 32 : 64;
     static constexpr int SUB = NT / 16;                        // 16-token blocks of scores
     static constexpr int KD = 16 / E;                          // dims of a 16-byte load of K
     static constexpr int KC = DP / (4 * KD);                   // loads of a K row (four lanes each)
@@ -671,14 +673,15 @@ hipError_t go_w(Kp &k, int &grid, hipStream_t stream) {
 //   1 row of 32 tokens 5.7, 5.7, 8.2; 300: 12.0, 7.7, 9.6; 600: 19.8, 10.5, 10.0; 2400: 67, 28, 10.6
 //   64 rows of 128 tokens 10.3, 9.2, 12.1; 600: 36.9, 29.6, 32.9; up to 1200: 59, 39, 39; up to 2400: 118, 78, 71
 //   256 rows of 128 tokens 24.4, 29.0, 30.2; up to 300: 32.8, 38.9, 43.5; up to 1200: 132, 130, 136; up to 2400: 255, 248, 244
-// and of 4 and 3 kv heads in 8 and 32 bits, heads of 64 and 256 the same way.  In pieces, four waves share the
+// and of 4 and 3 kv heads in 8 and 32 bits, heads of 64 and 256 the same way: 78 rows of 90 tokens, 4 heads of 256 in
+// 8 bits, more than blocks of four are resident, 11.7, 15.7; 150 rows, 2 heads of 256 in bf16 12.1, 16.7.  In pieces, four waves share the
 // tokens of one, and fewer pieces are left to join; one row of 100000 tokens 32.8 us by waves, 23.1 by fours.
 template <int CT, int DP, bool EXACT>
 hipError_t go(Kp &k, int &grid, hipStream_t stream) {
     using T = Tile<CT, DP, 1>;
     const int64_t heads = (int64_t)k.batch * k.n_kv * k.passes, waves = waves_of(DP);
     const int tiles = ((k.window > 0 ? k.window : k.max_len) + T::NT - 1) / T::NT;
-    const bool by_wave = tiles <= 1 || (heads >= waves / 2 && tiles <= (heads >= waves ? 32 : 16));
+    const bool by_wave = tiles <= 1 || (heads > waves / 4 && tiles <= (heads >= waves ? 32 : heads >= waves / 2 ? 16 : 8));
     const bool by_block = tiles <= (heads >= waves / 4 ? 40 : heads >= waves / 8 ? 20 : 12);
     k.whole = (by_wave || by_block) && heads < (1 << 22);      // (a grid's threads are counted in 32 bits)
     return (k.whole ? by_wave : heads >= waves) ? go_w<CT, DP, EXACT, 1>(k, grid, stream) : go_w<CT, DP, EXACT, 4>(k, grid, stream);

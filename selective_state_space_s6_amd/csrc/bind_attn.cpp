@@ -151,6 +151,11 @@ int64_t whole_number(PyObject *o, const char *name) {
     }
     return v;
 }
+uint32_t flag_bits(PyObject *o) {
+    const int64_t v = whole_number(o, "flags");
+    if (v < 0 || v > 0xffffffffLL) refuse(PyExc_ValueError, "flags: " + std::to_string(v) + " has bits that no flag has");
+    return (uint32_t)v;
+}
 float number(PyObject *o, const char *name) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) {
@@ -272,7 +277,7 @@ PyObject *pair(const Tensor &x, const Tensor &y) {
 PyObject *rope_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 10, [&]() -> PyObject * {
         const float eps = number(a[6], "eps");
-        const uint32_t flags = (uint32_t)whole_number(a[7], "flags");
+        const uint32_t flags = flag_bits(a[7]);
         const Rope r(a, flags);
         Tensor qo, ko;
         if (a[1] != Py_None && a[8] == Py_None && a[9] == Py_None && r.c.few(r.T * (r.H + r.Hk) * r.d)) {
@@ -291,7 +296,7 @@ PyObject *rope_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 15, [&]() -> PyObject * {
         const float eps = number(a[8], "eps");
-        const uint32_t flags = (uint32_t)whole_number(a[9], "flags");
+        const uint32_t flags = flag_bits(a[9]);
         const Rope r(a, flags);
         const bool has_k = a[1] != Py_None;
         const Tensor &gq = tensor(a[6], "dq_out");
@@ -366,7 +371,7 @@ struct Caches {
 PyObject *rope_cache_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 15, [&]() -> PyObject * {
         const float eps = number(a[10], "eps"), k_scale = number(a[11], "k_scale"), v_scale = number(a[12], "v_scale");
-        const uint32_t flags = (uint32_t)whole_number(a[13], "flags");
+        const uint32_t flags = flag_bits(a[13]);
         const Rope r(a, flags);
         const Tensor &v = tensor(a[6], "v");
         const void *pv = r.c.view(v, "v", r.type, {r.T, r.Hk, r.d});

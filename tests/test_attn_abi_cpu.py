@@ -208,6 +208,9 @@ def test_the_bindings_own_checks(m):
                           (dict(q=z(3, 8, 2).transpose(1, 2)), ValueError, "last dim"), (dict(), ValueError, "expected a GPU")]:
         with pytest.raises(err, match=word):
             m.ssm_qk_norm_rope_fwd(**dict(rope, **kw))
+    for flags in (1 << 32, -1):
+        with pytest.raises(ValueError, match="flags"):
+            m.ssm_qk_norm_rope_fwd(**rope, flags=flags)
     with pytest.raises(ValueError, match="dq_out: shape"):
         m.ssm_qk_norm_rope_bwd(**rope, dq_out=z(3, 1, 8), dk_out=z(3, 1, 8))
     c = z(4, 16, 1, 8)

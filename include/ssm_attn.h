@@ -173,9 +173,9 @@ int ssm_qk_norm_rope_cache_fwd(const void *q, const void *k, const void *v, cons
  * tokens of a prompt are rows with growing lens.
  * Arithmetic: products on the matrix cores (bf16 products are exact in fp32;
  * 8-bit caches are widened to bf16, which is exact; fp32 stays fp32), sums,
- * maxima and exponentials in fp32; exp(s_j) enters its product with v as the
- * sum of two bf16 values (16 bits) where v is bf16 or 8-bit, and the output is
- * rounded once.
+ * maxima and exponentials in fp32; exp(s_j) enters its product with v with all
+ * its bits (as the sum of three bf16 values where v is bf16 or 8-bit), and the
+ * output is rounded once.
  *
  * Layouts: q (batch, n_heads, headdim) [dtype] strided; k_cache, v_cache as
  * above [kv_dtype]; block_table (batch, max_pages) int32, row stride

@@ -441,14 +441,18 @@ __global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_att
                         for (int i = 0; i < 4; ++i)
                             acc[b][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vf[j][b].w[i]), x[j], acc[b][i], 0, 0, 0);
             } else {
-                // p as the sum of two bf16 values: one alone would double the output's error
+                // p as the sum of three bf16 values, all its 24 bits.  (Two keep 16 and more: outputs a few 1e-6 off before
+                // their rounding.  64 rows of up to 8192 tokens, bf16 204.4 us with two, 205.2 with three; 16 of 65536 in
+                // 8 bits 368.1 and 370.0; one of 2047 9.88 and 9.96.)
 #pragma unroll
                 for (int g = 0; g < T::VR; g += 8) {     // 32 tokens at a time
-                    u32x4 ph, pl;
+                    u32x4 ph, pm, pl;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         ph[j] = pack_bf16(x[g + 2 * j], x[g + 2 * j + 1]);
-                        pl[j] = pack_bf16(x[g + 2 * j] - lo_f(ph[j]), x[g + 2 * j + 1] - hi_f(ph[j]));
+                        const float r0 = x[g + 2 * j] - lo_f(ph[j]), r1 = x[g + 2 * j + 1] - hi_f(ph[j]);
+                        pm[j] = pack_bf16(r0, r1);
+                        pl[j] = pack_bf16(r0 - lo_f(pm[j]), r1 - hi_f(pm[j]));
                     }
 #pragma unroll
                     for (int b = 0; b < VB; ++b) {
@@ -460,6 +464,7 @@ __global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_att
                                 for (int j = 0; j < 4; ++j)
                                     vt[j] = perm(vf[g + 2 * j + 1][b].w[i / 2], vf[g + 2 * j][b].w[i / 2], i & 1 ? 0x07060302u : 0x05040100u);
                                 acc[b][i] = mfma_bf16(vt, ph, acc[b][i]);
+                                acc[b][i] = mfma_bf16(vt, pm, acc[b][i]);
                                 acc[b][i] = mfma_bf16(vt, pl, acc[b][i]);
                             }
                         } else {
@@ -473,8 +478,10 @@ __global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_att
                                     v1[j] = widen<true>(w);
                                 }
                                 acc[b][i] = mfma_bf16(v0, ph, acc[b][i]);
+                                acc[b][i] = mfma_bf16(v0, pm, acc[b][i]);
                                 acc[b][i] = mfma_bf16(v0, pl, acc[b][i]);
                                 acc[b][i + 1] = mfma_bf16(v1, ph, acc[b][i + 1]);
+                                acc[b][i + 1] = mfma_bf16(v1, pm, acc[b][i + 1]);
                                 acc[b][i + 1] = mfma_bf16(v1, pl, acc[b][i + 1]);
                             }
                         }

@@ -311,3 +311,33 @@ def test_in_a_graph_with_lens_and_table_changing(cuda_device, H, Hk, d):
         call()
         torch.cuda.synchronize()
         assert torch.equal(a, o) and torch.equal(b, lse)
+
+
+@pytest.mark.parametrize("H,Hk,d,cache,cols", [(8, 2, 128, "bf16", 1), (4, 4, 64, "bf16", 1), (2, 1, 256, "bf16", 1), (17, 1, 192, "bf16", 1),
+                                               (8, 2, 128, "f8", 1), (4, 2, 64, "f8", 1), (3, 1, 256, "f8", 1), (4, 2, 128, "f32", 1),
+                                               (8, 2, 128, "bf16", 4000), (8, 2, 128, "f8", 4000)])
+def test_the_weights_bits_cancel_where_v_does(cuda_device, H, Hk, d, cache, cols):
+    """Three tokens with scores 0, t and t + e, |e| <= 2^-12, and v = 0, 1 and -1: o = (p1 - p2) / (1 + p1 + p2) is about
+    2^-14, so the output's own rounding is under 2^-21 and a weight that lost its last bits shows.  (Two bf16
+    values in place of a weight are up to 2^-18 off, o up to 2^-18.) Every product and both scores are
+    exact in fp32; a weight under 1/2 takes (2 |s| + 4) u of itself from its exponent and the exponential, two of
+    them 5 u of o, and adding them up in fp32 8 u of the sum of weights at most, 5 u of o: within 12 u."""
+    import torch
+    B = 300 if cols == 1 else 40
+    rng = np.random.default_rng(31)
+    dt = {"bf16": torch.bfloat16, "f8": torch.float8_e4m3fn, "f32": torch.float32}[cache]
+    q = torch.zeros((B, H, d))
+    q[..., 0] = torch.tensor(-rng.uniform(0.7, 1.0, (B, H)))
+    q[..., 1] = torch.tensor(rng.uniform(2.0 ** -13, 2.0 ** -12, (B, H)) * rng.choice([-1, 1], (B, H)))
+    q = q.to(torch.float32 if cache == "f32" else torch.bfloat16).to(cuda_device)
+    kc, vc = torch.zeros((1, 16, Hk, d)), torch.zeros((1, 16, Hk, d))
+    kc[0, 1:3, :, 0], kc[0, 2, :, 1] = 1.0, 1.0
+    vc[0, 1], vc[0, 2] = 1.0, -1.0
+    kc, vc = kc.to(dt).to(cuda_device), vc.to(dt).to(cuda_device)
+    o, _ = _run(cuda_device, q, kc, vc, np.zeros((B, cols)), [3] * B, 1.0, 1.0)
+    t, e = _n(q)[..., 0], _n(q)[..., 1]
+    want = (np.exp(t) - np.exp(t + e)) / (1 + np.exp(t) + np.exp(t + e))
+    tol = (U if cache == "f32" else 2.0 ** -8) * np.abs(want) + 12 * U
+    worst = float((np.abs(_n(o) - want[..., None]) / tol[..., None]).max())
+    report("attn weights %s" % ((H, Hk, d, cache, cols),), of_bound=worst)
+    assert worst <= 1.0

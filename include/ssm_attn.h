@@ -11,7 +11,8 @@
  * Two of them are widened here, because q, k and v usually are slices of one
  * projection's rows and a cache usually is a view: tensors may be strided (the
  * strides are in elements, the last dimension has stride 1), and pointers need
- * only their element's alignment unless a limit below asks for more.
+ * only their element's alignment unless a limit below asks for more.  A
+ * workspace is an output: it may alias no other argument.
  *
  * What the operators compute stands at each of them; the definitions are the
  * common ones of decoder models and are not taken from the pages that

@@ -148,6 +148,11 @@ int ssm_qk_norm_rope_fwd(const void *q, const void *k, const float *wq, const fl
         return fail(SSM_ERR_INVALID_ARG, "%s: k_out aliases a k that is not contiguous", E);
     if (n_kv_heads > 0 && (q_out == k || k_out == q || q_out == k_out))
         return fail(SSM_ERR_INVALID_ARG, "%s: an output aliases the other tensor", E);
+    const bool norm = (flags & SSM_QK_NO_NORM) == 0;
+    const Named outs[] = {{q_out, "q_out"}, {n_kv_heads > 0 ? k_out : nullptr, "k_out"}};
+    const Named ins[] = {{norm ? wq : nullptr, "wq"}, {norm && n_kv_heads > 0 ? wk : nullptr, "wk"}, {rot_dim > 0 ? inv_freq : nullptr, "inv_freq"},
+                         {rot_dim > 0 ? positions : nullptr, "positions"}};
+    if ((rc = check_alias(E, outs, 2, ins, 4)) != SSM_OK) return rc;
     ssm::QkRopeArgs a{};
     a.q = q; a.k = k; a.wq = wq; a.wk = wk; a.inv_freq = inv_freq; a.positions = positions;
     a.q_out = q_out; a.k_out = k_out;
@@ -198,12 +203,18 @@ int ssm_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const fl
         return fail(SSM_ERR_INVALID_ARG, "%s: dq aliases a dq_out that is not contiguous", E);
     if (n_tokens > 0 && has_k && dk == dk_out && (dk_stride_head != headdim || dk_stride_token != n_kv_heads * headdim))
         return fail(SSM_ERR_INVALID_ARG, "%s: dk aliases a dk_out that is not contiguous", E);
-    const Named outs[] = {{dq, "dq"}, {has_k ? dk : nullptr, "dk"}, {norm ? dwq : nullptr, "dwq"},
-                          {norm && has_k ? dwk : nullptr, "dwk"}};
-    const Named ins[] = {{q, "q"}, {k, "k"}, {wq, "wq"}, {wk, "wk"}, {workspace, "workspace"}};
-    if ((rc = check_alias(E, outs, 4, ins, 5)) != SSM_OK) return rc;
-    REQUIRE_ALIGN(E, workspace);
     const size_t need = ssm_qk_norm_rope_bwd_workspace_size(n_tokens, n_heads, n_kv_heads, headdim, flags);
+    const Named outs[] = {{dq, "dq"}, {has_k ? dk : nullptr, "dk"}, {norm ? dwq : nullptr, "dwq"},
+                          {norm && has_k ? dwk : nullptr, "dwk"}, {need > 0 ? workspace : nullptr, "workspace"}};
+    const Named ins[] = {{q, "q"}, {has_k ? k : nullptr, "k"}, {norm ? wq : nullptr, "wq"}, {norm && has_k ? wk : nullptr, "wk"},
+                         {rot_dim > 0 ? inv_freq : nullptr, "inv_freq"}, {rot_dim > 0 ? positions : nullptr, "positions"}};
+    if ((rc = check_alias(E, outs, 5, ins, 6)) != SSM_OK) return rc;
+    // a side's blocks may overwrite their own cotangents, not those that the other side's still read
+    const Named gq = {dq_out, "dq_out"}, gk = {has_k ? dk_out : nullptr, "dk_out"}, both[] = {gq, gk};
+    if ((rc = check_alias(E, outs, 1, &gk, 1)) != SSM_OK) return rc;
+    if ((rc = check_alias(E, outs + 1, 1, &gq, 1)) != SSM_OK) return rc;
+    if ((rc = check_alias(E, outs + 2, 3, both, 2)) != SSM_OK) return rc;
+    REQUIRE_ALIGN(E, workspace);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return fail(SSM_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", E, need,
                     workspace ? workspace_bytes : (size_t)0);
@@ -252,8 +263,11 @@ int ssm_qk_norm_rope_cache_fwd(const void *q, const void *k, const void *v, cons
     if (q_out == q && (q_stride_head != headdim || q_stride_token != n_heads * headdim))
         return fail(SSM_ERR_INVALID_ARG, "%s: q_out aliases a q that is not contiguous", E);
     const Named outs[] = {{q_out, "q_out"}, {k_cache, "k_cache"}, {v_cache, "v_cache"}};
-    const Named ins[] = {{k, "k"}, {v, "v"}, {wq, "wq"}, {wk, "wk"}, {slots, "slots"}};
-    if ((rc = check_alias(E, outs, 3, ins, 5)) != SSM_OK) return rc;
+    const bool norm = (flags & SSM_QK_NO_NORM) == 0;
+    const Named ins[] = {{k, "k"}, {v, "v"}, {norm ? wq : nullptr, "wq"}, {norm ? wk : nullptr, "wk"},
+                         {rot_dim > 0 ? inv_freq : nullptr, "inv_freq"}, {rot_dim > 0 ? positions : nullptr, "positions"},
+                         {slots, "slots"}};
+    if ((rc = check_alias(E, outs, 3, ins, 7)) != SSM_OK) return rc;
     if (k_cache == q || v_cache == q) return fail(SSM_ERR_INVALID_ARG, "%s: a cache aliases q", E);
     ssm::QkRopeArgs a{};
     a.q = q; a.k = k; a.v = v; a.wq = wq; a.wk = wk; a.inv_freq = inv_freq; a.positions = positions; a.slots = slots;
@@ -332,10 +346,9 @@ int ssm_paged_attn_decode_fwd(const void *q, const void *k_cache, const void *v_
         return fail(SSM_ERR_UNSUPPORTED, "%s: a stride of q is not a multiple of 16 bytes", E);
     if ((sp * ce) % 16 != 0 || (st * ce) % 16 != 0 || (sh * ce) % 16 != 0)
         return fail(SSM_ERR_UNSUPPORTED, "%s: a stride of the caches is not a multiple of 16 bytes", E);
-    const Named outs[] = {{o, "o"}, {lse, "lse"}};
-    const Named ins[] = {{q, "q"}, {k_cache, "k_cache"}, {v_cache, "v_cache"}, {block_table, "block_table"},
-                         {lens, "lens"}, {workspace, "workspace"}};
-    if ((rc = check_alias(E, outs, 2, ins, 6)) != SSM_OK) return rc;
+    const Named outs[] = {{o, "o"}, {lse, "lse"}, {workspace, "workspace"}};
+    const Named ins[] = {{q, "q"}, {k_cache, "k_cache"}, {v_cache, "v_cache"}, {block_table, "block_table"}, {lens, "lens"}};
+    if ((rc = check_alias(E, outs, 3, ins, 5)) != SSM_OK) return rc;
     const size_t need = ssm_paged_attn_decode_fwd_workspace_size(batch, n_heads, n_kv_heads, headdim, max_pages, page_size);
     if (workspace == nullptr || workspace_bytes < need)
         return fail(SSM_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", E, need,

@@ -230,3 +230,40 @@ def test_the_bindings_own_checks(m):
             m.ssm_paged_attn_decode_fwd(**dict(attn, **kw))
     with pytest.raises(ValueError, match="ring: shape"):
         m.ssm_kv_pages_step(z(2, t=i), z(2, t=i), z(2, 3, t=i), z(9, t=i), z(3, t=i), page_size=4, n_tokens=1)
+
+
+def test_no_output_on_an_input_of_the_other_side(lib):
+    """What one block writes while another still reads it is refused: an output or the workspace on any input but
+    its own (dq on dq_out, dk on dk_out)."""
+    need = lib.ssm_qk_norm_rope_bwd_workspace_size(4, 2, 2, 64, 0)
+    base = {n: _p(i) for i, n in enumerate(BWD[:12])}
+    base.update(n_tokens=4, n_heads=2, n_kv_heads=2, headdim=64, rot_dim=64, q_st=128, q_sh=64, k_st=128, k_sh=64,
+                dq_st=128, dq_sh=64, dk_st=128, dk_sh=64, eps=1e-6, dtype=1, flags=0, workspace=_p(20), workspace_bytes=need,
+                stream=None)
+    own = {("dq", "dq_out"), ("dk", "dk_out")}
+    ins = ["q", "k", "wq", "wk", "inv_freq", "positions", "dq_out", "dk_out"]
+    _table(lib, "ssm_qk_norm_rope_bwd", BWD, base, [
+        ({o: base[i]}, INVALID, f"{o} aliases {i}") for o in ("dq", "dk", "dwq", "dwk", "workspace") for i in ins if (o, i) not in own
+    ] + [({"workspace": base[o]}, INVALID, "alias") for o in ("dq", "dk", "dwq", "dwk")])
+
+    base = {n: _p(i) for i, n in enumerate(ROPE[:8])}
+    base.update(n_tokens=4, n_heads=2, n_kv_heads=2, headdim=64, rot_dim=64, q_st=128, q_sh=64, k_st=128, k_sh=64,
+                eps=1e-6, dtype=1, flags=0, stream=None)
+    _table(lib, "ssm_qk_norm_rope_fwd", ROPE, base, [
+        ({o: base[i]}, INVALID, f"{o} aliases {i}") for o in ("q_out", "k_out") for i in ("wq", "wk", "inv_freq", "positions")])
+
+    base = {n: _p(i) for i, n in enumerate(CACHE[:11])}
+    base.update(n_tokens=4, n_heads=2, n_kv_heads=1, headdim=64, rot_dim=64, n_pages=8, page_size=16, q_st=256, q_sh=64,
+                k_st=256, k_sh=64, v_st=256, v_sh=64, c_sp=1024, c_st=64, c_sh=64, eps=1e-6, k_scale=1.0, v_scale=1.0, dtype=1,
+                kv_dtype=2, flags=0, stream=None)
+    _table(lib, "ssm_qk_norm_rope_cache_fwd", CACHE, base, [
+        ({o: base[i]}, INVALID, f"{o} aliases {i}") for o in ("q_out", "k_cache", "v_cache") for i in ("inv_freq", "positions", "slots")])
+
+    need = lib.ssm_paged_attn_decode_fwd_workspace_size(4, 8, 2, 64, 8, 16)
+    base = {n: _p(i) for i, n in enumerate(ATTN[:7])}
+    base.update(batch=4, n_heads=8, n_kv_heads=2, headdim=64, max_pages=8, table_stride=8, n_pages=32, page_size=16, q_sr=512,
+                q_sh=64, c_sp=2048, c_st=128, c_sh=64, scale=0.125, window=0, k_scale=1.0, v_scale=1.0, dtype=1, kv_dtype=1,
+                workspace=_p(20), workspace_bytes=need, stream=None)
+    _table(lib, "ssm_paged_attn_decode_fwd", ATTN, base, [
+        (dict(workspace=base[i]), INVALID, f"workspace aliases {i}") for i in ("q", "k_cache", "v_cache", "block_table", "lens")
+    ] + [(dict(workspace=base[o]), INVALID, "alias") for o in ("o", "lse")])

@@ -115,7 +115,8 @@ int ssm_qk_norm_rope_fwd(const void *q, const void *k, const float *wq, const fl
  * Layouts: q, k, dq_out, dk_out [dtype] strided; dq, dk [dtype] contiguous (dq
  * may be dq_out and dk may be dk_out where those are contiguous); dwq, dwk
  * (headdim) fp32, or NULL under SSM_QK_NO_NORM.  The sums are held in fp32 over
- * a block's tokens and joined in fp64, in an order fixed by the shape.
+ * at most 32 heads of a lane and over a block's lanes, and in fp64 else, in an
+ * order fixed by the shape: their error does not grow with the tokens.
  * Limits as for the forward.
  * Workspace: ssm_qk_norm_rope_bwd_workspace_size() bytes, 16-byte aligned (the
  * blocks' shares of dwq and dwk; 0 under SSM_QK_NO_NORM). */

@@ -46,6 +46,7 @@ constexpr int fwd_blocks(int esize, bool cache) { return esize == 2 && !cache ? 
 constexpr int kBwdWaves = 8;
 constexpr int kBwdBlocks = 2 * kCUs;
 constexpr int kOneWaves = 16;       // of the only block of a side
+constexpr int kChain = 32;          // heads of a lane whose shares of dw are added up in fp32 before they go on in fp64
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const bf16x2 r = __builtin_convertvector((f32x2){a, b}, bf16x2);   // to nearest even
@@ -179,6 +180,7 @@ struct Kp {
     int d, rot, units, lg;         // units of a head, log2 of its lanes
     float eps, inv_d, k_scale, v_scale;
     bool norm;
+    int sums;                      // backward, FOLD: where the sums in fp64 begin in LDS, in floats
 };
 
 // LDS of a wave is read by its own lanes: its instructions are in order, the compiler's
@@ -436,8 +438,11 @@ __global__ void __launch_bounds__(kFwdWaves * 64, fwd_blocks(sizeof(T), KV != 0)
 
 // The gradients.  A wave keeps its share of dw in registers (a lane's elements are the same
 // in every head); the shares of its lane groups are joined across lanes at the end, those of
-// the block's waves in LDS.
-template <typename T, int V, bool IL, int WAVES>
+// the block's waves in LDS.  FOLD: where a lane has more than kChain heads, what it has goes to a sum in
+// fp64 each time that it has so many, in its own part of LDS: the error of dw does not grow with the tokens.
+// (Tokens of 16 + 4 heads of 128, us without and with: 65536 in bf16 203.4, 203.7, in fp32 402.2, 403.7; of 3 + 1 heads
+// of 90, one element a lane, 300000 in bf16 580, 588.  The same tests in one kernel cost those that need none 1%.)
+template <typename T, int V, bool IL, int WAVES, bool FOLD>
 __global__ void __launch_bounds__(WAVES * 64, 4) qk_rope_bwd_kernel(Kp a) {
     typedef Lane<T, V, IL> L;
     constexpr int NU = L::NU;
@@ -451,6 +456,12 @@ __global__ void __launch_bounds__(WAVES * 64, 4) qk_rope_bwd_kernel(Kp a) {
     for (int n = 0; n < NU; ++n)
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) dw[n][i] = 0.0f;
+    double *sums = (double *)(tab + a.sums) + wave * (64 * NU * 2 * V) + me.lane;
+    if constexpr (FOLD) {
+#pragma unroll
+        for (int i = 0; i < NU * 2 * V; ++i) sums[i * 64] = 0.0;
+    }
+    int chain = 0;
     Walk at(s, (uint32_t)(blk * WAVES + wave));
     if (at.part < s.parts) {
         int pass = at.pass0;
@@ -507,6 +518,15 @@ __global__ void __launch_bounds__(WAVES * 64, 4) qk_rope_bwd_kernel(Kp a) {
                         dw[n][i] = fmaf(g[n][i], x[n][i] * r, dw[n][i]);
                         g[n][i] = r * fmaf(w[n][i], g[n][i], -x[n][i] * c);
                     }
+                if (FOLD && ++chain == kChain) {
+                    chain = 0;
+#pragma unroll
+                    for (int i = 0; i < NU * 2 * V; ++i) {
+                        float &v = dw[i / (2 * V)][i % (2 * V)];
+                        sums[i * 64] += (double)v;
+                        v = 0.0f;
+                    }
+                }
             }
             T *yp = (T *)s.y + ((int64_t)p.t * s.heads + p.h) * a.d;
 #pragma unroll
@@ -523,6 +543,13 @@ __global__ void __launch_bounds__(WAVES * 64, 4) qk_rope_bwd_kernel(Kp a) {
         }
     }
     if (!a.norm) return;
+    if constexpr (FOLD) {
+#pragma unroll
+        for (int i = 0; i < NU * 2 * V; ++i) {
+            float &v = dw[i / (2 * V)][i % (2 * V)];
+            v = (float)(sums[i * 64] + (double)v);
+        }
+    }
     __syncthreads();                             // the angles' last readers
 #pragma unroll
     for (int n = 0; n < NU; ++n)
@@ -646,14 +673,16 @@ void fwd_type(const Kp &k, unsigned blocks, size_t lds, bool bf16, int v, bool i
     }
 }
 
-template <typename T, int V, int WAVES>
+template <typename T, int V, int WAVES, bool FOLD>
 void bwd_waves_go(const Kp &k, unsigned blocks, bool il, size_t lds, hipStream_t stream) {
-    if (il) hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, true, WAVES>), dim3(blocks), dim3(WAVES * 64), lds, stream, k);
-    else hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, false, WAVES>), dim3(blocks), dim3(WAVES * 64), lds, stream, k);
+    if (il) hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, true, WAVES, FOLD>), dim3(blocks), dim3(WAVES * 64), lds, stream, k);
+    else hipLaunchKernelGGL((qk_rope_bwd_kernel<T, V, false, WAVES, FOLD>), dim3(blocks), dim3(WAVES * 64), lds, stream, k);
 }
 template <typename T, int V>
 void bwd_go(const Kp &k, unsigned blocks, bool one, bool il, size_t lds, hipStream_t stream) {
-    one ? bwd_waves_go<T, V, kOneWaves>(k, blocks, il, lds, stream) : bwd_waves_go<T, V, kBwdWaves>(k, blocks, il, lds, stream);
+    if (one) bwd_waves_go<T, V, kOneWaves, false>(k, blocks, il, lds, stream);
+    else if (k.sums) bwd_waves_go<T, V, kBwdWaves, true>(k, blocks, il, lds, stream);
+    else bwd_waves_go<T, V, kBwdWaves, false>(k, blocks, il, lds, stream);
 }
 
 }  // namespace
@@ -743,12 +772,17 @@ hipError_t launch_qk_rope_bwd(const QkRopeBwdArgs &a, hipStream_t stream, const 
     // call in one launch and in two: 4 tokens, 1 step 6.4 and 9.3; 8 tokens, 2 steps 7.6 and 9.2; 16 tokens, 4
     // steps 10.3 and 9.3.)
     const bool one = norm && a.n_tokens > 0 && deal(1, kOneWaves) <= 2;
-    if (!one) deal(kBwdBlocks, kBwdWaves);
+    const bool fold = !one && deal(kBwdBlocks, kBwdWaves) > kChain && norm;
     const int waves = one ? kOneWaves : kBwdWaves;
     float *ws = (float *)a.workspace;
     k.side[0].part = one ? a.dwq : ws;
     k.side[1].part = one ? a.dwk : norm ? ws + (int64_t)k.side[0].blocks * a.headdim : nullptr;
-    const size_t lds = std::max(table_bytes(k, waves), norm ? (size_t)waves * a.headdim * sizeof(float) : 0);
+    size_t lds = std::max(table_bytes(k, waves), norm ? (size_t)waves * a.headdim * sizeof(float) : 0);
+    if (fold) {                        // and at most 32 KiB of sums behind at most 16 KiB
+        lds = (lds + 15) / 16 * 16;
+        k.sums = (int)(lds / sizeof(float));
+        lds += (size_t)waves * 64 * (v == 4 ? 8 : 4) * sizeof(double);
+    }
     const unsigned blocks = (unsigned)(k.side[0].blocks + k.side[1].blocks);
     const bool il = (a.flags & SSM_ROPE_INTERLEAVED) != 0;
     if (blocks > 0) {

@@ -311,3 +311,29 @@ def test_on_a_stream_and_in_a_graph(cuda_device):
         torch.cuda.synchronize()
         for a, b in zip(have, outs + [out[n] for n in ("dq", "dk", "dwq", "dwk")]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,d,dtype,both", [(4_200_003, 256, "f32", False), (1_100_001, 255, "f32", True), (8_400_001, 256, "bf16", False)])
+def test_dw_of_millions_of_tokens(cuda_device, T, d, dtype, both):
+    """Every token alike (one row, expanded), not rotated: dw is T times one token's term, and fp32 additions of one
+    term, each rounded the same way for long, drift with their number.  A lane adds up hundreds of terms here.
+    Of those at most 32 in a row are fp32, then 6 of lane groups and 8 of waves, and a few roundings to and
+    from fp64: 50 u.  With x = 1 and eps = 0 a term is its cotangent itself; else it is within 40 u of itself."""
+    import torch
+    rng = np.random.default_rng(41)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    t = lambda a: torch.tensor(np.asarray(a, np.float32), device=cuda_device).to(dt)  # noqa: E731
+    x = t(np.ones((1, 1, d)) if dtype == "f32" else rng.standard_normal((1, 1, d)))
+    dy = t(rng.standard_normal((1, 1, d)))
+    w = torch.ones(d, device=cuda_device)
+    pos = torch.zeros(1, dtype=torch.int32, device=cuda_device).expand(T).contiguous()
+    xs, gs = x.expand(T, 1, d), dy.expand(T, 1, d)
+    out = {"dq": torch.empty((T, 1, d), dtype=dt, device=cuda_device)}
+    if both:
+        out["dk"] = torch.empty_like(out["dq"])
+    eps = 0.0 if dtype == "f32" else 1e-6
+    got = lib().ssm_qk_norm_rope_bwd(xs, xs if both else None, w, w if both else None, torch.zeros(0, device=cuda_device), pos, gs,
+                                     gs if both else None, eps=eps, out=out)
+    term = _n(dy)[0, 0] * _n(x)[0, 0] / np.sqrt((_n(x) ** 2).mean() + eps)
+    for n in ("dwq", "dwk") if both else ("dwq",):
+        _check("rope %s of %d tokens" % (n, T), got[n], T * term, (50 + (40 if dtype == "bf16" else 0)) * U * T * np.abs(term))

@@ -10,9 +10,8 @@ small compiled module (csrc/bind_attn.cpp), because these calls are short and fr
 from __future__ import annotations
 
 import ctypes
-import os
 
-from . import LIB_PATH, _I, _Z, _check, _lib
+from . import _I, _Z, _check, _lib
 
 __all__ = [
     "ssm_kv_pages_step", "ssm_qk_norm_rope_fwd", "ssm_qk_norm_rope_bwd", "ssm_qk_norm_rope_bwd_workspace_size",
@@ -20,12 +19,23 @@ __all__ = [
     "SSM_ROPE_INTERLEAVED", "SSM_QK_NO_NORM", "SSM_KV_F32", "SSM_KV_BF16", "SSM_KV_F8E4M3",
 ]
 
-_BIND_PATH = os.path.join(os.path.dirname(LIB_PATH), "_attn_bind.so")
-if not os.path.exists(_BIND_PATH):
-    raise ImportError(
-        f"{_BIND_PATH} is missing: build it with `python selective_state_space_s6_amd/build.py` "
-        "(there is no non-HIP fallback)")
-from . import _attn_bind as _bind  # noqa: E402
+
+class _NotLoaded:
+    """In the compiled module's place where that is missing or was built for another torch: the scans,
+    which do not need it, import all the same, and every call of this module raises."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"_attn_bind.so does not load ({self._why}): build it with `python "
+                          "selective_state_space_s6_amd/build.py` (there is no non-HIP fallback)") from self._why
+
+
+try:
+    from . import _attn_bind as _bind
+except ImportError as e:
+    _bind = _NotLoaded(e)
 
 SSM_ROPE_INTERLEAVED, SSM_QK_NO_NORM = 0x1, 0x2
 SSM_KV_F32, SSM_KV_BF16, SSM_KV_F8E4M3 = 0, 1, 2

@@ -4,10 +4,13 @@ compiled part of the Python binding (host code only, against torch's headers).
 Usage: python selective_state_space_s6_amd/build.py   (or __graft_entry__.build())
 Each source is compiled to an object in parallel, then linked into a shared
 library next to this file.  Always recompiles (no staleness heuristics).
+libssmscan.so needs hipcc alone and is linked first; where torch is not installed it is all
+that is built.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -75,18 +78,19 @@ def build(verbose: bool = True) -> str:
     objs = [os.path.join(objdir, s.replace(".hip", ".o")) for s in SOURCES]
     bind_obj = os.path.join(objdir, "bind_attn.o")
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
-        bind = ex.submit(_compile_bind, bind_obj)
+        bind = ex.submit(_compile_bind, bind_obj) if importlib.util.find_spec("torch") else None
         list(ex.map(lambda so: _compile(*so), zip(SOURCES, objs)))
-        bind.result()
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_bind(bind_obj)
+    if bind:
+        bind.result()
+        _link_bind(bind_obj)
     if verbose:
-        print(f"built {LIB}, {BIND}")
+        print(f"built {LIB}, " + (BIND if bind else "and no _attn_bind.so: torch is not installed"))
     return LIB
 
 

@@ -7,7 +7,10 @@ cache pages and maps the step's tokens to slots, the norm and rotation of q and 
 cache, attention reads it, and the SSD scan carries its state.  A step of one token a
 request copies nothing to the host: lengths, tables and slots stay on the device.
 
-  python examples/hybrid_decode.py [--steps 12] [--cache bf16|f8] [--check]
+A request that the free pages do not cover is refused for the step: its tokens are in no
+cache and change no state, and the loop offers them again in the next one.
+
+  python examples/hybrid_decode.py [--steps 12] [--cache bf16|f8] [--pages 20] [--check]
 
 --check recomputes every request from scratch in fp64 (dense causal attention, the
 sequential recurrence) and prints how far the served hidden states are from that.
@@ -81,17 +84,20 @@ class Server:
         """Requests are to hold `hold` (batch,) int32 tokens: 0 ends one, and the grown ones'
         new tokens stand in `tokens` one request after the other (one_each: one of each
         request).  Returns the hidden states of the new tokens and the step's maps.  A prompt is
-        a growth of many tokens."""
+        a growth of many tokens.  A refused request (m["len"] is not what it was to hold) keeps its
+        pages and its states, and the hidden states of its tokens mean nothing."""
         grown = self.held
         m = lib.ssm_kv_pages_step(self.held, hold, self.table, self.free_ring, self.ring, page_size=PAGE,
                                   n_tokens=len(tokens))
         self.held, self.ring = m["len"], m["ring"]
         request = m["request"].long()
-        table, lens = self.table[request], m["positions"] + 1      # a row of attention for each token
+        held = m["slots"] >= 0                                       # (not of a refused request)
+        # a row of attention for each token; none of a refused one, whose further pages it does not have
+        table, lens = self.table[request], torch.where(held, m["positions"] + 1, 0).int()
         x = self.w["embed"][tokens]
         for w, state in zip(self.w["layers"], self.layers):
             u = rms(x) @ w["in"].T
-            x = x + (self.ssm(w, u, state, None if one_each else m["starts"].tolist(), grown) if "A_log" in w else
+            x = x + (self.ssm(w, u, state, None if one_each else m["starts"].tolist(), grown, held) if "A_log" in w else
                      self.attention(w, u, state, m, table, lens)) @ w["out"].T
         return x, m
 
@@ -104,21 +110,23 @@ class Server:
         o = lib.ssm_paged_attn_decode_fwd(q, kv[0], kv[1], table, lens, scale=HD ** -0.5, k_scale=s, v_scale=s)
         return o.flatten(1).float()
 
-    def ssm(self, w, u, state, starts, grown):
+    def ssm(self, w, u, state, starts, grown, held):
         """One call for all requests where each has one new token (starts is None), else a call
-        for each of them."""
+        for each of them.  A refused request's tokens are steps of no length, which leave its state as it is."""
         x, b, c, dt = split_ssm(u)
+        dt = torch.where(held[:, None], dt, -1e4)       # softplus: 0
         scan = lambda s, h, t: lib.ssd_chunk_scan_fwd(  # noqa: E731
             x[s].view(h.shape[0], t, SH, SP), dt[s].view(-1, t, SH), w["dt_bias"], w["A_log"], b[s].view(-1, t, 1, SN),
             c[s].view(-1, t, 1, SN), w["D"], h, h_final=h)[0]
         n = len(u)
         if starts is None:
+            state.mul_((grown > 0)[:, None, None, None])                    # a new request starts from zero
             return scan(slice(0, n), state, 1).flatten(1).view(n, -1)
         y = torch.empty((n, SH * SP), device=self.dev)
         for r in range(len(state)):
             lo, hi = starts[r], starts[r + 1]
             if hi > lo:
-                h = state[r:r + 1].contiguous() * (grown[r] > 0)       # a new request starts from zero
+                h = state[r:r + 1].contiguous() * (grown[r] > 0)
                 y[lo:hi] = scan(slice(lo, hi), h, hi - lo).view(hi - lo, -1)
                 state[r] = h[0]
         return y
@@ -166,16 +174,16 @@ def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=12)
     ap.add_argument("--cache", choices=("bf16", "f8"), default="bf16")
+    ap.add_argument("--pages", type=int, default=20)
     ap.add_argument("--check", action="store_true")
     a = ap.parse_args(argv)
     batch = 4
-    sv = Server(batch, n_pages=20, cache=a.cache)
+    sv = Server(batch, n_pages=a.pages, cache=a.cache)
     g = torch.Generator().manual_seed(1)
     draw = lambda n: torch.randint(VOCAB, (n,), generator=g).tolist()  # noqa: E731
-    said = [draw(n) for n in (21, 1, 34, 16)]            # prompts; what each place's request holds
+    said = [[] for _ in range(batch)]                    # what each place's request holds
+    new = [draw(n) for n in (21, 1, 34, 16)]             # and what comes to it next: a prompt, or a token
     hidden = [[] for _ in range(batch)]
-    hold = [len(s) for s in said]
-    feed = [t for s in said for t in s]
     worst = 0.0
 
     def check(r):
@@ -184,34 +192,24 @@ def main(argv=None):
         return float((got.double() - want).norm() / want.norm())
 
     for step in range(a.steps + 1):
-        grown = [h - (len(s) if step else 0) for h, s in zip(hold, said)]
-        x, m = sv.step(torch.tensor(hold, dtype=torch.int32, device=sv.dev), torch.tensor(feed, device=sv.dev),
-                       one_each=all(n == 1 for n in grown))
-        if step:
-            at = 0
-            for r in range(batch):
-                if hold[r] == 0:
-                    said[r] = []
-                elif grown[r] > 0:
-                    said[r] = said[r] + feed[at:at + grown[r]]
-                    at += grown[r]
-        for r, part in enumerate(x.split([max(0, h) for h in (hold if step == 0 else grown)])):
-            hidden[r] = [] if hold[r] == 0 else hidden[r] + [part]
-        # next: the likeliest token of each request; the second one ends after five steps and its
-        # place goes to a new prompt the step after
-        starts = m["starts"].tolist()
+        hold = [len(s) + len(n) if n else 0 for s, n in zip(said, new)]          # nothing new: it ends
+        x, m = sv.step(torch.tensor(hold, dtype=torch.int32, device=sv.dev),
+                       torch.tensor([t for n in new for t in n], device=sv.dev), one_each=all(len(n) == 1 for n in new))
+        # next: the likeliest token of each request (of a refused one, the same again); the second one
+        # ends after five steps and its place goes to a new prompt the step after
+        starts, held = m["starts"].tolist(), sv.held.tolist()
         logits = x @ sv.w["embed"].T
-        hold, feed = [], []
-        for r in range(batch):
+        for r, part in enumerate(x.split([len(n) for n in new])):
+            if not new[r]:
+                said[r], hidden[r], new[r] = [], [], draw(19)
+            elif held[r] == hold[r]:
+                said[r], hidden[r] = said[r] + new[r], hidden[r] + [part]
+                new[r] = [int(logits[starts[r + 1] - 1].argmax())]
             if step == 5 and r == 1:
-                if a.check:
+                if a.check and said[r]:
                     worst = max(worst, check(r))
-                hold.append(0)
-                continue
-            new = draw(19) if not said[r] else [int(logits[starts[r + 1] - 1].argmax())]
-            hold.append(len(said[r]) + len(new))
-            feed += new
-        print(f"step {step}: {starts[-1]} new tokens, held {sv.held.tolist()}, free pages {int(sv.ring[1])}, "
+                new[r] = []
+        print(f"step {step}: {starts[-1]} new tokens, held {held}, free pages {int(sv.ring[1])}, "
               f"refused {int(m['denied'])}", flush=True)
     if a.check:
         worst = max([worst] + [check(r) for r in range(batch) if said[r]])

@@ -207,8 +207,14 @@ PyObject *pages_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
         auto *p_ring = (const int32_t *)c.whole(a[4], "ring", i32, {2});
         const hipStream_t stream = c.stream();
         const int64_t room = tokens > 0 ? tokens : 0;
-        const auto [slots, request, positions, len, starts, ring_out, denied] = c.make_together<7>(
-            {{ScalarType::Long, {room}}, {i32, {room}}, {i32, {room}}, {i32, {batch}}, {i32, {batch + 1}}, {i32, {2}}, {i32, {1}}});
+        Tensor slots, request, positions, len, starts, ring_out, denied;
+        if (c.few(4 * room)) {
+            std::tie(slots, request, positions, len, starts, ring_out, denied) = std::tuple_cat(c.make_together<7>(
+                {{ScalarType::Long, {room}}, {i32, {room}}, {i32, {room}}, {i32, {batch}}, {i32, {batch + 1}}, {i32, {2}}, {i32, {1}}}));
+        } else {    // len and ring go on to the next step, the tokens' maps need not
+            std::tie(slots, request, positions) = std::tuple_cat(c.make_together<3>({{ScalarType::Long, {room}}, {i32, {room}}, {i32, {room}}}));
+            std::tie(len, starts, ring_out, denied) = std::tuple_cat(c.make_together<4>({{i32, {batch}}, {i32, {batch + 1}}, {i32, {2}}, {i32, {1}}}));
+        }
         const int rc = ssm_kv_pages_step(
             p_old, p_new, p_table, p_free, p_ring, (int32_t *)ring_out.data_ptr(), (int32_t *)len.data_ptr(),
             (int32_t *)starts.data_ptr(), (int32_t *)request.data_ptr(), (int32_t *)positions.data_ptr(),
@@ -410,7 +416,7 @@ PyObject *attn_decode_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t window = whole_number(a[6], "window");
         const bool want_lse = a[11] != Py_None || PyObject_IsTrue(a[9]) == 1;
         Tensor o, lse;
-        if (want_lse && a[10] == Py_None && a[11] == Py_None) {
+        if (want_lse && a[10] == Py_None && a[11] == Py_None && c.few(B * H * d)) {
             std::tie(o, lse) = std::tuple_cat(c.make_together<2>({{type, {B, H, d}}, {ScalarType::Float, {B, H}}}));
         } else {
             o = c.out(a[10], "o", type, {B, H, d});

@@ -97,3 +97,18 @@ def test_pages_many_steps_as_a_program_runs_them(cuda_device):
         g_held, g_ring = got["len"], got["ring"]
         _same({k: v.cpu().numpy().astype(np.int64) for k, v in dict(got, block_table=g_table, free_ring=g_place).items()}, want)
         held, table, place, ring = want["len"], want["block_table"], want["free_ring"], want["ring"]
+
+
+def test_what_goes_on_to_the_next_step_holds_little_memory(cuda_device):
+    """len, ring, starts and denied of a step with a million new tokens (16 MB of maps) share their memory with
+    each other at most, and with no more than 4 MiB of maps where those are smaller."""
+    import torch
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    for n in (1 << 20, 1 << 12):
+        pages = n // 256 + 2
+        got = lib().ssm_kv_pages_step(i32([0, 3]), i32([n, 4]), torch.zeros((2, pages), dtype=torch.int32, device=cuda_device),
+                                      torch.arange(pages, dtype=torch.int32, device=cuda_device), i32([0, pages]), page_size=256, n_tokens=n + 1)
+        assert got["len"].tolist() == [n, 4] and got["starts"].tolist() == [0, n, n + 1] and got["denied"].tolist() == [0]
+        assert got["positions"][[0, n - 1, n]].tolist() == [0, n - 1, 3] and got["request"][[0, n]].tolist() == [0, 1]
+        for k in ("len", "ring", "starts", "denied"):
+            assert got[k].untyped_storage().nbytes() <= (4096 if n == 1 << 20 else (4 << 20) + 4096), (n, k)

@@ -341,3 +341,14 @@ def test_the_weights_bits_cancel_where_v_does(cuda_device, H, Hk, d, cache, cols
     worst = float((np.abs(_n(o) - want[..., None]) / tol[..., None]).max())
     report("attn weights %s" % ((H, Hk, d, cache, cols),), of_bound=worst)
     assert worst <= 1.0
+
+
+def test_lse_does_not_hold_a_large_output(cuda_device):
+    """lse kept for a later join: its memory is its own where o is over 4 MiB."""
+    import torch
+    for B in (20, 4000):
+        q, kc, vc, table, lens, s = _make(cuda_device, 12, [3] * B, 8, 2, 128, "bf16", 16, "nhd")
+        o, lse = _run(cuda_device, q, kc, vc, table, lens, 0.1, s)
+        assert lse.untyped_storage().nbytes() <= (B * 8 * 4 + 512 if B == 4000 else (4 << 20) + B * 8 * 4 + 512)
+        a, _ = _run(cuda_device, q, kc, vc, table, lens, 0.1, s, o=torch.empty_like(q))
+        assert torch.equal(a, o)

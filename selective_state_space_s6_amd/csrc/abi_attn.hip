@@ -43,6 +43,11 @@ int check_element(const char *E, const void *p, const char *name, int esize) {
     return SSM_OK;
 }
 
+// heads (n_tokens, n_heads, headdim) without a gap; strides of a dim of one entry are not used
+bool gapless(int64_t n_tokens, int64_t n_heads, int64_t headdim, int64_t st, int64_t sh) {
+    return (n_heads == 1 || sh == headdim) && (n_tokens == 1 || st == n_heads * headdim);
+}
+
 // what the norm and rotation entry points have in common; n_kv_heads may be 0
 int check_rope(const char *E, const void *q, const void *k, const float *wq, const float *wk, const float *inv_freq,
                const int32_t *positions, int64_t n_tokens, int64_t n_heads, int64_t n_kv_heads, int64_t headdim,
@@ -142,9 +147,9 @@ int ssm_qk_norm_rope_fwd(const void *q, const void *k, const float *wq, const fl
     for (const Named &t : ts)
         if ((rc = check_element(E, t.p, t.name, es)) != SSM_OK) return rc;
     // in place only where the layout is the output's
-    if (q_out == q && (q_stride_head != headdim || q_stride_token != n_heads * headdim))
+    if (q_out == q && !gapless(n_tokens, n_heads, headdim, q_stride_token, q_stride_head))
         return fail(SSM_ERR_INVALID_ARG, "%s: q_out aliases a q that is not contiguous", E);
-    if (n_kv_heads > 0 && k_out == k && (k_stride_head != headdim || k_stride_token != n_kv_heads * headdim))
+    if (n_kv_heads > 0 && k_out == k && !gapless(n_tokens, n_kv_heads, headdim, k_stride_token, k_stride_head))
         return fail(SSM_ERR_INVALID_ARG, "%s: k_out aliases a k that is not contiguous", E);
     if (n_kv_heads > 0 && (q_out == k || k_out == q || q_out == k_out))
         return fail(SSM_ERR_INVALID_ARG, "%s: an output aliases the other tensor", E);
@@ -199,9 +204,9 @@ int ssm_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const fl
     const Named ts[] = {{q, "q"}, {k, "k"}, {dq_out, "dq_out"}, {dk_out, "dk_out"}, {dq, "dq"}, {dk, "dk"}};
     for (const Named &t : ts)
         if ((rc = check_element(E, t.p, t.name, es)) != SSM_OK) return rc;
-    if (n_tokens > 0 && dq == dq_out && (dq_stride_head != headdim || dq_stride_token != n_heads * headdim))
+    if (n_tokens > 0 && dq == dq_out && !gapless(n_tokens, n_heads, headdim, dq_stride_token, dq_stride_head))
         return fail(SSM_ERR_INVALID_ARG, "%s: dq aliases a dq_out that is not contiguous", E);
-    if (n_tokens > 0 && has_k && dk == dk_out && (dk_stride_head != headdim || dk_stride_token != n_kv_heads * headdim))
+    if (n_tokens > 0 && has_k && dk == dk_out && !gapless(n_tokens, n_kv_heads, headdim, dk_stride_token, dk_stride_head))
         return fail(SSM_ERR_INVALID_ARG, "%s: dk aliases a dk_out that is not contiguous", E);
     const size_t need = ssm_qk_norm_rope_bwd_workspace_size(n_tokens, n_heads, n_kv_heads, headdim, flags);
     const Named outs[] = {{dq, "dq"}, {has_k ? dk : nullptr, "dk"}, {norm ? dwq : nullptr, "dwq"},
@@ -260,7 +265,7 @@ int ssm_qk_norm_rope_cache_fwd(const void *q, const void *k, const void *v, cons
         if ((rc = check_element(E, t.p, t.name, es)) != SSM_OK) return rc;
     if ((rc = check_element(E, k_cache, "k_cache", ce)) != SSM_OK) return rc;
     if ((rc = check_element(E, v_cache, "v_cache", ce)) != SSM_OK) return rc;
-    if (q_out == q && (q_stride_head != headdim || q_stride_token != n_heads * headdim))
+    if (q_out == q && !gapless(n_tokens, n_heads, headdim, q_stride_token, q_stride_head))
         return fail(SSM_ERR_INVALID_ARG, "%s: q_out aliases a q that is not contiguous", E);
     const Named outs[] = {{q_out, "q_out"}, {k_cache, "k_cache"}, {v_cache, "v_cache"}};
     const bool norm = (flags & SSM_QK_NO_NORM) == 0;

@@ -337,3 +337,28 @@ def test_dw_of_millions_of_tokens(cuda_device, T, d, dtype, both):
     term = _n(dy)[0, 0] * _n(x)[0, 0] / np.sqrt((_n(x) ** 2).mean() + eps)
     for n in ("dwq", "dwk") if both else ("dwq",):
         _check("rope %s of %d tokens" % (n, T), got[n], T * term, (50 + (40 if dtype == "bf16" else 0)) * U * T * np.abs(term))
+
+
+def test_in_place_where_a_dim_has_one_entry(cuda_device):
+    """Contiguous as torch counts it: the stride of a token or a head that is alone means nothing."""
+    import torch
+    m = lib()
+    gen = torch.Generator(device=cuda_device).manual_seed(51)
+    r = lambda *s: torch.randn(s, generator=gen, device=cuda_device).to(torch.bfloat16)  # noqa: E731
+    w, f = torch.rand(64, device=cuda_device) + 0.5, torch.rand(32, device=cuda_device)
+    for T, H, Hk in ((1, 4, 2), (9, 1, 1), (1, 1, 1)):
+        pos = torch.arange(T, dtype=torch.int32, device=cuda_device)
+        make = (lambda h: r(1, 7, 64)[:, :h]) if T == 1 else (lambda h: r(T, 64).as_strided((T, 1, 64), (64, 1000, 1)))
+        q, k, gq, gk = make(H), make(Hk), make(H), make(Hk)
+        assert q.is_contiguous() and (q.stride(0) != H * 64 or q.stride(1) != 64)
+        want = m.ssm_qk_norm_rope_fwd(q, k, w, w, f, pos)
+        grads = m.ssm_qk_norm_rope_bwd(q, k, w, w, f, pos, gq, gk)
+        got = m.ssm_qk_norm_rope_bwd(q, k, w, w, f, pos, gq, gk, out={"dq": gq, "dk": gk})
+        assert got["dq"].data_ptr() == gq.data_ptr() and all(torch.equal(got[n], grads[n]) for n in grads)
+        cache = [torch.zeros((1, 16, Hk, 64), dtype=torch.bfloat16, device=cuda_device) for _ in range(2)]
+        qc = q.clone()
+        assert qc.stride() == q.stride()
+        a = m.ssm_qk_norm_rope_cache_fwd(qc, k, k, w, w, f, pos, pos.long(), *cache, q_out=qc)
+        assert a.data_ptr() == qc.data_ptr() and torch.equal(a, want[0])
+        a, b = m.ssm_qk_norm_rope_fwd(q, k, w, w, f, pos, q_out=q, k_out=k)
+        assert a.data_ptr() == q.data_ptr() and torch.equal(a, want[0]) and torch.equal(b, want[1])

@@ -414,7 +414,9 @@ PyObject *attn_decode_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
         auto *pl = (const int32_t *)c.whole(a[4], "lens", ScalarType::Int, {B});
         const float scale = number(a[5], "scale"), k_scale = number(a[7], "k_scale"), v_scale = number(a[8], "v_scale");
         const int64_t window = whole_number(a[6], "window");
-        const bool want_lse = a[11] != Py_None || PyObject_IsTrue(a[9]) == 1;
+        const int asked = PyObject_IsTrue(a[9]);
+        if (asked < 0) throw Refused{};          // with the error that its truth raised
+        const bool want_lse = a[11] != Py_None || asked == 1;
         Tensor o, lse;
         if (want_lse && a[10] == Py_None && a[11] == Py_None && c.few(B * H * d)) {
             std::tie(o, lse) = std::tuple_cat(c.make_together<2>({{type, {B, H, d}}, {ScalarType::Float, {B, H}}}));

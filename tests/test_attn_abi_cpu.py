@@ -267,3 +267,11 @@ def test_no_output_on_an_input_of_the_other_side(lib):
     _table(lib, "ssm_paged_attn_decode_fwd", ATTN, base, [
         (dict(workspace=base[i]), INVALID, f"workspace aliases {i}") for i in ("q", "k_cache", "v_cache", "block_table", "lens")
     ] + [(dict(workspace=base[o]), INVALID, "alias") for o in ("o", "lse")])
+
+
+def test_return_lse_that_is_no_truth_value(m):
+    """A flag whose truth raises passes its own error on, not one about something else."""
+    z = lambda *s, t=torch.float32: torch.zeros(s, dtype=t)  # noqa: E731
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        m.ssm_paged_attn_decode_fwd(z(2, 2, 8), z(4, 16, 1, 8), z(4, 16, 1, 8), z(2, 5, t=torch.int32), z(2, t=torch.int32), scale=1.0,
+                                    return_lse=z(2))

@@ -352,3 +352,30 @@ def test_lse_does_not_hold_a_large_output(cuda_device):
         assert lse.untyped_storage().nbytes() <= (B * 8 * 4 + 512 if B == 4000 else (4 << 20) + B * 8 * 4 + 512)
         a, _ = _run(cuda_device, q, kc, vc, table, lens, 0.1, s, o=torch.empty_like(q))
         assert torch.equal(a, o)
+
+
+LSE_CASES = [CASES[i] for i in (1, 5, 9, 12, 16, 18, 23, 24, 28, 30, 34, 37, 39, 43)] + [([n], 8, 2, 128, c, 16, "nhd", 0) for n in (0, 1, 700, 6400) for c in ("bf16", "f8", "f32")]
+
+
+@pytest.mark.parametrize("case", LSE_CASES, ids=lambda c: "%d-%d-H%d-%d-d%d-%s-p%d-%s-w%d" % ((len(c[0]), max(c[0])) + c[1:]))
+def test_lse_is_finite_where_it_should_be(cuda_device, case):
+    """lse alone, with a workspace that holds NaN before the call: -inf where a row has no token and nowhere else,
+    finite elsewhere, and all of it within its bound (a NaN is within none)."""
+    import torch
+    lens, H, Hk, d, cache, ps, layout, window = case
+    q, kc, vc, table, lens, s = _make(cuda_device, 60 + d, lens, H, Hk, d, cache, ps, layout, cols=400 if len(lens) == 1 and lens[0] < 7000 else None)
+    ws = torch.full((lib().ssm_paged_attn_decode_fwd_workspace_size(len(lens), H, Hk, d, table.shape[1], ps),), 255, dtype=torch.uint8,
+                    device=cuda_device)
+    sc = d ** -0.5
+    got = _n(_run(cuda_device, q, kc, vc, table, lens, sc, s, window, workspace=ws)[1])
+    k64 = _n(kc) * s
+    _, want = paged.paged_attn_decode(_n(q), k64, _n(vc) * s, table, lens, sc, window)
+    assert (np.isfinite(got) == np.isfinite(want)).all() and (np.isneginf(got) == np.isneginf(want)).all()
+    n = np.minimum(np.maximum(lens, 0), table.shape[1] * ps)[:, None]
+    # |s| <= scale |k| |q| of the largest cached row (rows that no request holds are NaN)
+    big = abs(sc) * np.sqrt(np.nan_to_num((k64 ** 2).sum(-1)).max()) * np.sqrt((_n(q) ** 2).sum(-1))
+    tol = 2 * (d + 6) * U * big + 4 * U + n * U + 4 * U * np.abs(np.where(np.isfinite(want), want, 0.0))
+    there = np.isfinite(want)
+    ratio = np.abs(got[there] - want[there]) / tol[there]
+    report("attn lse %s" % (case[1:],), of_bound=float(ratio.max()) if ratio.size else 0.0)
+    assert (ratio <= 1.0).all()

@@ -91,8 +91,8 @@ int ssm_kv_pages_step(const int32_t *len_old, const int32_t *len_new, int32_t *b
  *   (out[a], out[b]) = (y[a] cos theta_j - y[b] sin theta_j, y[b] cos theta_j + y[a] sin theta_j)
  * with (a, b) = (j, j + rot_dim/2), or (2j, 2j+1) under SSM_ROPE_INTERLEAVED;
  * out = y from rot_dim on.  w is wq for q heads and wk for k heads.
- * Arithmetic: fp32, the angle reduced to a turn in fp64 (positions of any size
- * keep fp32 accuracy), outputs rounded once.
+ * Arithmetic: fp32, the angle formed and reduced to a turn in fp64 (off by 2^-24
+ * at most at positions up to 2^28, by 5e-7 at 2^31), outputs rounded once.
  *
  * Layouts: q (n_tokens, n_heads, headdim), k (n_tokens, n_kv_heads, headdim)
  * [dtype] with the given strides; wq, wk (headdim) fp32; inv_freq (rot_dim/2)

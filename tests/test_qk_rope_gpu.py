@@ -362,3 +362,29 @@ def test_in_place_where_a_dim_has_one_entry(cuda_device):
         assert a.data_ptr() == qc.data_ptr() and torch.equal(a, want[0])
         a, b = m.ssm_qk_norm_rope_fwd(q, k, w, w, f, pos, q_out=q, k_out=k)
         assert a.data_ptr() == q.data_ptr() and torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
+@pytest.mark.parametrize("il", [False, True])
+def test_far_and_negative_positions(cuda_device, il):
+    """Positions up to the ends of 32 bits.  Formed and reduced in fp64, an angle there is off by up to 2^-53 of
+    the product's three roundings each: 3 * 2^-53 * 2^31 = 12 u, beside the 32 u of the rest."""
+    import torch
+    T, H, d = 64, 2, 64
+    rng = np.random.default_rng(61)
+    q = torch.tensor(rng.standard_normal((T, H, d)), dtype=torch.float32, device=cuda_device)
+    w = torch.tensor(rng.normal(1, 0.1, d), dtype=torch.float32, device=cuda_device)
+    f = torch.tensor(1e4 ** (-np.arange(d // 2) / (d // 2)), dtype=torch.float32, device=cuda_device)
+    at = np.concatenate([2 ** 31 - 1 - np.arange(24), -2 ** 31 + np.arange(16), -np.arange(12), 2 ** np.arange(12, 24)])
+    pos = torch.tensor(at, dtype=torch.int32, device=cuda_device)
+    m = lib()
+    y, _ = m.ssm_qk_norm_rope_fwd(q, None, w, None, f, pos, flags=m.SSM_ROPE_INTERLEAVED if il else 0)
+    # the angle's whole turns taken off in more than 64 bits before the oracle's cosines
+    turn = np.longdouble(2) * np.arctan2(np.longdouble(0), np.longdouble(-1))
+    th = np.asarray(at, np.longdouble)[:, None] * _n(f).astype(np.longdouble)[None]
+    th = (th - turn * np.rint(th / turn)).astype(np.float64)[:, None]
+    flat = paged.qk_norm_rope(_n(q), _n(w), _n(f), 0 * _n(pos), interleaved=il)
+    a, b = (slice(0, d, 2), slice(1, d, 2)) if il else (slice(0, d // 2), slice(d // 2, d))
+    want = flat.copy()
+    want[..., a] = flat[..., a] * np.cos(th) - flat[..., b] * np.sin(th)
+    want[..., b] = flat[..., b] * np.cos(th) + flat[..., a] * np.sin(th)
+    _check("rope far positions %d" % il, y, want, (32 + 12) * U * _pair(flat.copy(), d, il))

@@ -388,3 +388,26 @@ def test_far_and_negative_positions(cuda_device, il):
     want[..., a] = flat[..., a] * np.cos(th) - flat[..., b] * np.sin(th)
     want[..., b] = flat[..., b] * np.cos(th) + flat[..., a] * np.sin(th)
     _check("rope far positions %d" % il, y, want, (32 + 12) * U * _pair(flat.copy(), d, il))
+
+
+def test_backward_of_lanes_with_many_heads(cuda_device):
+    """More than 32 heads a lane with tokens that differ, turned (one element a lane): bounds as of the other shapes,
+    and twice the same; and of tokens alike (vectors of four) every row of dq the same and within its bound."""
+    import torch
+    case = (80000, 6, 3, 31, 10, "bf16", False, True)
+    test_backward(cuda_device, case)
+    q, k, v, w, f, pos, g, flags = _make(case, cuda_device, 2)
+    a, b = (lib().ssm_qk_norm_rope_bwd(q, k, w[0], w[1], f, pos, g[0], g[1]) for _ in range(2))
+    assert all(torch.equal(a[n], b[n]) for n in a)
+
+    q, k, v, w, f, pos, g, flags = _make((1, 1, 1, 64, 32, "f32", True, True), cuda_device, 3)
+    T = 1_000_000
+    row = lambda t: t.expand(T, -1, -1)  # noqa: E731
+    got = lib().ssm_qk_norm_rope_bwd(row(q), row(k), w[0], w[1], f, pos.expand(T).contiguous(), row(g[0]), row(g[1]), flags=flags)
+    for n, x, wx, gx in (("q", q, w[0], g[0]), ("k", k, w[1], g[1])):
+        dx, _ = paged.qk_norm_rope_bwd(_n(x), _n(wx), _n(f), _n(pos), _n(gx), interleaved=True)
+        size = _pair(np.abs(_n(gx)), 32, True)
+        r = 1.0 / np.sqrt((_n(x) ** 2).mean(-1, keepdims=True) + 1e-6)
+        wg, nx = np.abs(_n(wx)) * size, np.abs(_n(x)) * r
+        assert (got["d" + n] == got["d" + n][:1]).all()
+        _check("rope alike d" + n, got["d" + n][:1], dx, 64 * U * r * (wg + nx * (wg * nx).mean(-1, keepdims=True)))

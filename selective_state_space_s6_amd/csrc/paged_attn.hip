@@ -30,7 +30,7 @@
 // Measured (both kernels): 64 rows of up to 8192 tokens, 32 + 8 heads of 128, bf16, 1.06 GB of
 // cache 205 us (5.2 TB/s; the counters show those bytes fetched and no others); 16 rows of 65536,
 // 64 + 8 heads of 128, 8 bits, 2.15 GB 370 us (5.8 TB/s); 48 rows of up to 5000 tokens, 5 + 1
-// heads of 256, fp32, 234 MB 62 us (3.8 TB/s, 6 of it the join); one row of 2047 tokens 10 us, two
+// heads of 256, fp32, 234 MB 62 us (3.8 TB/s, 6 of it the join); one row of 2047 tokens 9.9 us, two
 // launches that each wait for a few loads in a chain (lengths, pages, K, V).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -120,14 +120,14 @@ __device__ __forceinline__ float head_sum(float v) {
     return v + __shfl_xor(v, 32);
 }
 
-// waves on one of a compute unit's 4 SIMDs, for heads of up to dp (why: Tile::PER_SIMD)
+// waves on one of a compute unit's 4 SIMDs that the work is cut for, for heads of up to dp (why: Tile::PER_SIMD)
 constexpr int per_simd(int dp) { return dp <= 64 ? 3 : dp <= 128 ? 2 : 1; }
 // One (cache type, padded head size): register shapes of a tile
 template <int CT, int DP, int W> struct Tile {
     static constexpr int E = CT == KF32 ? 4 : CT == KBF16 ? 2 : 1;
-    // tokens: about 8 KiB of K (and of V), so that a wave has that much on its way at any time.  (8-bit heads of
-    // 256 in tiles of 64 and of 32 tokens: 1 row of 600 15.1 and 11.4 us, 78 rows of up to 600 25.0 and 18.5, 10 of
-    // 16000 73.9 and 77.3.)
+    // tokens: 4 to 16 KiB of K (and of V), 8 most often, that a wave has on its way at any time.  (8-bit heads of
+    // 256 in tiles of 64 and of 32 tokens: 1 row of 600 15.8 and 11.9 us, 78 rows of up to 600 26.4 and 19.1, 10 of
+    // 16000 73.3 and 76.0.)
     static constexpr int NT = CT == KF32 ? (DP <= 64 ? 32 : 16) : CT == KBF16 ? (DP <= 64 ? 64 : 32) : DP > 128 ? 32 : 64;
     static constexpr int SUB = NT / 16;                        // 16-token blocks of scores
     static constexpr int KD = 16 / E;                          // dims of a 16-byte load of K
@@ -138,11 +138,18 @@ template <int CT, int DP, int W> struct Tile {
     static constexpr int VR = NT / 4;                          // V rows of a lane
     static constexpr int QW = CT == KF8 ? 2 : 1;               // operands of q to a K load
     static constexpr int UNIT = W * NT;
-    // resident blocks of a compute unit, by the registers of a tile's K, V and output (and of q,
-    // which waits in LDS where those leave it no room).  Heads of 256 on 2 waves a SIMD would spill:
-    // fp32 118 us against 58; of 128 on 3 do a little: 64 rows of up to 16000 tokens, 8 kv heads in 8 bits 228 us on 2
-    // and 234 on 3, of up to 2000 32 and 41; bf16 374 and 375; 59 and 60.  Heads of 64 do not: in 8 bits 16000 tokens
-    // each 222 us on 2, 201 on 3, bf16 411 and 360, fp32 713 and 675, up to 16000 bf16 224 and 212.
+    // blocks of a compute unit that the work is cut for, by the registers of a tile's K, V and output (and of q,
+    // which waits in LDS where those leave it no room).
+    //  - Up to 64: 3 waves a SIMD, at most 168 registers; fp32 and four-wave bf16 kernels spill 12 to 20 bytes a lane
+    //    for it.  8 kv heads of 64, 16000 tokens each, us on 2 and on 3: 8 bits 222, 201; bf16 411, 360; fp32 713, 675.
+    //  - Up to 128: 2.  3 spill: 64 rows of up to 16000 tokens, 8 kv heads in 8 bits 228 us on 2 and 234 on 3, of up
+    //    to 2000 32 and 41; bf16 374 and 375; 59 and 60.
+    //  - Above: 1.  fp32 heads of 256 would spill 250 bytes on 2 (118 us against 58), bf16 ones 170.  8-bit heads, and
+    //    bf16 ones of up to 192, have room for 2 as they are compiled (202 to 256 registers), so a second block may
+    //    well run beside the first, but twice the pieces gain as often as they lose: us on 1 and on 2, 8-bit heads of
+    //    256 (4 kv heads), 1 row of 16000 tokens 16.5, 18.8; 78 rows of 3000 104, 108; 256 of them 290, 272; bf16
+    //    heads of 192 (3 kv heads), 78 rows of 600 tokens 21.8, 31.0; 10 rows of 16000 73.7, 77.0; 8-bit ones of 192
+    //    (4 kv heads), 10 rows of 3000 22.2, 21.0, 256 rows of 600 46.6, 51.6.
     static constexpr int PER_SIMD = per_simd(DP);
     static constexpr int RES = PER_SIMD * 4 / W;
     static constexpr bool QLDS = DP > 128;
@@ -646,7 +653,7 @@ __global__ void __launch_bounds__(kNT) paged_attn_join_kernel(Kp a, int grid) {
 int64_t passes_of(int64_t group) { return (group + kHeads - 1) / kHeads; }
 int64_t align16(int64_t n) { return (n + 15) & ~int64_t(15); }
 
-// (row, kv head)s that occupy the chip with a wave each
+// (row, kv head)s that occupy the chip with a wave each, by the waves that the work is cut for
 int64_t waves_of(int64_t d) { return (d <= 128 ? 2 : 1) * 4 * kCUs; }
 
 template <int CT, int DP, bool EXACT, int W>
@@ -680,9 +687,11 @@ hipError_t go_w(Kp &k, int &grid, hipStream_t stream) {
 //   1 row of 32 tokens 5.7, 5.7, 8.2; 300: 12.0, 7.7, 9.6; 600: 19.8, 10.5, 10.0; 2400: 67, 28, 10.6
 //   64 rows of 128 tokens 10.3, 9.2, 12.1; 600: 36.9, 29.6, 32.9; up to 1200: 59, 39, 39; up to 2400: 118, 78, 71
 //   256 rows of 128 tokens 24.4, 29.0, 30.2; up to 300: 32.8, 38.9, 43.5; up to 1200: 132, 130, 136; up to 2400: 255, 248, 244
-// and of 4 and 3 kv heads in 8 and 32 bits, heads of 64 and 256 the same way: 78 rows of 90 tokens, 4 heads of 256 in
-// 8 bits, more than blocks of four are resident, 11.7, 15.7; 150 rows, 2 heads of 256 in bf16 12.1, 16.7.  In pieces, four waves share the
-// tokens of one, and fewer pieces are left to join; one row of 100000 tokens 32.8 us by waves, 23.1 by fours.
+// and of 4 and 3 kv heads in 8 and 32 bits, heads of 64 and 256 the same way: above 128, with more heads than a
+// quarter of waves_of, 78 rows of 90 tokens, 4 heads of 256 in 8 bits 11.7, 15.7; 150 rows, 2 heads of 256 in bf16
+// 12.1, 16.7 (one block of four a compute unit in bf16; in 8 bits two fit, and four waves still idle on rows of 3
+// tiles).  In pieces, four waves share the tokens of one, and fewer pieces are left to join; one row of 100000
+// tokens 32.8 us by waves, 23.1 by fours.  (Taken with weights in two bf16 parts; three are up to 3% slower either way.)
 template <int CT, int DP, bool EXACT>
 hipError_t go(Kp &k, int &grid, hipStream_t stream) {
     using T = Tile<CT, DP, 1>;

@@ -833,5 +833,7 @@ def ssd_cplx_mimo_chunk_scan_fwd(x, dt, dt_bias, A_log, B, C, D, h0=None, *, chu
 
 from . import attn as _attn  # noqa: E402  (needs the library and the helpers above)
 from .attn import *  # noqa: E402,F401,F403
+from . import longctx as _longctx  # noqa: E402
+from .longctx import *  # noqa: E402,F401,F403
 
-__all__ += _attn.__all__
+__all__ += _attn.__all__ + _longctx.__all__

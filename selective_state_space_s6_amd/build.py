@@ -23,7 +23,10 @@ LIB = os.path.join(HERE, "libssmscan.so")
 BIND = os.path.join(HERE, "_attn_bind.so")
 SOURCES = ["abi.hip", "s6_scan.hip", "s6_seg.hip", "s6_fused.hip", "s6_decode.hip", "s6_bwd.hip", "ssd_scan.hip", "ssd_decode.hip", "ssd_bwd.hip", "cssd_scan.hip",
            "trap_rotate.hip", "conv1d.hip", "s6_grouped.hip", "scratch.hip",
-           "abi_attn.hip", "kv_pages.hip", "qk_rope.hip", "paged_attn.hip"]
+           "abi_attn.hip", "kv_pages.hip", "qk_rope.hip", "paged_attn.hip",
+           "abi_longctx.hip", "prefix_attn.hip", "select_attn.hip", "kv_bounds.hip", "page_select.hip", "kv_mass.hip",
+           "kv_evict.hip"]
+BIND_SOURCES = ["bind_attn.cpp", "bind_longctx.cpp"]
 ARCH = os.environ.get("SSM_OFFLOAD_ARCH", "gfx950")
 # Packed fp32 ops are switched off: the compiler must not emit v_pk_{add,mul,fma}_f32.
 # MFMA accumulators are kept in ordinary VGPRs, so the fp32 state that the SSD
@@ -48,7 +51,7 @@ def _compile(src: str, obj: str) -> None:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stdout}\n{r.stderr}")
 
 
-def _compile_bind(obj: str) -> None:
+def _compile_bind(src: str, obj: str) -> None:
     import sysconfig
 
     import torch
@@ -56,15 +59,15 @@ def _compile_bind(obj: str) -> None:
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", "/opt/rocm/include",
-           "-I", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "bind_attn.cpp"), "-o", obj]
+           "-I", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for bind_attn.cpp:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
 
 
-def _link_bind(obj: str) -> None:
+def _link_bind(objs: list[str]) -> None:
     import torch
-    cmd = ["g++", "-shared", "-o", BIND + ".tmp", obj, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+    cmd = ["g++", "-shared", "-o", BIND + ".tmp", *objs, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
            "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-L", HERE, "-l:libssmscan.so", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -76,9 +79,9 @@ def build(verbose: bool = True) -> str:
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     objs = [os.path.join(objdir, s.replace(".hip", ".o")) for s in SOURCES]
-    bind_obj = os.path.join(objdir, "bind_attn.o")
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
-        bind = ex.submit(_compile_bind, bind_obj) if importlib.util.find_spec("torch") else None
+    bind_objs = [os.path.join(objdir, s.replace(".cpp", ".o")) for s in BIND_SOURCES]
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 2, os.cpu_count() or 4)) as ex:
+        bind = [ex.submit(_compile_bind, s, o) for s, o in zip(BIND_SOURCES, bind_objs)] if importlib.util.find_spec("torch") else []
         list(ex.map(lambda so: _compile(*so), zip(SOURCES, objs)))
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
@@ -87,8 +90,9 @@ def build(verbose: bool = True) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     if bind:
-        bind.result()
-        _link_bind(bind_obj)
+        for b in bind:
+            b.result()
+        _link_bind(bind_objs)
     if verbose:
         print(f"built {LIB}, " + (BIND if bind else "and no _attn_bind.so: torch is not installed"))
     return LIB

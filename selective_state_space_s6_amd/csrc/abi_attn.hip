@@ -6,42 +6,12 @@
 #include <stdint.h>
 
 #include "../../include/ssm_attn.h"
-#include "abi_common.hpp"
+#include "abi_attn_common.hpp"
 #include "attn_launchers.hpp"
 
-using ssm::fail;
-using ssm::launched;
-using ssm::too_big;
+using namespace ssm;
 
 namespace {
-
-constexpr int64_t k2p31 = int64_t(1) << 31;
-
-#define REQUIRE_NOT_NEG(entry, v)                                                                 \
-    do {                                                                                          \
-        if ((v) < 0) return fail(SSM_ERR_INVALID_ARG, "%s: %s must be >= 0 (got %lld)", entry, #v, \
-                                 (long long)(v));                                                 \
-    } while (0)
-
-// two tensors of one call that may not share their first element
-struct Named { const void *p; const char *name; };
-int check_alias(const char *E, const Named *outs, int no, const Named *ins, int ni) {
-    for (int i = 0; i < no; ++i) {
-        if (outs[i].p == nullptr) continue;
-        for (int j = 0; j < ni; ++j)
-            if (outs[i].p == ins[j].p) return fail(SSM_ERR_INVALID_ARG, "%s: %s aliases %s", E, outs[i].name, ins[j].name);
-        for (int j = i + 1; j < no; ++j)
-            if (outs[i].p == outs[j].p) return fail(SSM_ERR_INVALID_ARG, "%s: %s aliases %s", E, outs[i].name, outs[j].name);
-    }
-    return SSM_OK;
-}
-
-// elements of `dtype` start at multiples of their size
-int check_element(const char *E, const void *p, const char *name, int esize) {
-    if (((uintptr_t)p & (uintptr_t)(esize - 1)) != 0)
-        return fail(SSM_ERR_UNSUPPORTED, "%s: %s is not aligned to its elements", E, name);
-    return SSM_OK;
-}
 
 // heads (n_tokens, n_heads, headdim) without a gap; strides of a dim of one entry are not used
 bool gapless(int64_t n_tokens, int64_t n_heads, int64_t headdim, int64_t st, int64_t sh) {
@@ -75,20 +45,6 @@ int check_rope(const char *E, const void *q, const void *k, const float *wq, con
         if (n_kv_heads > 0) REQUIRE_PTR(E, wk);
     }
     if (rot_dim > 0) { REQUIRE_PTR(E, inv_freq); REQUIRE_PTR(E, positions); }
-    return SSM_OK;
-}
-
-// cache strides: rows must not overlap by sign, and every offset must fit the kernels' arithmetic
-int check_cache(const char *E, int64_t n_pages, int64_t page_size, int64_t n_kv_heads, int64_t headdim,
-                int64_t sp, int64_t st, int64_t sh, int esize) {
-    REQUIRE_POS(E, n_pages); REQUIRE_POS(E, page_size);
-    if (n_pages >= k2p31 || page_size >= k2p31 || n_pages * page_size >= k2p31)
-        return fail(SSM_ERR_UNSUPPORTED, "%s: n_pages * page_size must be below 2^31", E);
-    if (sp < 0 || st < 0 || sh < 0)
-        return fail(SSM_ERR_INVALID_ARG, "%s: cache strides must be >= 0", E);
-    const double extent = ((double)(n_pages - 1) * (double)sp + (double)(page_size - 1) * (double)st +
-                           (double)(n_kv_heads - 1) * (double)sh + (double)headdim) * esize;
-    if (extent >= 68719476736.0) return fail(SSM_ERR_UNSUPPORTED, "%s: a cache's extent must be below 2^36 bytes", E);
     return SSM_OK;
 }
 

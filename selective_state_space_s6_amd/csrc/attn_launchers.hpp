@@ -1,10 +1,10 @@
-// attn_launchers.hpp -- host-side kernel launchers behind include/ssm_attn.h.
-// Arguments have been validated by abi_attn.hip before any of these is called.
+// attn_launchers.hpp -- host-side kernel launchers behind include/ssm_attn.h and include/ssm_longctx.h.
+// Arguments have been validated by abi_attn.hip and abi_longctx.hip before any of these is called.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "../../include/ssm_attn.h"
+#include "../../include/ssm_longctx.h"
 
 namespace ssm {
 
@@ -49,11 +49,60 @@ struct PagedAttnArgs {
     int64_t batch, n_heads, n_kv_heads; int headdim;
     int64_t max_pages, table_stride, n_pages, page_size, q_sr, q_sh, c_sp, c_st, c_sh;
     float scale, k_scale, v_scale; int64_t window; int kv_dtype; void *workspace;
+    const int32_t *selected; int64_t top_k;      // (batch, kv heads, top_k) pages of each (row, kv head), or NULL
+    bool o_f32;                                  // o in fp32 whatever the cache's type
 };
 size_t paged_attn_workspace_bytes(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t headdim,
                                   int64_t max_pages, int64_t page_size);
 // units of work of the longest rows: must stay below 2^31
 double paged_attn_max_units(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t max_pages, int64_t page_size);
 hipError_t launch_paged_attn(const PagedAttnArgs &a, hipStream_t stream, const char **kernel_name);
+// the same over chosen pages (select_attn.hip): `selected` is set, window is 0
+hipError_t launch_select_attn(const PagedAttnArgs &a, hipStream_t stream, const char **kernel_name);
+
+// attention with shared prefixes (prefix_attn.hip): `own` are the rows' own tokens
+struct PrefixAttnArgs {
+    PagedAttnArgs own;
+    const int32_t *prefix; const int32_t *prefix_table; const int32_t *prefix_lens;
+    int64_t n_prefixes, max_prefix_pages, prefix_stride;
+};
+size_t prefix_attn_workspace_bytes(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t headdim,
+                                   int64_t max_prefix_pages, int64_t max_pages, int64_t page_size);
+hipError_t launch_prefix_attn(const PrefixAttnArgs &a, hipStream_t stream, const char **kernel_name);
+
+// smallest and largest keys of pages (kv_bounds.hip); cache strides and rows in bytes
+struct KvBoundsArgs {
+    const char *k; char *bounds; const int32_t *table; const int32_t *len_old; const int32_t *lens;
+    int64_t table_stride, c_sp, c_st, c_sh;
+    int batch, n_kv, row_bytes, max_pages, n_pages, page_size, kv_dtype;
+};
+hipError_t launch_kv_bounds(const KvBoundsArgs &a, hipStream_t stream, const char **kernel_name);
+
+// choice of pages by their bounds (page_select.hip); q's strides in elements
+struct PageSelectArgs {
+    const void *q; const char *bounds; const int32_t *table; const int32_t *lens; int32_t *selected; uint32_t *keys;
+    int64_t table_stride, q_sr, q_sh;
+    int batch, n_heads, n_kv, d, max_pages, n_pages, page_size, top_k, first, last, kv_dtype; bool bf16;
+};
+size_t page_select_workspace_bytes(int64_t batch, int64_t n_kv_heads, int64_t max_pages, int64_t top_k);
+hipError_t launch_page_select(const PageSelectArgs &a, hipStream_t stream, const char **kernel_name);
+
+// softmax weight that cached tokens gather (kv_mass.hip); strides in elements
+struct KvMassArgs {
+    const void *q; const void *k_cache; const float *lse; float *mass; const int32_t *block_table;
+    const int32_t *starts; const int32_t *positions; const int32_t *len_old; const int32_t *lens;
+    int64_t n_tokens, batch, n_heads, n_kv_heads; int headdim;
+    int64_t max_pages, table_stride, n_pages, page_size, q_st, q_sh, c_sp, c_st, c_sh;
+    float scale, k_scale; int kv_dtype;
+};
+hipError_t launch_kv_mass(const KvMassArgs &a, hipStream_t stream, const char **kernel_name);
+
+// eviction (kv_evict.hip); cache strides and rows in bytes
+struct KvEvictArgs {
+    char *k; char *v; float *mass; const int32_t *table; const int32_t *lens; int32_t *len_out; int32_t *kept;
+    int64_t table_stride, c_sp, c_st, c_sh;
+    int batch, n_kv, row_bytes, max_pages, n_pages, page_size, budget, recent;
+};
+hipError_t launch_kv_evict(const KvEvictArgs &a, hipStream_t stream, const char **kernel_name);
 
 }  // namespace ssm

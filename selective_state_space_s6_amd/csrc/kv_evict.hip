@@ -1,0 +1,163 @@
+// kv_evict.hip -- eviction from a paged key-value cache by the attention weight that tokens gathered
+// (ssm_kv_evict in include/ssm_longctx.h).
+//
+// Two launches.  The choice: a block for each (request, kv head), keys in shared memory (topk.hpp).  The
+// move: kept tokens go forward in their order, in place.  Token i comes from place kept[i] >= i, and
+// both rise with i, so a run of tokens whose old values are all in registers may be stored: what it
+// overwrites are places below the run's end, which no later token comes from.  One block takes such runs one
+// after the other; for more blocks at once, a (request, kv head)'s rows are cut along headdim, which are moves
+// of their own, as are k, v and mass.  Bound: HBM, the moved rows read and written.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <algorithm>
+
+#include "attn_launchers.hpp"
+#include "topk.hpp"
+
+namespace ssm {
+namespace {
+
+constexpr int kPick = 1024;         // threads of the choice
+constexpr int kMove = 256;          // threads of the move
+constexpr int kRun = 8;             // 16-byte pieces of a thread in a run
+constexpr int kMostKept = 32768;    // keys that the choice keeps in shared memory at most
+
+__global__ void __launch_bounds__(kPick) evict_pick_kernel(KvEvictArgs a, int room) {
+    __shared__ TopKShared<kPick> sh;
+    extern __shared__ uint32_t own[];
+    const int tid = threadIdx.x;
+    const int row = blockIdx.x / a.n_kv, g = blockIdx.x - row * a.n_kv;
+    const PageSize ps(a.page_size);
+    const int n = min(max(a.lens[row], 0), a.max_pages * a.page_size);
+    int32_t *kept = a.kept + (int64_t)blockIdx.x * a.budget;
+    if (g == 0 && tid == 0) a.len_out[row] = min(n, a.budget);
+    if (n <= a.budget) {
+        for (int i = tid; i < a.budget; i += kPick) kept[i] = i < n ? i : -1;
+        return;
+    }
+    const int want = a.budget - a.recent, m = n - a.recent;
+    for (int i = tid; i < a.recent; i += kPick) kept[want + i] = m + i;
+    if (want == 0) return;
+    const int32_t *table = a.table + (int64_t)row * a.table_stride;
+    auto load = [&](int i) {
+        const int p = ps.of(i), page = table[p];
+        if ((uint32_t)page >= (uint32_t)a.n_pages) return kKeyLowest;
+        return key_of(a.mass[((int64_t)page * a.n_kv + g) * a.page_size + ps.place(i, p)]);
+    };
+    for (int i = tid; i < min(m, room); i += kPick) own[i] = load(i);
+    __syncthreads();
+    auto key = [&](int i) { return i < room ? own[i] : load(i); };
+    const Cut cut = find_cut<kPick>(sh, m, want, key);
+    put_chosen<kPick>(sh, m, cut, key, [&](int place, int i) { kept[place] = i; });
+}
+
+// the first i < n with kept[i] != i (n if none): once one is, all later ones are
+__device__ __forceinline__ int first_moved(const int32_t *kept, int n) {
+    __shared__ int at;
+    const int step = (n + kMove - 1) / kMove;
+    int lo = 0;
+    for (int s = step, count = kMove; ; s = 1, count = step) {       // in steps, then one by one within a step
+        __syncthreads();
+        if (threadIdx.x == 0) at = n;
+        __syncthreads();
+        for (int i = threadIdx.x; i < count; i += kMove) {
+            const int x = lo + i * s;
+            if (x < n && kept[x] != x && (i == 0 || kept[x - s] == x - s)) at = x;      // of one x at most
+        }
+        __syncthreads();
+        const int got = at;
+        if (s == 1) return got;
+        lo = got < n ? max(0, got - s + 1) : (n - 1) / s * s;
+    }
+}
+
+// slices: parts of a row's 16-byte pieces for k and for v; block 2 * slices of a head moves mass
+__global__ void __launch_bounds__(kMove) evict_move_kernel(KvEvictArgs a, int slices) {
+    const int tid = threadIdx.x;
+    const int hr = blockIdx.x / (2 * slices + 1), part = blockIdx.x - hr * (2 * slices + 1);
+    const int row = hr / a.n_kv, g = hr - row * a.n_kv;
+    const PageSize ps(a.page_size);
+    const int n = min(max(a.lens[row], 0), a.max_pages * a.page_size);
+    if (n <= a.budget) return;
+    const int32_t *kept = a.kept + (int64_t)hr * a.budget, *table = a.table + (int64_t)row * a.table_stride;
+    const int from = first_moved(kept, a.budget);
+    // a token's page (-1: none) and place
+    auto page_at = [&](int p) { return (uint32_t)table[p] < (uint32_t)a.n_pages ? table[p] : -1; };
+
+    if (part == 2 * slices) {
+        for (int base = from; base < a.budget; base += kMove * kRun) {
+            float x[kRun];
+            int to[kRun];                         // page of the new place, -1: not moved
+#pragma unroll
+            for (int u = 0; u < kRun; ++u) {
+                const int i = base + u * kMove + tid;
+                to[u] = -1;
+                x[u] = 0.0f;
+                if (i < a.budget) {
+                    const int j = kept[i], pj = ps.of(j), src = page_at(pj);
+                    to[u] = src >= 0 ? page_at(ps.of(i)) : -1;
+                    if (src >= 0) x[u] = a.mass[((int64_t)src * a.n_kv + g) * a.page_size + ps.place(j, pj)];
+                }
+            }
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // every value is in a register
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kRun; ++u) {
+                const int i = base + u * kMove + tid;
+                if (to[u] >= 0) a.mass[((int64_t)to[u] * a.n_kv + g) * a.page_size + ps.place(i, ps.of(i))] = x[u];
+            }
+        }
+        return;
+    }
+    const int pieces = a.row_bytes / 16;          // of a row
+    const int s = part >> 1;
+    char *cache = (part & 1 ? a.v : a.k) + (int64_t)g * a.c_sh;
+    const int c0 = s * pieces / slices, cs = (s + 1) * pieces / slices - c0;
+    const int side = kMove / cs;                  // tokens side by side
+    const int sub = tid / cs, c = c0 + tid - sub * cs;
+    const bool works = sub < side;
+    for (int base = from; base < a.budget; base += side * kRun) {
+        u32x4 x[kRun];
+        int to[kRun];
+#pragma unroll
+        for (int u = 0; u < kRun; ++u) {
+            const int i = base + u * side + sub;
+            to[u] = -1;
+            x[u] = (u32x4){0, 0, 0, 0};
+            if (works && i < a.budget) {
+                const int j = kept[i], pj = ps.of(j), src = page_at(pj);
+                to[u] = src >= 0 ? page_at(ps.of(i)) : -1;
+                if (src >= 0) x[u] = *(const u32x4 *)(cache + (int64_t)src * a.c_sp + (int64_t)ps.place(j, pj) * a.c_st + c * 16);
+            }
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kRun; ++u) {
+            const int i = base + u * side + sub;
+            if (to[u] >= 0) *(u32x4 *)(cache + (int64_t)to[u] * a.c_sp + (int64_t)ps.place(i, ps.of(i)) * a.c_st + c * 16) = x[u];
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_kv_evict(const KvEvictArgs &a, hipStream_t stream, const char **kernel_name) {
+    *kernel_name = "evict_pick_kernel";
+    const int64_t heads = (int64_t)a.batch * a.n_kv, most = (int64_t)a.max_pages * a.page_size;
+    const int room = (int)std::min<int64_t>(most, kMostKept);
+    if (room > 8192) {                   // more than a block has unasked
+        const hipError_t e = hipFuncSetAttribute((const void *)evict_pick_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, room * 4);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(evict_pick_kernel, dim3((unsigned)heads), dim3(kPick), (size_t)room * 4, stream, a, room);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || most <= a.budget) return e;
+    *kernel_name = "evict_move_kernel";
+    int slices = 1;
+    while (slices * 4 <= a.row_bytes / 16 && heads * slices < 512) slices *= 2;
+    hipLaunchKernelGGL(evict_move_kernel, dim3((unsigned)(heads * (2 * slices + 1))), dim3(kMove), 0, stream, a, slices);
+    return hipGetLastError();
+}
+
+}  // namespace ssm

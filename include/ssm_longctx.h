@@ -157,8 +157,8 @@ int ssm_select_attn_decode_fwd(const void *q, const void *k_cache, const void *v
  * fp32; mass (n_pages, n_kv_heads, page_size) fp32 contiguous, updated in place;
  * starts (batch + 1), positions (n_tokens), len_old, lens (batch) int32.  starts
  * outside [0, n_tokens] are cut to it.  A page belongs to one request here.
- * Limits: those of ssm_paged_attn_decode_fwd, and n_pages * n_kv_heads * page_size
- * below 2^31.  n_tokens may be 0 (q, lse and positions may then be NULL).  No
+ * Limits: batch <= SSM_KV_MAX_BATCH; those of ssm_paged_attn_decode_fwd, and n_pages *
+ * n_kv_heads * page_size below 2^31.  n_tokens may be 0 (q, lse and positions may then be NULL).  No
  * workspace. */
 int ssm_kv_mass_update(const void *q, const void *k_cache, const float *lse, float *mass,
                        const int32_t *block_table, const int32_t *starts, const int32_t *positions,

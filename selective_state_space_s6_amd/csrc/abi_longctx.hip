@@ -206,6 +206,9 @@ int ssm_kv_mass_update(const void *q, const void *k_cache, const float *lse, flo
     TRY(check_heads(E, n_tokens, n_heads, n_kv_heads, q_st, q_sh, dtype, kv_dtype));
     TRY(check_scales(E, scale, k_scale, 1.0f, kv_dtype));
     TRY(check_paged(E, batch, headdim, max_pages, table_stride, n_pages, page_size, n_kv_heads, sp, st, sh, kv_dtype));
+    if (batch > SSM_KV_MAX_BATCH)
+        return fail(SSM_ERR_UNSUPPORTED, "%s: batch %lld > %d", E, (long long)batch, SSM_KV_MAX_BATCH);
+    TRY(check_units(E, batch, n_heads, n_kv_heads, max_pages, page_size));
     if ((double)n_pages * (double)n_kv_heads * (double)page_size >= 2147483648.0)
         return fail(SSM_ERR_UNSUPPORTED, "%s: problem too large", E);
     if (batch == 0) return SSM_OK;

@@ -9,7 +9,7 @@
 // walk tiles of tokens of their own and join at the end.  Operands go from global memory straight
 // into the matrix instructions' registers as in paged_attn_kernel.hpp (scores S^T = K Q^T, output O^T = V^T P^T,
 // V transposed by byte permutations, here once for all columns); q waits in shared memory.
-// A block's share is (16 NQ columns, kv head, one of `splits` parts of the prefix).  Blocks of the same part and
+// A block's share is (16 NQ columns, kv head, one of `splits` parts of their rows' prefixes, end to end).  Blocks of the same part and
 // other columns run on one XCD at one time, so that all but the first of them find K and V in its L2.
 // Bound: for few columns HBM; from about 100 columns a kv head on the matrix cores and the exponentials beside them.
 //
@@ -55,22 +55,56 @@ template <int CT, int DP> struct PTile {
     static constexpr int QW = CT == KF8 ? 2 : 1;               // operands of q to a load of K
     static constexpr int UNIT = kW * NT;
 };
-// columns of 16 that a block can take by the registers of their outputs
-constexpr int most_nq(int dp) { return dp <= 128 ? 4 : 2; }
+
+// A block's place in the work: 16-column groups are (row, head) pairs of one kv head
+struct Place { int split, tile, kv, row0, nrows, nh, h0; };
+__device__ __forceinline__ bool place_of(const Pp &a, Place &p) {
+    const int j = blockIdx.x >> 3, combo = j / a.tiles * 8 + (blockIdx.x & 7);
+    if (combo >= a.combos) return false;
+    p.tile = j % a.tiles;
+    p.split = combo % a.splits;
+    const int kp = combo / a.splits, pass = kp % a.passes;
+    p.kv = kp / a.passes;
+    p.row0 = p.tile * a.rows;
+    p.nrows = min(a.rows, a.batch - p.row0);
+    p.nh = min(a.gm, a.group - pass * a.gm);
+    p.h0 = p.kv * a.group + pass * a.gm;
+    return true;
+}
+
+// The prefixes of a block's rows, each at its first row's lane, in one line of units of `unit` tokens; the block's
+// part of it.
+struct Line { int id, len, units, upto, first, last; uint64_t leaders; };
+__device__ __forceinline__ Line line_of(const Pp &a, const Place &p, int lane, int unit) {
+    Line n;
+    n.id = lane < p.nrows ? a.prefix[p.row0 + lane] : -1;
+    if ((uint32_t)n.id >= (uint32_t)a.n_prefixes) n.id = -1;
+    n.len = n.id >= 0 ? min(max(a.lens[n.id], 0), a.max_len) : 0;
+    n.leaders = 0;
+    for (uint64_t left = __ballot(n.id >= 0); left;) {
+        const int l = __builtin_ctzll(left);
+        n.leaders |= uint64_t(1) << l;
+        left &= ~__ballot(n.id == __builtin_amdgcn_readlane(n.id, l));
+    }
+    n.units = n.leaders >> lane & 1 ? (n.len + unit - 1) / unit : 0;
+    n.upto = wave_scan(n.units);
+    const int all = __builtin_amdgcn_readlane(n.upto, 63);
+    n.first = (int)((int64_t)p.split * all / a.splits);
+    n.last = (int)((int64_t)(p.split + 1) * all / a.splits);
+    return n;
+}
 
 template <int CT, int DP, bool EXACT, int NQ>
-__global__ void __launch_bounds__(kNT, 1) prefix_attn_kernel(Pp a) {
+__global__ void __launch_bounds__(kNT, DP * NQ <= 256 ? 2 : 1) prefix_few_kernel(Pp a) {
     using T = PTile<CT, DP>;
     constexpr int VD = T::VD, VB = T::VB, PITCH = DP + 4;
     extern __shared__ float lds[];          // q, and at the end the waves' outputs, 16 columns at a time
     u32x4 *q_lds = (u32x4 *)lds;
     __shared__ float wave_m[kW][16 * NQ], wave_l[kW][16 * NQ];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
-    const int j = blockIdx.x >> 3, combo = j / a.tiles * 8 + (blockIdx.x & 7), tile = j % a.tiles;
-    if (combo >= a.combos) return;
-    const int split = combo % a.splits, kp = combo / a.splits, pass = kp % a.passes, kv = kp / a.passes;
-    const int row0 = tile * a.rows, nrows = min(a.rows, a.batch - row0);
-    const int nh = min(a.gm, a.group - pass * a.gm), h0 = kv * a.group + pass * a.gm;
+    Place at;
+    if (!place_of(a, at)) return;
+    const int split = at.split, kv = at.kv, row0 = at.row0, nrows = at.nrows, nh = at.nh, h0 = at.h0;
     const PageSize ps(a.page_size);
 
     // this lane's columns: their row in the block (-1: none) and head
@@ -98,8 +132,8 @@ __global__ void __launch_bounds__(kNT, 1) prefix_attn_kernel(Pp a) {
             q_lds[(i * NQ + n) * 64 + lane] = x;
         }
     }
-    const int id = lane < nrows ? a.prefix[row0 + lane] : -1;
-    uint64_t left = __ballot((uint32_t)id < (uint32_t)a.n_prefixes);
+    Line line = line_of(a, at, lane, T::UNIT);
+    const int first = line.first, last = line.last;
     __syncthreads();
 
     float m[NQ], l[NQ];                      // of the columns; l over this lane's tokens only
@@ -116,12 +150,13 @@ __global__ void __launch_bounds__(kNT, 1) prefix_attn_kernel(Pp a) {
     const char *kb = a.k + kv * a.c_sh + grp * 16, *vb = a.v + kv * a.c_sh;
 
     // one prefix after the other, with the columns of its rows
-    while (left) {
-        const int p = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-        const uint64_t mine = __ballot(id == p);
-        left &= ~mine;
-        const int len = min(max(a.lens[p], 0), a.max_len), units = (len + T::UNIT - 1) / T::UNIT;
-        const int u0 = (int)((int64_t)split * units / a.splits), u1 = (int)((int64_t)(split + 1) * units / a.splits);
+    for (; line.leaders; line.leaders &= line.leaders - 1) {
+        const int lead = __builtin_ctzll(line.leaders), end = __builtin_amdgcn_readlane(line.upto, lead);
+        const int begin = end - __builtin_amdgcn_readlane(line.units, lead);
+        const int u0 = max(first, begin) - begin, u1 = min(last, end) - begin;
+        if (u0 >= u1) continue;
+        const int p = __builtin_amdgcn_readlane(line.id, lead), len = __builtin_amdgcn_readlane(line.len, lead);
+        const uint64_t mine = __ballot(line.id == p);
         const int t_end = min(len, u1 * T::UNIT);
         const int32_t *table = a.table + (int64_t)p * a.table_stride;
         bool in[NQ], all_in = true;
@@ -336,21 +371,32 @@ __global__ void __launch_bounds__(kNT, 1) prefix_attn_kernel(Pp a) {
         }
     }
 
-    // ---- join the block's waves, 16 columns at a time
+    // ---- join the block's waves
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
         l[n] = head_sum(l[n]);
         if (grp == 0) { wave_m[wave][n * 16 + col] = m[n]; wave_l[wave][n * 16 + col] = l[n]; }
     }
-    const int d4 = a.d / 4;
+    __syncthreads();                         // (readers of q, too)
+    const int64_t to0 = ((int64_t)split * a.batch + row0) * a.n_heads + h0;
+    // a column's maximum and sum, by one thread
+    if (tid < 16 * NQ) {
+        const int r = tid / a.gm, h = tid - r * a.gm;
+        float mt = -INFINITY, ls = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) mt = fmaxf(mt, wave_m[w][tid]);
+#pragma unroll
+        for (int w = 0; w < kW; ++w) ls += wave_l[w][tid] * (mt == -INFINITY ? 1.0f : exp2_fast(wave_m[w][tid] - mt));
+        if (r < nrows && h < nh) *(float2 *)(a.ml + (to0 + r * a.n_heads + h) * 2) = make_float2(mt, ls);
+    }
+    if (first >= last) return;               // no tokens: weighs nothing
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-        __syncthreads();                     // readers of q, or of the 16 columns before
         float top = wave_m[0][n * 16 + col];
 #pragma unroll
         for (int w = 1; w < kW; ++w) top = fmaxf(top, wave_m[w][n * 16 + col]);
         const float f = top == -INFINITY ? 0.0f : exp2_fast(m[n] - top);
-        float *to = lds + (wave * 16 + col) * PITCH;
+        float *to = lds + (wave * 16 * NQ + n * 16 + col) * PITCH;
 #pragma unroll
         for (int b = 0; b < VB; ++b)
 #pragma unroll
@@ -359,53 +405,426 @@ __global__ void __launch_bounds__(kNT, 1) prefix_attn_kernel(Pp a) {
                 for (int i = 0; i < VD; i += 4)
                     *(float4 *)(to + (b * 16 + grp * 4 + r) * VD + i) =
                         make_float4(acc[n][b][i][r] * f, acc[n][b][i + 1][r] * f, acc[n][b][i + 2][r] * f, acc[n][b][i + 3][r] * f);
-        __syncthreads();
-        for (int i = tid; i < 16 * d4; i += kNT) {
-            const int cc = i / d4, e = (i - cc * d4) * 4, c = n * 16 + cc, r = c / a.gm, h = c - r * a.gm;
-            if (r >= nrows || h >= nh) continue;
-            f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-            float ls = 0.0f, mt = -INFINITY;
+    }
+    __syncthreads();
+    constexpr int D4 = DP / 4, SIDE = kNT / D4;          // columns side by side, 4 dims a thread
+    const int cc = tid / D4, e = (tid - cc * D4) * 4;
+    if (cc >= SIDE || (!EXACT && e >= a.d)) return;
+#pragma unroll 4
+    for (int c = cc; c < 16 * NQ; c += SIDE) {
+        const int r = c / a.gm, h = c - r * a.gm;
+        if (r >= nrows || h >= nh) continue;
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int w = 0; w < kW; ++w) {
-                v += *(const f32x4 *)(lds + (w * 16 + cc) * PITCH + e);
-                mt = fmaxf(mt, wave_m[w][c]);
-            }
-#pragma unroll
-            for (int w = 0; w < kW; ++w) ls += wave_l[w][c] * (mt == -INFINITY ? 1.0f : exp2_fast(wave_m[w][c] - mt));
-            const int64_t at = ((int64_t)split * a.batch + row0 + r) * a.n_heads + h0 + h;
-            *(f32x4 *)(a.part + at * a.d + e) = v;
-            if (e == 0) *(float2 *)(a.ml + at * 2) = make_float2(mt, ls);
-        }
+        for (int w = 0; w < kW; ++w) v += *(const f32x4 *)(lds + (w * 16 * NQ + c) * PITCH + e);
+        *(f32x4 *)(a.part + (to0 + r * a.n_heads + h) * a.d + e) = v;
     }
 }
 
-// Joins the parts of a (row, query head), a wave each, lanes of 4 dims; the row's own tokens are one
-// more part, already normalised.
+// ---- many columns: a block's waves have columns of their own and share the tokens
+template <int CT, int DP> struct FTile {
+    using P = PTile<CT, DP>;
+    static constexpr bool F32 = CT == KF32;
+    static constexpr int E = P::E, KD = P::KD, KC = P::KC, QW = P::QW, VD = P::VD, VB = P::VB, VW = P::VW;
+    // tokens of a tile: 32 KiB of K and V in shared memory, as operands (8-bit ones widened)
+    static constexpr int NT = F32 ? (DP <= 64 ? 64 : DP <= 128 ? 32 : 16) : DP <= 128 ? 64 : 32;
+    static constexpr int PT = F32 ? 16 : 32;                   // tokens that are weighed at a time
+    static constexpr int SUB = NT / 16, KOPS = SUB * KC * QW;
+    static constexpr int VOPS = F32 ? NT / 4 * VB : NT / 32 * VB * VD;
+    static constexpr int BUF = (KOPS + VOPS) * 64;             // 16-byte operands of a lane, of one buffer
+    // V is brought by the first waves, K by the others
+    static constexpr int VWAVES = F32 ? 2 : NT / 32 * VB, KWAVES = kW - VWAVES;
+    static constexpr int KL = SUB * KC / KWAVES;               // loads of K of a wave
+    static constexpr int VL = F32 ? NT / 4 * VB / 2 : 8;       // and of V
+    static constexpr int REGS = KL * 4 > VL * VW ? KL * 4 : VL * VW;
+    static constexpr uint64_t ALL = NT == 64 ? ~uint64_t(0) : (uint64_t(1) << NT) - 1;
+    static_assert(SUB * KC % KWAVES == 0 && VWAVES < kW, "");
+};
+
+// For the compiler's order of a run of READS operands from shared memory with PER matrix instructions each: AHEAD
+// operands are on their way before the first is used, and one more is asked for with each.
+template <int READS, int PER, int AHEAD = 3>
+__device__ __forceinline__ void ahead() {
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD < READS ? AHEAD : READS, 0);
+#pragma unroll
+    for (int i = 0; i < READS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
+        if (i + AHEAD < READS) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+}
+
+// x minus the bf16 value of ph that `which`, a pair of bf16 values, has a -1 for (exact: x is rounded in ph)
+__device__ __forceinline__ float minus(uint32_t ph, uint32_t which, float x) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, ph), __builtin_bit_cast(bf16x2, which), x, false);
+}
+
+template <int CT, int DP, bool EXACT, int NQ>
+__global__ void __launch_bounds__(kNT, 2) prefix_many_kernel(Pp a) {
+    using T = FTile<CT, DP>;
+    constexpr int VD = T::VD, VB = T::VB;
+    extern __shared__ u32x4 bufs[];          // two of: K's operands, V's operands
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
+    Place at;
+    if (!place_of(a, at)) return;
+    const PageSize ps(a.page_size);
+    Line line = line_of(a, at, lane, T::NT);
+
+    // this lane's columns: their row in the block (-1: none) and head; q with the sign of the scale
+    const uint32_t flip = a.scale2 < 0.0f ? (T::F32 ? 0x80000000u : 0x80008000u) : 0u;
+    const float scale2 = fabsf(a.scale2);
+    int crow[NQ], chead[NQ];
+    u32x4 q[NQ][T::KC * T::QW];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        const int c = (wave * NQ + n) * 16 + col, r = c / a.gm;
+        chead[n] = c - r * a.gm;
+        crow[n] = r < at.nrows && chead[n] < at.nh ? r : -1;
+#pragma unroll
+        for (int i = 0; i < T::KC * T::QW; ++i) {
+            const int dim = i / T::QW * 4 * T::KD + grp * T::KD + i % T::QW * 8;
+            u32x4 x = {0, 0, 0, 0};
+            if (crow[n] >= 0 && (EXACT || dim < a.d))
+                x = *(const u32x4 *)(a.q + (at.row0 + crow[n]) * a.q_sr + (at.h0 + chead[n]) * a.q_sh + dim * (T::F32 ? 4 : 2));
+#pragma unroll
+            for (int w = 0; w < 4; ++w) x[w] ^= flip;
+            q[n][i] = x;
+        }
+    }
+    bool any = false;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) any = any || crow[n] >= 0;
+    const bool works = __any(any);           // (a wave without columns only brings K and V)
+
+    // Maxima and sums of the columns.  A sum is a row of the output with V = 1, the same in all four of its places;
+    // of fp32 it is the first place, over this lane's tokens only.
+    float m[NQ];
+    f32x4 l[NQ], acc[NQ][VB][VD];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        m[n] = -INFINITY;
+        l[n] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int b = 0; b < VB; ++b)
+#pragma unroll
+            for (int i = 0; i < VD; ++i) acc[n][b][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    // -1 in the low or the high half of a pair.  (Out of the compiler's sight: as a constant, 0x0000bf80 becomes the
+    // instruction's own -1.0, which stands in the high half.)
+    uint32_t low = 0xbf80u, high = 0xbf800000u;
+    asm("" : "+s"(low), "+s"(high));
+    const char *kb = a.k + at.kv * a.c_sh, *vb = a.v + at.kv * a.c_sh;
+    const uint32_t sp16 = (uint32_t)(a.c_sp / 16), st16 = (uint32_t)(a.c_st / 16);
+
+    // one prefix after the other, with the columns of its rows
+    for (; line.leaders; line.leaders &= line.leaders - 1) {
+        const int lead = __builtin_ctzll(line.leaders), end = __builtin_amdgcn_readlane(line.upto, lead);
+        const int begin = end - __builtin_amdgcn_readlane(line.units, lead);
+        const int u0 = max(line.first, begin) - begin, u1 = min(line.last, end) - begin;
+        if (u0 >= u1) continue;
+        const int p = __builtin_amdgcn_readlane(line.id, lead), t_end = min(__builtin_amdgcn_readlane(line.len, lead), u1 * T::NT);
+        const uint64_t mine = __ballot(line.id == p);
+        const int32_t *table = a.table + (int64_t)p * a.table_stride;
+        bool in[NQ], all_in = true;
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            in[n] = crow[n] >= 0 && (mine >> crow[n] & 1);
+            all_in = all_in && (in[n] || crow[n] < 0);
+        }
+        all_in = __all(all_in);
+
+        // a lane's token of a tile: its page (-1: none); tokens that are none read the cache's first row
+        auto page_of = [&](int t0) {
+            const int t = t0 + (lane & (T::NT - 1));
+            return t < t_end ? table[ps.of(t)] : -1;
+        };
+        // (places in 16 bytes: a cache is smaller than 2^36)
+        auto off_of = [&](int t0, int page) -> uint32_t {
+            const int t = t0 + (lane & (T::NT - 1));
+            return (uint32_t)page < (uint32_t)a.n_pages ? (uint32_t)page * sp16 + (uint32_t)ps.place(t, ps.of(t)) * st16 : 0u;
+        };
+        auto row_of = [&](uint32_t off, int tok) { return (uint64_t)(uint32_t)__shfl((int)off, tok) * 16; };
+        uint32_t reg[T::REGS];
+        // the wave's part of a tile, from memory
+        auto bring = [&](uint32_t off) {
+            if (wave < T::VWAVES) {
+#pragma unroll
+                for (int x = 0; x < T::VL; ++x) {
+                    const int i = T::F32 ? wave * T::VL + x : x, g = T::F32 ? i / VB : wave / VB * 8 + x, b = T::F32 ? i % VB : wave % VB;
+                    const int dim = (b * 16 + col) * VD;      // past headdim: the row's first dims, in rows of the result that are not kept
+                    const Words<T::VW> v = ld_words<T::VW>(vb + row_of(off, (g >> 2) * 16 + grp * 4 + (g & 3)) + (EXACT || dim < a.d ? dim * T::E : 0));
+#pragma unroll
+                    for (int w = 0; w < T::VW; ++w) reg[x * T::VW + w] = v.w[w];
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < T::KL; ++x) {
+                    const int i = (wave - T::VWAVES) * T::KL + x, s = i / T::KC, c = i - s * T::KC;
+                    const bool is = EXACT || (c * 4 + grp) * T::KD < a.d;        // past headdim: the row's own first dims, and zero instead
+                    const u32x4 k = *(const u32x4 *)(kb + row_of(off, 16 * s + col) + (is ? c * 64 + grp * 16 : 0));
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) reg[x * 4 + w] = is ? k[w] : 0u;
+                }
+            }
+        };
+        // and as operands into a buffer; tokens that are none get V = 0
+        auto put = [&](u32x4 *buf, uint64_t ok) {
+            if (wave < T::VWAVES) {
+                u32x4 *to = buf + T::KOPS * 64 + lane;
+                if (ok != T::ALL) {
+#pragma unroll
+                    for (int x = 0; x < T::VL; ++x) {
+                        const int g = T::F32 ? (wave * T::VL + x) / VB : wave / VB * 8 + x;
+                        const bool is = ok >> ((g >> 2) * 16 + grp * 4 + (g & 3)) & 1;
+#pragma unroll
+                        for (int w = 0; w < T::VW; ++w) reg[x * T::VW + w] = is ? reg[x * T::VW + w] : 0u;
+                    }
+                }
+                if constexpr (T::F32) {
+#pragma unroll
+                    for (int x = 0; x < T::VL; ++x)
+                        to[(wave * T::VL + x) * 64] = (u32x4){reg[x * 4], reg[x * 4 + 1], reg[x * 4 + 2], reg[x * 4 + 3]};
+                } else if constexpr (CT == KBF16) {
+#pragma unroll
+                    for (int i = 0; i < VD; ++i) {
+                        u32x4 v;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = perm(reg[(2 * e + 1) * T::VW + i / 2], reg[2 * e * T::VW + i / 2], i & 1 ? 0x07060302u : 0x05040100u);
+                        to[(wave * VD + i) * 64] = v;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VD; i += 2) {
+                        u32x4 v0, v1;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t w = perm(reg[(2 * e + 1) * T::VW + i / 4], reg[2 * e * T::VW + i / 4], i & 2 ? 0x07030602u : 0x05010400u);
+                            v0[e] = widen<false>(w);
+                            v1[e] = widen<true>(w);
+                        }
+                        to[(wave * VD + i) * 64] = v0;
+                        to[(wave * VD + i + 1) * 64] = v1;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < T::KL; ++x) {
+                    u32x4 *to = buf + ((wave - T::VWAVES) * T::KL + x) * T::QW * 64 + lane;
+                    const uint32_t *k = reg + x * 4;
+                    if constexpr (CT == KF8) {
+                        to[0] = (u32x4){widen<false>(k[0]), widen<true>(k[0]), widen<false>(k[1]), widen<true>(k[1])};
+                        to[64] = (u32x4){widen<false>(k[2]), widen<true>(k[2]), widen<false>(k[3]), widen<true>(k[3])};
+                    } else {
+                        to[0] = (u32x4){k[0], k[1], k[2], k[3]};
+                    }
+                }
+            }
+        };
+
+        // The pipeline: a tile is weighed from one buffer while the next is on its way to registers, and goes to the
+        // other buffer behind it; pages are asked for two tiles ahead.
+        int t0 = u0 * T::NT, side = 0;
+        int page = page_of(t0);
+        uint64_t ok = __ballot((uint32_t)page < (uint32_t)a.n_pages) & T::ALL, ok_next = 0;
+        bring(off_of(t0, page));
+        page = page_of(t0 + T::NT);
+        __syncthreads();                     // readers of the prefix before
+        put(bufs, ok);
+        ok_next = __ballot((uint32_t)page < (uint32_t)a.n_pages) & T::ALL;
+        if (t0 + T::NT < t_end) bring(off_of(t0 + T::NT, page));
+        page = page_of(t0 + 2 * T::NT);
+        __syncthreads();
+        for (; t0 < t_end; t0 += T::NT, side ^= 1) {
+            const u32x4 *kop = bufs + side * T::BUF + lane, *vop = kop + T::KOPS * 64;
+            if (works) {
+                const bool masked = ok != T::ALL || !all_in;
+                const uint64_t bits = ok >> (grp * 4);
+#pragma unroll
+                for (int part = 0; part < T::NT / T::PT; ++part) {
+                    constexpr int SUB = T::PT / 16, NX = T::PT / 4, KN = T::KC * T::QW;
+                    f32x4 s[NQ][SUB];
+                    const u32x4 *kp = kop + part * SUB * KN * 64;
+#pragma unroll
+                    for (int i = 0; i < SUB; ++i) {
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) s[n][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int c = 0; c < KN; ++c) {
+                            const u32x4 k = kp[(i * KN + c) * 64];
+#pragma unroll
+                            for (int n = 0; n < NQ; ++n) {
+                                if constexpr (T::F32) {
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        s[n][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k[e]), __uint_as_float(q[n][c][e]), s[n][i], 0, 0, 0);
+                                } else {
+                                    s[n][i] = mfma_bf16(k, q[n][c], s[n][i]);
+                                }
+                            }
+                        }
+                    }
+                    ahead<SUB * KN, NQ * (T::F32 ? 4 : 1)>();
+                    // Scores that do not count are -inf for the maximum, and their weights 0.
+                    auto counts = [&](int n, int i) { return (bits >> ((part * SUB + (i >> 2)) * 16 + (i & 3)) & 1) && in[n]; };
+                    if (masked) {
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                            for (int i = 0; i < NX; ++i) s[n][i >> 2][i & 3] = counts(n, i) ? s[n][i >> 2][i & 3] : -INFINITY;
+                    }
+                    float top[NQ];
+                    bool higher = false;
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        top[n] = s[n][0][0];
+#pragma unroll
+                        for (int i = 1; i < NX; ++i) top[n] = fmaxf(top[n], s[n][i >> 2][i & 3]);
+                        top[n] = top[n] == -INFINITY ? -INFINITY : top[n] * scale2;
+                        higher = higher || top[n] > m[n] + kSlack;
+                    }
+                    if (__any(higher)) {
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) {
+                            const float m_new = fmaxf(m[n], head_max(top[n]));
+                            const float f = m_new == -INFINITY ? 1.0f : exp2_fast(m[n] - m_new);
+                            m[n] = m_new;
+                            l[n] *= f;
+#pragma unroll
+                            for (int b = 0; b < VB; ++b)
+#pragma unroll
+                                for (int i = 0; i < VD; ++i) acc[n][b][i] *= f;
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        const float m_use = m[n] == -INFINITY ? 0.0f : m[n];
+#pragma unroll
+                        for (int i = 0; i < NX; ++i) s[n][i >> 2][i & 3] = exp2_fast(fmaf(s[n][i >> 2][i & 3], scale2, -m_use));
+                        if (masked) {
+#pragma unroll
+                            for (int i = 0; i < NX; ++i) s[n][i >> 2][i & 3] = counts(n, i) ? s[n][i >> 2][i & 3] : 0.0f;
+                        }
+                        if constexpr (T::F32) {
+#pragma unroll
+                            for (int i = 0; i < NX; ++i) l[n][0] += s[n][i >> 2][i & 3];
+                        }
+                    }
+                    if constexpr (T::F32) {
+                        const u32x4 *vp = vop + part * NX * VB * 64;
+#pragma unroll
+                        for (int i = 0; i < NX; ++i)
+#pragma unroll
+                            for (int b = 0; b < VB; ++b) {
+                                const u32x4 v = vp[(i * VB + b) * 64];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                                    for (int n = 0; n < NQ; ++n)
+                                        acc[n][b][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(v[e]), s[n][i >> 2][i & 3], acc[n][b][e], 0, 0, 0);
+                            }
+                        ahead<NX * VB, NQ * 4>();
+                    } else {
+                        const u32x4 *vp = vop + part * VB * VD * 64;
+                        u32x4 ph[NQ], pl[NQ];
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float x0 = s[n][i >> 1][2 * i & 3], x1 = s[n][i >> 1][(2 * i & 3) + 1];
+                                ph[n][i] = pack_bf16(x0, x1);
+                                pl[n][i] = pack_bf16(minus(ph[n][i], low, x0), minus(ph[n][i], high, x1));
+                            }
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) {
+                            const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+                            l[n] = mfma_bf16(ones, ph[n], l[n]);
+                            l[n] = mfma_bf16(ones, pl[n], l[n]);
+                        }
+#pragma unroll
+                        for (int b = 0; b < VB; ++b)
+#pragma unroll
+                            for (int i = 0; i < VD; ++i) {
+                                const u32x4 v = vp[(b * VD + i) * 64];
+#pragma unroll
+                                for (int n = 0; n < NQ; ++n) acc[n][b][i] = mfma_bf16(v, ph[n], acc[n][b][i]);
+#pragma unroll
+                                for (int n = 0; n < NQ; ++n) acc[n][b][i] = mfma_bf16(v, pl[n], acc[n][b][i]);
+                            }
+                        ahead<VB * VD, NQ * 2>();
+                    }
+                }
+            }
+            ok = ok_next;
+            if (t0 + T::NT < t_end) {
+                put(bufs + (side ^ 1) * T::BUF, ok);
+                ok_next = __ballot((uint32_t)page < (uint32_t)a.n_pages) & T::ALL;
+                if (t0 + 2 * T::NT < t_end) bring(off_of(t0 + 2 * T::NT, page));
+                page = page_of(t0 + 3 * T::NT);
+            }
+            __syncthreads();
+        }
+    }
+
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        const float sum = T::F32 ? head_sum(l[n][0]) : l[n][0];
+        if (crow[n] < 0) continue;
+        const int64_t to = ((int64_t)at.split * a.batch + at.row0 + crow[n]) * a.n_heads + at.h0 + chead[n];
+        if (grp == 0) *(float2 *)(a.ml + to * 2) = make_float2(m[n], sum);
+        if (line.first >= line.last) continue;       // no tokens: weighs nothing
+#pragma unroll
+        for (int b = 0; b < VB; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int dim = (b * 16 + grp * 4 + r) * VD;
+                if (!EXACT && dim >= a.d) continue;
+#pragma unroll
+                for (int i = 0; i < VD; i += 4)
+                    *(f32x4 *)(a.part + to * a.d + dim + i) =
+                        (f32x4){acc[n][b][i][r], acc[n][b][i + 1][r], acc[n][b][i + 2][r], acc[n][b][i + 3][r]};
+            }
+    }
+}
+
+// Joins the parts of a (row, query head), a wave each; the row's own tokens are one more part, already
+// normalised.  Lane i forms the weight of part i; then 64 / (d / 4) parts at a time are added up, 4 dims a lane.
 template <bool BF16>
 __global__ void __launch_bounds__(kNT) prefix_join_kernel(Pp a) {
     const int lane = threadIdx.x & 63;
     const int64_t rh = (int64_t)blockIdx.x * kW + (threadIdx.x >> 6), all = (int64_t)a.batch * a.n_heads;
     if (rh >= all) return;
-    const int e = lane * 4;
-    const bool has = e < a.d;
+    const int d4 = a.d / 4, side = 64 / d4, sub = lane / d4, e = (lane - sub * d4) * 4;
+    const bool has = sub < side;
     const float own = a.lse_own[rh] * kLog2e;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (has) o = *(const f32x4 *)(a.o_own + rh * a.d + e);
-    float m = own;
-    for (int s = lane; s < a.splits; s += 64) m = fmaxf(m, a.ml[(s * all + rh) * 2]);
+    if (lane < d4) o = *(const f32x4 *)(a.o_own + rh * a.d + e);
+    float2 w = make_float2(-INFINITY, 0.0f);                  // (at most 64 parts)
+    if (lane < a.splits) w = *(const float2 *)(a.ml + (lane * all + rh) * 2);
+    float m = fmaxf(own, w.x);
 #pragma unroll
     for (int x = 32; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
-    const float m_use = m == -INFINITY ? 0.0f : m;
-    float sum = exp2_fast(own - m_use);
-    o *= sum;
-    for (int s = 0; s < a.splits; ++s) {
-        const float2 w = *(const float2 *)(a.ml + (s * all + rh) * 2);
-        const float f = exp2_fast(w.x - m_use);
-        sum += w.y == 0.0f ? 0.0f : w.y * f;
-        if (has && f > 0.0f && w.y != 0.0f) o += *(const f32x4 *)(a.part + (s * all + rh) * a.d + e) * (f * a.v_scale);
+    const float m_use = m == -INFINITY ? 0.0f : m, f = exp2_fast(w.x - m_use), own_f = exp2_fast(own - m_use);
+    float sum = w.y == 0.0f ? 0.0f : w.y * f;
+#pragma unroll
+    for (int x = 32; x > 0; x >>= 1) sum += __shfl_xor(sum, x);
+    sum += own_f;
+    o *= own_f;
+    // what weighs nothing may never have been written
+    const float part_f = f > 0.0f && w.y != 0.0f ? f * a.v_scale : 0.0f;
+#pragma unroll 8
+    for (int s0 = 0; s0 < a.splits; s0 += side) {
+        const int s = s0 + sub;
+        const float x = __shfl(part_f, s & 63);
+        if (has && s < a.splits && x != 0.0f) o += *(const f32x4 *)(a.part + (s * all + rh) * a.d + e) * x;
     }
+    for (int s = 1; s < side; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x = __shfl(o[i], lane + s * d4);
+            o[i] += sub == 0 ? x : 0.0f;
+        }
     const float n = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-    if (has) {
+    if (lane < d4) {
         if constexpr (BF16) *(uint2 *)(a.o + (rh * a.d + e) * 2) = make_uint2(pack_bf16(o[0] * n, o[1] * n), pack_bf16(o[2] * n, o[3] * n));
         else *(f32x4 *)(a.o + (rh * a.d + e) * 4) = o * n;
     }
@@ -416,58 +835,61 @@ __global__ void __launch_bounds__(kNT) prefix_join_kernel(Pp a) {
 int64_t align16(int64_t n) { return (n + 15) & ~int64_t(15); }
 
 // How the columns of all rows are cut into blocks
-struct Cut { int nq, gm, passes, rows, tiles, splits; };
-Cut cut_of(int64_t batch, int64_t n_heads, int64_t n_kv, int64_t d, int64_t max_len) {
+struct Cut { int nq, gm, passes, rows, tiles, splits; bool many; };
+Cut cut_of(int64_t batch, int64_t n_heads, int64_t n_kv, int64_t d, int64_t max_len, int64_t n_prefixes) {
     Cut c;
-    const int64_t group = n_heads / n_kv, cols = batch * group;
-    c.nq = (int)std::min<int64_t>(d <= 128 ? 4 : 2, cols > 32 ? 4 : cols > 16 ? 2 : 1);
-    c.gm = (int)std::min<int64_t>(group, 16 * c.nq);
+    const int64_t group = n_heads / n_kv, all = batch * group;
+    c.many = all > 32;
+    c.nq = !c.many ? (all > 16 ? 2 : 1) : all > 64 && d <= 128 ? 2 : 1;
+    const int64_t cols = 16 * c.nq * (c.many ? kW : 1);
+    c.gm = (int)std::min<int64_t>(group, cols);
     c.passes = (int)((group + c.gm - 1) / c.gm);
-    c.rows = (int)std::min<int64_t>(batch, 16 * c.nq / c.gm);
+    c.rows = (int)std::min<int64_t>(std::min<int64_t>(batch, cols / c.gm), 64);
     c.tiles = (int)((batch + c.rows - 1) / c.rows);
-    // one block a compute unit, of at least a unit of 64 tokens
-    const int64_t heads = c.tiles * n_kv * c.passes, units = std::max<int64_t>(1, max_len / 128);
-    c.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(kCUs / heads, units), 64));
+    // two blocks a compute unit, of at least some 128 tokens
+    const int64_t heads = c.tiles * n_kv * c.passes;
+    const int64_t units = std::max<int64_t>(1, (max_len + 127) / 128 * std::min<int64_t>(n_prefixes, c.rows));
+    c.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(2 * kCUs / heads, units), 64));
     return c;
 }
 
-template <int CT, int DP, bool EXACT, int NQ>
-hipError_t go_q(const Pp &k, hipStream_t stream) {
-    using T = PTile<CT, DP>;
-    const size_t lds = std::max((size_t)kW * 16 * (DP + 4) * sizeof(float), (size_t)T::KC * T::QW * NQ * 1024);
+template <typename F>
+hipError_t launch_with(F kernel, size_t lds, const Pp &k, hipStream_t stream) {
     if (lds > 32 * 1024) {               // more than a block has unasked, from 64 KiB on
-        const hipError_t e = hipFuncSetAttribute((const void *)prefix_attn_kernel<CT, DP, EXACT, NQ>,
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess) return e;
     }
     const unsigned grid = (unsigned)((k.combos + 7) / 8 * 8 * k.tiles);
-    hipLaunchKernelGGL((prefix_attn_kernel<CT, DP, EXACT, NQ>), dim3(grid), dim3(kNT), lds, stream, k);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kNT), lds, stream, k);
     return hipGetLastError();
 }
-template <int CT, int DP, bool EXACT>
-hipError_t go(const Pp &k, int nq, hipStream_t stream) {
-    if constexpr (DP <= 128) {
-        if (nq == 4) return go_q<CT, DP, EXACT, 4>(k, stream);
+template <int CT, int DP, bool EXACT, int NQ>
+hipError_t go_q(const Pp &k, bool many, hipStream_t stream) {
+    using T = PTile<CT, DP>;
+    if constexpr (DP <= 128 || NQ == 1) {
+        if (many) return launch_with(prefix_many_kernel<CT, DP, EXACT, NQ>, 2 * FTile<CT, DP>::BUF * 16, k, stream);
     }
-    return nq == 2 ? go_q<CT, DP, EXACT, 2>(k, stream) : go_q<CT, DP, EXACT, 1>(k, stream);
+    const size_t lds = std::max((size_t)kW * 16 * NQ * (DP + 4) * sizeof(float), (size_t)T::KC * T::QW * NQ * 1024);
+    return launch_with(prefix_few_kernel<CT, DP, EXACT, NQ>, lds, k, stream);
 }
 template <int CT, int DP>
-hipError_t go_d(const Pp &k, int nq, hipStream_t stream) {
-    return k.d == DP ? go<CT, DP, true>(k, nq, stream) : go<CT, DP, false>(k, nq, stream);
+hipError_t go_d(const Pp &k, const Cut &c, hipStream_t stream) {
+    if (k.d == DP) return c.nq == 2 ? go_q<CT, DP, true, 2>(k, c.many, stream) : go_q<CT, DP, true, 1>(k, c.many, stream);
+    return c.nq == 2 ? go_q<CT, DP, false, 2>(k, c.many, stream) : go_q<CT, DP, false, 1>(k, c.many, stream);
 }
 template <int CT>
-hipError_t go_type(const Pp &k, int nq, hipStream_t stream) {
-    if (k.d <= 64) return go_d<CT, 64>(k, nq, stream);
-    if (k.d <= 128) return go_d<CT, 128>(k, nq, stream);
-    if (k.d <= 192) return go_d<CT, 192>(k, nq, stream);
-    return go_d<CT, 256>(k, nq, stream);
+hipError_t go_type(const Pp &k, const Cut &c, hipStream_t stream) {
+    if (k.d <= 64) return go_d<CT, 64>(k, c, stream);
+    if (k.d <= 128) return go_d<CT, 128>(k, c, stream);
+    if (k.d <= 192) return go_d<CT, 192>(k, c, stream);
+    return go_d<CT, 256>(k, c, stream);
 }
 
 }  // namespace
 
 size_t prefix_attn_workspace_bytes(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t headdim,
                                    int64_t max_prefix_pages, int64_t max_pages, int64_t page_size) {
-    const Cut c = cut_of(batch, n_heads, n_kv_heads, headdim, max_prefix_pages * page_size);
+    const Cut c = cut_of(batch, n_heads, n_kv_heads, headdim, max_prefix_pages * page_size, batch);   // (the most splits that any number has)
     const int64_t rh = batch * n_heads;
     return align16(paged_attn_workspace_bytes(batch, n_heads, n_kv_heads, headdim, max_pages, page_size)) +
            align16(rh * headdim * 4) + align16(rh * 4) + align16(c.splits * rh * 8) + c.splits * rh * headdim * 4;
@@ -477,7 +899,7 @@ hipError_t launch_prefix_attn(const PrefixAttnArgs &p, hipStream_t stream, const
     PagedAttnArgs a = p.own;
     const int e = a.kv_dtype == SSM_KV_F32 ? 4 : a.kv_dtype == SSM_KV_BF16 ? 2 : 1, qe = a.kv_dtype == SSM_KV_F32 ? 4 : 2;
     const int64_t rh = a.batch * a.n_heads;
-    const Cut c = cut_of(a.batch, a.n_heads, a.n_kv_heads, a.headdim, p.max_prefix_pages * a.page_size);
+    const Cut c = cut_of(a.batch, a.n_heads, a.n_kv_heads, a.headdim, p.max_prefix_pages * a.page_size, p.n_prefixes);
     char *ws = (char *)a.workspace + align16(paged_attn_workspace_bytes(a.batch, a.n_heads, a.n_kv_heads, a.headdim, a.max_pages, a.page_size));
     Pp k = {};
     k.o_own = (const float *)ws; ws += align16(rh * a.headdim * 4);
@@ -499,9 +921,9 @@ hipError_t launch_prefix_attn(const PrefixAttnArgs &p, hipStream_t stream, const
     a.o = (void *)k.o_own; a.lse = (float *)k.lse_own; a.o_f32 = true;
     hipError_t rc = launch_paged_attn(a, stream, kernel_name);
     if (rc != hipSuccess) return rc;
-    *kernel_name = "prefix_attn_kernel";
-    rc = a.kv_dtype == SSM_KV_F32 ? go_type<KF32>(k, c.nq, stream)
-       : a.kv_dtype == SSM_KV_BF16 ? go_type<KBF16>(k, c.nq, stream) : go_type<KF8>(k, c.nq, stream);
+    *kernel_name = c.many ? "prefix_many_kernel" : "prefix_few_kernel";
+    rc = a.kv_dtype == SSM_KV_F32 ? go_type<KF32>(k, c, stream)
+       : a.kv_dtype == SSM_KV_BF16 ? go_type<KBF16>(k, c, stream) : go_type<KF8>(k, c, stream);
     if (rc != hipSuccess) return rc;
     *kernel_name = "prefix_join_kernel";
     const dim3 grid((unsigned)((rh + kW - 1) / kW));

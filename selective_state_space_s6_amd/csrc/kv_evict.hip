@@ -17,11 +17,11 @@
 namespace ssm {
 namespace {
 
-constexpr int kPick = 1024;         // threads of the choice
 constexpr int kMove = 256;          // threads of the move
 constexpr int kRun = 8;             // 16-byte pieces of a thread in a run
 constexpr int kMostKept = 32768;    // keys that the choice keeps in shared memory at most
 
+template <int kPick>                // threads
 __global__ void __launch_bounds__(kPick) evict_pick_kernel(KvEvictArgs a, int room) {
     __shared__ TopKShared<kPick> sh;
     extern __shared__ uint32_t own[];
@@ -44,7 +44,21 @@ __global__ void __launch_bounds__(kPick) evict_pick_kernel(KvEvictArgs a, int ro
         if ((uint32_t)page >= (uint32_t)a.n_pages) return kKeyLowest;
         return key_of(a.mass[((int64_t)page * a.n_kv + g) * a.page_size + ps.place(i, p)]);
     };
-    for (int i = tid; i < min(m, room); i += kPick) own[i] = load(i);
+    constexpr int U = 8;                          // keys of a thread on their way at once
+    for (int i0 = tid; i0 < min(m, room); i0 += U * kPick) {
+        int page[U], p[U];
+        float x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) page[u] = table[p[u] = ps.of(min(i0 + u * kPick, m - 1))];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = (uint32_t)page[u] < (uint32_t)a.n_pages ? page[u] : 0;
+            x[u] = a.mass[((int64_t)at * a.n_kv + g) * a.page_size + ps.place(min(i0 + u * kPick, m - 1), p[u])];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * kPick < min(m, room)) own[i0 + u * kPick] = (uint32_t)page[u] < (uint32_t)a.n_pages ? key_of(x[u]) : kKeyLowest;
+    }
     __syncthreads();
     auto key = [&](int i) { return i < room ? own[i] : load(i); };
     const Cut cut = find_cut<kPick>(sh, m, want, key);
@@ -80,62 +94,65 @@ __global__ void __launch_bounds__(kMove) evict_move_kernel(KvEvictArgs a, int sl
     const int n = min(max(a.lens[row], 0), a.max_pages * a.page_size);
     if (n <= a.budget) return;
     const int32_t *kept = a.kept + (int64_t)hr * a.budget, *table = a.table + (int64_t)row * a.table_stride;
-    const int from = first_moved(kept, a.budget);
-    // a token's page (-1: none) and place
-    auto page_at = [&](int p) { return (uint32_t)table[p] < (uint32_t)a.n_pages ? table[p] : -1; };
-
-    if (part == 2 * slices) {
-        for (int base = from; base < a.budget; base += kMove * kRun) {
-            float x[kRun];
-            int to[kRun];                         // page of the new place, -1: not moved
-#pragma unroll
-            for (int u = 0; u < kRun; ++u) {
-                const int i = base + u * kMove + tid;
-                to[u] = -1;
-                x[u] = 0.0f;
-                if (i < a.budget) {
-                    const int j = kept[i], pj = ps.of(j), src = page_at(pj);
-                    to[u] = src >= 0 ? page_at(ps.of(i)) : -1;
-                    if (src >= 0) x[u] = a.mass[((int64_t)src * a.n_kv + g) * a.page_size + ps.place(j, pj)];
-                }
-            }
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // every value is in a register
-            __syncthreads();
-#pragma unroll
-            for (int u = 0; u < kRun; ++u) {
-                const int i = base + u * kMove + tid;
-                if (to[u] >= 0) a.mass[((int64_t)to[u] * a.n_kv + g) * a.page_size + ps.place(i, ps.of(i))] = x[u];
-            }
-        }
-        return;
-    }
-    const int pieces = a.row_bytes / 16;          // of a row
-    const int s = part >> 1;
-    char *cache = (part & 1 ? a.v : a.k) + (int64_t)g * a.c_sh;
-    const int c0 = s * pieces / slices, cs = (s + 1) * pieces / slices - c0;
+    // Runs of tokens.  Where a token comes from and goes to is looked up a run ahead, and stays unmoved where both are
+    // one or have no page.
+    const bool is_mass = part == 2 * slices;
+    const int pieces = a.row_bytes / 16, s = part >> 1;
+    const int c0 = is_mass ? 0 : s * pieces / slices, cs = is_mass ? 1 : (s + 1) * pieces / slices - c0;
     const int side = kMove / cs;                  // tokens side by side
     const int sub = tid / cs, c = c0 + tid - sub * cs;
     const bool works = sub < side;
-    for (int base = from; base < a.budget; base += side * kRun) {
-        u32x4 x[kRun];
-        int to[kRun];
+    const int run = side * kRun;
+    const int from = a.budget > 8 * run ? first_moved(kept, a.budget) : 0;
+    struct Move { int src, dst; };                // token places among all (page * page_size + place); src < 0: none
+    Move now[kRun], next[kRun];
+    auto look_up = [&](Move (&m)[kRun], int base) {
+        int j[kRun], src[kRun], dst[kRun];
+        // (without branches: all of a run's loads on their way together)
+#pragma unroll
+        for (int u = 0; u < kRun; ++u) j[u] = kept[min(base + u * side + sub, a.budget - 1)];
+#pragma unroll
+        for (int u = 0; u < kRun; ++u) {
+            src[u] = table[ps.of(j[u])];
+            dst[u] = table[ps.of(min(base + u * side + sub, a.budget - 1))];
+        }
 #pragma unroll
         for (int u = 0; u < kRun; ++u) {
             const int i = base + u * side + sub;
-            to[u] = -1;
-            x[u] = (u32x4){0, 0, 0, 0};
-            if (works && i < a.budget) {
-                const int j = kept[i], pj = ps.of(j), src = page_at(pj);
-                to[u] = src >= 0 ? page_at(ps.of(i)) : -1;
-                if (src >= 0) x[u] = *(const u32x4 *)(cache + (int64_t)src * a.c_sp + (int64_t)ps.place(j, pj) * a.c_st + c * 16);
-            }
+            const bool is = works && i < a.budget && j[u] != i && (uint32_t)src[u] < (uint32_t)a.n_pages && (uint32_t)dst[u] < (uint32_t)a.n_pages;
+            m[u].src = is ? src[u] * a.page_size + ps.place(j[u], ps.of(j[u])) : -1;
+            m[u].dst = is ? dst[u] * a.page_size + ps.place(i, ps.of(i)) : -1;
         }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    };
+    look_up(next, from);
+    char *cache = (part & 1 ? a.v : a.k) + (int64_t)g * a.c_sh + c * 16;
+    auto row_of = [&](int t) {
+        const int page = ps.of(t);
+        return cache + (int64_t)page * a.c_sp + (int64_t)ps.place(t, page) * a.c_st;
+    };
+    auto mass_of = [&](int t) {
+        const int page = ps.of(t);
+        return a.mass + ((int64_t)page * a.n_kv + g) * a.page_size + ps.place(t, page);
+    };
+    for (int base = from; base < a.budget; base += run) {
+#pragma unroll
+        for (int u = 0; u < kRun; ++u) now[u] = next[u];
+        u32x4 x[kRun];
+#pragma unroll
+        for (int u = 0; u < kRun; ++u) {
+            x[u] = (u32x4){0, 0, 0, 0};
+            if (now[u].src < 0) continue;
+            if (is_mass) x[u][0] = __float_as_uint(*mass_of(now[u].src));
+            else x[u] = *(const u32x4 *)row_of(now[u].src);
+        }
+        if (base + run < a.budget) look_up(next, base + run);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // every value of the run is in a register
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < kRun; ++u) {
-            const int i = base + u * side + sub;
-            if (to[u] >= 0) *(u32x4 *)(cache + (int64_t)to[u] * a.c_sp + (int64_t)ps.place(i, ps.of(i)) * a.c_st + c * 16) = x[u];
+            if (now[u].src < 0) continue;
+            if (is_mass) *mass_of(now[u].dst) = __uint_as_float(x[u][0]);
+            else *(u32x4 *)row_of(now[u].dst) = x[u];
         }
     }
 }
@@ -146,11 +163,15 @@ hipError_t launch_kv_evict(const KvEvictArgs &a, hipStream_t stream, const char 
     *kernel_name = "evict_pick_kernel";
     const int64_t heads = (int64_t)a.batch * a.n_kv, most = (int64_t)a.max_pages * a.page_size;
     const int room = (int)std::min<int64_t>(most, kMostKept);
+    // 16 waves where that is one block a compute unit at most, else 8
+    const bool wide = heads <= 256;
     if (room > 8192) {                   // more than a block has unasked
-        const hipError_t e = hipFuncSetAttribute((const void *)evict_pick_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, room * 4);
+        const hipError_t e = hipFuncSetAttribute(wide ? (const void *)evict_pick_kernel<1024> : (const void *)evict_pick_kernel<512>,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, room * 4);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(evict_pick_kernel, dim3((unsigned)heads), dim3(kPick), (size_t)room * 4, stream, a, room);
+    if (wide) hipLaunchKernelGGL((evict_pick_kernel<1024>), dim3((unsigned)heads), dim3(1024), (size_t)room * 4, stream, a, room);
+    else hipLaunchKernelGGL((evict_pick_kernel<512>), dim3((unsigned)heads), dim3(512), (size_t)room * 4, stream, a, room);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || most <= a.budget) return e;
     *kernel_name = "evict_move_kernel";

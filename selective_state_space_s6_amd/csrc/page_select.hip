@@ -18,9 +18,10 @@
 namespace ssm {
 namespace {
 
-constexpr int kNT = 256;            // threads of a block, both kernels
+constexpr int kNT = 256;            // threads of a scoring block
 constexpr int kPages = 2;           // pages of a lane
 constexpr int kStep = kNT / 4 * kPages;      // pages of a block
+constexpr int kBlocks = 2048;       // scoring blocks: twice what is resident at once, since rows' lengths differ
 constexpr int kKept = 8192;         // keys that the choice keeps in shared memory
 
 template <int CT> struct Wide {
@@ -48,33 +49,47 @@ __global__ void __launch_bounds__(kNT) page_score_kernel(PageSelectArgs a, int c
     const int n = ps.to_hold(min(max(a.lens[row], 0), a.max_pages * a.page_size));
     if (n <= a.top_k) return;                     // all of them: no score is asked for
     const int lo = a.first, hi = n - a.last;      // what scores decide about
+    if (lo + chunk * kStep >= hi) return;
     const int group = a.n_heads / a.n_kv, dims = a.d / N;            // chunks of 16 bytes
     const int64_t row_bytes = (int64_t)dims * 16;
     uint32_t *keys = a.keys + (int64_t)hr * a.max_pages;
     const int32_t *table = a.table + (int64_t)row * a.table_stride;
     constexpr int PITCH = N * GH + 1;             // (a chunk further is another bank)
+    auto page_at = [&](int i) { return i < hi ? table[i] : -1; };
+    auto load_q = [&](int h0) {
+        for (int i = tid; i < a.d * GH; i += kNT) {
+            const int dim = i / GH, h = i - dim * GH;
+            double v = 0.0;
+            if (h0 + h < group) {
+                const int64_t at = row * a.q_sr + (int64_t)(g * group + h0 + h) * a.q_sh + dim;
+                v = a.bf16 ? (double)lo_f(((const uint16_t *)a.q)[at]) : (double)((const float *)a.q)[at];
+            }
+            // (a NaN stays one)
+            qs[dim / N * PITCH + dim % N * GH + h] = make_double2(v > 0.0 || v != v ? v : 0.0, v < 0.0 || v != v ? v : 0.0);
+        }
+    };
+    int next[kPages];
+#pragma unroll
+    for (int u = 0; u < kPages; ++u) next[u] = page_at(lo + chunk * kStep + u * (kNT / 4) + (tid >> 2));
+    if (group <= GH) {
+        load_q(0);
+        __syncthreads();
+    }
     for (int p0 = lo + chunk * kStep; p0 < hi; p0 += chunks * kStep) {
         uint32_t best[kPages];
         int page[kPages];
+        const char *b[kPages];
 #pragma unroll
         for (int u = 0; u < kPages; ++u) {
-            const int i = p0 + u * (kNT / 4) + (tid >> 2);
-            page[u] = i < hi ? table[i] : -1;
+            page[u] = next[u];
+            next[u] = page_at(p0 + chunks * kStep + u * (kNT / 4) + (tid >> 2));
             best[u] = 0;
+            b[u] = a.bounds + ((int64_t)((uint32_t)page[u] < (uint32_t)a.n_pages ? page[u] : 0) * a.n_kv + g) * 2 * row_bytes + l * 16;
         }
         for (int h0 = 0; h0 < group; h0 += GH) {
-            if (p0 == lo + chunk * kStep || group > GH) {
+            if (group > GH) {
                 __syncthreads();
-                for (int i = tid; i < a.d * GH; i += kNT) {
-                    const int dim = i / GH, h = i - dim * GH;
-                    double v = 0.0;
-                    if (h0 + h < group) {
-                        const int64_t at = row * a.q_sr + (int64_t)(g * group + h0 + h) * a.q_sh + dim;
-                        v = a.bf16 ? (double)lo_f(((const uint16_t *)a.q)[at]) : (double)((const float *)a.q)[at];
-                    }
-                    // (a NaN stays one)
-                    qs[dim / N * PITCH + dim % N * GH + h] = make_double2(v > 0.0 || v != v ? v : 0.0, v < 0.0 || v != v ? v : 0.0);
-                }
+                load_q(h0);
                 __syncthreads();
             }
             double acc[kPages][GH];
@@ -82,22 +97,27 @@ __global__ void __launch_bounds__(kNT) page_score_kernel(PageSelectArgs a, int c
             for (int u = 0; u < kPages; ++u)
 #pragma unroll
                 for (int h = 0; h < GH; ++h) acc[u][h] = 0.0;
-            for (int c = l; c < dims; c += 4) {
-                u32x4 low[kPages], high[kPages];
+            u32x4 low[kPages], high[kPages];
+            auto load = [&](int c) {
 #pragma unroll
                 for (int u = 0; u < kPages; ++u) {
-                    const uint32_t p = (uint32_t)page[u] < (uint32_t)a.n_pages ? page[u] : 0;
-                    const char *b = a.bounds + ((int64_t)p * a.n_kv + g) * 2 * row_bytes + c * 16;
-                    low[u] = *(const u32x4 *)b;
-                    high[u] = *(const u32x4 *)(b + row_bytes);
+                    low[u] = *(const u32x4 *)(b[u] + (c - l) * 16);
+                    high[u] = *(const u32x4 *)(b[u] + row_bytes + (c - l) * 16);
                 }
+            };
+            if (l < dims) load(l);
+            for (int c = l; c < dims; c += 4) {
+                u32x4 x0[kPages], y0[kPages];
+#pragma unroll
+                for (int u = 0; u < kPages; ++u) { x0[u] = low[u]; y0[u] = high[u]; }
+                if (c + 4 < dims) load(c + 4);
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
                     double x[kPages], y[kPages];
 #pragma unroll
                     for (int u = 0; u < kPages; ++u) {
-                        x[u] = Wide<CT>::at(low[u], e);
-                        y[u] = Wide<CT>::at(high[u], e);
+                        x[u] = Wide<CT>::at(x0[u], e);
+                        y[u] = Wide<CT>::at(y0[u], e);
                     }
 #pragma unroll
                     for (int h = 0; h < GH; ++h) {
@@ -127,8 +147,9 @@ __global__ void __launch_bounds__(kNT) page_score_kernel(PageSelectArgs a, int c
     }
 }
 
-__global__ void __launch_bounds__(kNT) page_select_kernel(PageSelectArgs a) {
-    __shared__ TopKShared<kNT> sh;
+template <int NT>                   // threads
+__global__ void __launch_bounds__(NT) page_select_kernel(PageSelectArgs a) {
+    __shared__ TopKShared<NT> sh;
     __shared__ uint32_t kept[kKept];
     const int tid = threadIdx.x;
     const int row = blockIdx.x / a.n_kv;
@@ -136,27 +157,27 @@ __global__ void __launch_bounds__(kNT) page_select_kernel(PageSelectArgs a) {
     const int n = ps.to_hold(min(max(a.lens[row], 0), a.max_pages * a.page_size));
     int32_t *out = a.selected + (int64_t)blockIdx.x * a.top_k;
     if (n <= a.top_k) {
-        for (int i = tid; i < a.top_k; i += kNT) out[i] = i < n ? i : -1;
+        for (int i = tid; i < a.top_k; i += NT) out[i] = i < n ? i : -1;
         return;
     }
     const int m = n - a.first - a.last, want = a.top_k - a.first - a.last;
-    for (int i = tid; i < a.first; i += kNT) out[i] = i;
-    for (int i = tid; i < a.last; i += kNT) out[a.top_k - a.last + i] = n - a.last + i;
+    for (int i = tid; i < a.first; i += NT) out[i] = i;
+    for (int i = tid; i < a.last; i += NT) out[a.top_k - a.last + i] = n - a.last + i;
     if (want == 0) return;
     const uint32_t *keys = a.keys + (int64_t)blockIdx.x * a.max_pages + a.first;
-    for (int i = tid; i < min(m, kKept); i += kNT) kept[i] = keys[i];
+    for (int i = tid; i < min(m, kKept); i += NT) kept[i] = keys[i];
     __syncthreads();
     auto key = [&](int i) { return i < kKept ? kept[i] : keys[i]; };
-    const Cut cut = find_cut<kNT>(sh, m, want, key);
-    put_chosen<kNT>(sh, m, cut, key, [&](int place, int i) { out[a.first + place] = a.first + i; });
+    const Cut cut = find_cut<NT>(sh, m, want, key);
+    put_chosen<NT>(sh, m, cut, key, [&](int place, int i) { out[a.first + place] = a.first + i; });
 }
 
 template <int CT>
 void go(const PageSelectArgs &a, hipStream_t stream) {
     const int group = a.n_heads / a.n_kv;
-    // blocks that share the pages of a (row, kv head): all of them where that is few blocks in all
+    // blocks that share the pages of a (row, kv head)
     const int64_t heads = (int64_t)a.batch * a.n_kv;
-    const int64_t chunks = std::max<int64_t>(1, std::min<int64_t>((a.max_pages + kStep - 1) / kStep, 16384 / heads));
+    const int64_t chunks = std::max<int64_t>(1, std::min<int64_t>((a.max_pages + kStep - 1) / kStep, kBlocks / heads));
     const dim3 grid((unsigned)(heads * chunks));
     const int gh = group >= 5 ? 8 : group >= 3 ? 4 : group;
     const size_t lds = (size_t)(a.d / Wide<CT>::N) * (Wide<CT>::N * gh + 1) * sizeof(double2);
@@ -184,7 +205,11 @@ hipError_t launch_page_select(const PageSelectArgs &a, hipStream_t stream, const
         if (e != hipSuccess) return e;
     }
     *kernel_name = "page_select_kernel";
-    hipLaunchKernelGGL(page_select_kernel, dim3((unsigned)(a.batch * a.n_kv)), dim3(kNT), 0, stream, a);
+    // (16 waves where that is one block a compute unit at most, else 8: 256 choices among up to 2048 pages 7.6 us with 16, 8.4
+    // with 8, 12 with 4)
+    const int64_t heads = (int64_t)a.batch * a.n_kv;
+    if (heads <= 256) hipLaunchKernelGGL((page_select_kernel<1024>), dim3((unsigned)heads), dim3(1024), 0, stream, a);
+    else hipLaunchKernelGGL((page_select_kernel<512>), dim3((unsigned)heads), dim3(512), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -2,10 +2,11 @@
 // indexes in rising order.
 //
 // Keys are 32 bits whose order as whole numbers is the wanted one (key_of).  The want-th largest is
-// found from the top byte down: counts of the next byte's values among the keys that match so far, in
-// shared memory, until a value's keys are wanted whole or all four bytes are known; counts of whole
-// numbers do not depend on the order in which they are added.  A second pass counts, index by index,
-// the keys above and equal, and so places the chosen ones in their order without a sort.
+// found from the top 11 bits down (11, 11, 10): counts of the next bits' values among the keys that match so
+// far, in shared memory, until a value's keys are wanted whole or all bits are known; counts of whole
+// numbers do not depend on the order in which they are added.  (By 8 bits it would be four rounds, and the
+// first, sign and most of the exponent, would add most keys of one magnitude to a few counters.)  A second pass counts, index by index, the keys above and equal, and so
+// places the chosen ones in their order without a sort.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -24,8 +25,8 @@ constexpr uint32_t kKeyLowest = 0x007fffffu;      // of -inf
 
 template <int NT>
 struct TopKShared {
-    int hist[256];
-    int sums[NT / 64];
+    int hist[2048];
+    int sums[NT / 64], equal[NT / 64];
     int bin, left, whole;
 };
 
@@ -35,79 +36,81 @@ struct Cut { int64_t above; int ties; };
 // 0 < want <= n; every thread of the block calls it
 template <int NT, typename Key>
 __device__ __forceinline__ Cut find_cut(TopKShared<NT> &sh, int n, int want, Key key) {
-    const int tid = threadIdx.x, lane = tid & 63;
+    constexpr int B = 2048 / NT, W = NT / 64;     // counters of a thread
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     uint32_t prefix = 0, mask = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += NT) sh.hist[i] = 0;
+#pragma unroll
+    for (int round = 0; round < 3; ++round) {
+        const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
+        const uint32_t digit = round == 2 ? 1023u : 2047u;
+#pragma unroll
+        for (int i = 0; i < B; ++i) sh.hist[i * NT + tid] = 0;
         __syncthreads();
         for (int i = tid; i < n; i += NT) {
             const uint32_t k = key(i);
-            if ((k & mask) == prefix) atomicAdd(&sh.hist[k >> shift & 255], 1);
+            if ((k & mask) == prefix) atomicAdd(&sh.hist[k >> shift & digit], 1);
         }
         __syncthreads();
-        if (tid < 64) {                           // lane 0 has the highest values
-            int c[4], own = 0;
+        int c[B], own = 0;                        // thread 0 has the highest values
 #pragma unroll
-            for (int i = 0; i < 4; ++i) own += c[i] = sh.hist[255 - 4 * lane - i];
-            int before = wave_scan(own) - own;
-            if (before < want && want <= before + own) {
-                int i = 0;
-                while (before + c[i] < want) before += c[i++];
-                sh.bin = 255 - 4 * lane - i;
-                sh.left = want - before;
-                sh.whole = c[i] == want - before;
+        for (int i = 0; i < B; ++i) own += c[i] = sh.hist[2047 - B * tid - i];
+        int before = wave_scan(own);
+        if (lane == 63) sh.sums[wave] = before;
+        before -= own;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w) before += w < wave ? sh.sums[w] : 0;
+        if (before < want && want <= before + own) {
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                if (before < want && want <= before + c[i]) {
+                    sh.bin = 2047 - B * tid - i;
+                    sh.left = want - before;
+                    sh.whole = c[i] == want - before;
+                }
+                before += c[i];
             }
         }
         __syncthreads();
         prefix |= (uint32_t)sh.bin << shift;
-        mask |= 0xffu << shift;
+        mask |= digit << shift;
         want = sh.left;
         if (sh.whole) return {(int64_t)prefix - 1, 0};
     }
     return {(int64_t)prefix, want};
 }
 
-// Calls put(place, i) for every chosen index i; places rise with i, from 0 on.
+// Calls put(place, i) for every chosen index i; places rise with i, from 0 on.  A wave has consecutive
+// indexes, 64 at a time, counts them, and goes over them again once it knows what stands before them.
 template <int NT, typename Key, typename Put>
 __device__ __forceinline__ void put_chosen(TopKShared<NT> &sh, int n, Cut cut, Key key, Put put) {
-    constexpr int V = 4, W = NT / 64;             // consecutive indexes of a thread
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int above = 0, equal = 0;                     // before this round's indexes
-    for (int base = 0; base < n; base += NT * V) {
-        uint32_t k[V];
-        int own = 0;                              // keys above in the low half, equal ones in the high half
+    constexpr int W = NT / 64;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int part = (n + NT - 1) / NT * 64, i0 = wave * part, i1 = min(i0 + part, n);
+    const uint64_t lower = (uint64_t(1) << lane) - 1;
+    int above = 0, equal = 0;
+#pragma unroll 4
+    for (int i = i0 + lane; i - lane < i1; i += 64) {
+        const int64_t k = i < i1 ? (int64_t)key(i) : -2;
+        above += __popcll(__ballot(k > cut.above));
+        equal += __popcll(__ballot(k == cut.above));
+    }
+    if (lane == 0) { sh.sums[wave] = above; sh.equal[wave] = equal; }
+    __syncthreads();
+    above = equal = 0;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int i = base + tid * V + v;
-            k[v] = i < n ? key(i) : 0u;
-            if (i < n) own += ((int64_t)k[v] > cut.above ? 1 : 0) + ((int64_t)k[v] == cut.above ? 1 << 16 : 0);
-        }
-        int at = wave_scan(own);
-        if (lane == 63) sh.sums[wave] = at;
-        at -= own;
-        __syncthreads();
-        int all = 0;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            at += w < wave ? sh.sums[w] : 0;
-            all += sh.sums[w];
-        }
-        int a = above + (at & 0xffff), e = equal + (at >> 16);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int i = base + tid * V + v;
-            if (i >= n) break;
-            if ((int64_t)k[v] > cut.above) {
-                put(a + min(e, cut.ties), i);
-                ++a;
-            } else if ((int64_t)k[v] == cut.above) {
-                if (e < cut.ties) put(a + e, i);
-                ++e;
-            }
-        }
-        above += all & 0xffff;
-        equal += all >> 16;
-        __syncthreads();                          // readers of sums
+    for (int w = 0; w < W; ++w) {
+        above += w < wave ? sh.sums[w] : 0;
+        equal += w < wave ? sh.equal[w] : 0;
+    }
+#pragma unroll 4
+    for (int i = i0 + lane; i - lane < i1; i += 64) {
+        const int64_t k = i < i1 ? (int64_t)key(i) : -2;
+        const uint64_t a = __ballot(k > cut.above), e = __ballot(k == cut.above);
+        const int mine = equal + __popcll(e & lower), place = above + __popcll(a & lower) + min(mine, cut.ties);
+        if (k > cut.above || (k == cut.above && mine < cut.ties)) put(place, i);
+        above += __popcll(a);
+        equal += __popcll(e);
     }
 }
 

@@ -811,11 +811,18 @@ __global__ void __launch_bounds__(kNT) prefix_join_kernel(Pp a) {
     o *= own_f;
     // what weighs nothing may never have been written
     const float part_f = f > 0.0f && w.y != 0.0f ? f * a.v_scale : 0.0f;
-#pragma unroll 8
-    for (int s0 = 0; s0 < a.splits; s0 += side) {
-        const int s = s0 + sub;
-        const float x = __shfl(part_f, s & 63);
-        if (has && s < a.splits && x != 0.0f) o += *(const f32x4 *)(a.part + (s * all + rh) * a.d + e) * x;
+    // (read all the same, eight on their way together, and not used)
+    const float *part = a.part + rh * a.d + (has ? e : 0);
+    for (int s0 = 0; s0 < a.splits; s0 += 8 * side) {
+        f32x4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = *(const f32x4 *)(part + min(s0 + i * side + sub, a.splits - 1) * all * a.d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int s = s0 + i * side + sub;
+            const float x = __shfl(part_f, s & 63);
+            o += has && s < a.splits && x != 0.0f ? v[i] * x : (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        }
     }
     for (int s = 1; s < side; ++s)
 #pragma unroll

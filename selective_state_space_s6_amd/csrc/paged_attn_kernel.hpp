@@ -148,10 +148,9 @@ __device__ __forceinline__ int block_of(int worker, int side, int lg) {
 }
 
 template <int CT, int DP, bool EXACT, int W, bool SEL>      // EXACT: headdim == DP; W: waves of a block; SEL: chosen pages
-__global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_attn_kernel(Kp a) {
-    using T = Tile<CT, DP, W>;
+__device__ __forceinline__ void paged_attn_block(const Kp &a, int block, int all_blocks, float *lds) {
+    using T = Tile<CT, DP, W>;               // lds: q, and at a piece's end the waves' outputs
     constexpr int VD = T::VD, VB = T::VB;
-    extern __shared__ float lds[];          // q, and at a piece's end the waves' outputs
     u32x4 *q_lds = (u32x4 *)lds;
     __shared__ int scan[W], found[3];
     __shared__ float wave_m[W][kHeads], wave_l[W][kHeads];
@@ -160,7 +159,7 @@ __global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_att
 
     // ---- this block's piece [u, u_end) of the line of units, and the row that u is in
     const int per = (a.n_kv >> a.wh_lg) * a.passes;      // (kv heads side by side, pass) of a row
-    const int blk = worker_of(blockIdx.x, a.wh_lg), side = side_of(blockIdx.x, a.wh_lg);
+    const int blk = worker_of(block, a.wh_lg), side = side_of(block, a.wh_lg);
     int units = 0, u, u_end, row, row_u, row_len;
     if (a.whole) {                          // the units of its own row alone, from 0 on
         row = (int)((uint32_t)blk / (uint32_t)per);
@@ -189,18 +188,18 @@ __global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_att
         u = hp * units + (int)((int64_t)i * units / a.fixed);
         u_end = hp * units + (int)((int64_t)(i + 1) * units / a.fixed);
         if (u >= u_end) {                   // weighs nothing
-            if (tid < a.gmax) *(float2 *)(a.ml + ((int64_t)2 * blockIdx.x * a.gmax + tid) * 2) = make_float2(-INFINITY, 0.0f);
+            if (tid < a.gmax) *(float2 *)(a.ml + ((int64_t)2 * block * a.gmax + tid) * 2) = make_float2(-INFINITY, 0.0f);
             return;
         }
     } else if (a.batch <= 64) {                    // each wave for itself: row `lane`
         const int len = lane < a.batch ? a.lens[lane] : 0, own_units = span_of<SEL>(a, len).units * per;
         const int upto = wave_scan(own_units), before = upto - own_units;
         units = __builtin_amdgcn_readlane(upto, 63);
-        if (blockIdx.x == 0 && wave == 0) {
+        if (block == 0 && wave == 0) {
             if (lane < a.batch) a.start[lane] = before;
             if (lane == 0) a.start[a.batch] = units;
         }
-        const int blocks = min((int)gridDim.x >> a.wh_lg, units);
+        const int blocks = min(all_blocks >> a.wh_lg, units);
         if (blk >= blocks) return;
         u = (int)((int64_t)blk * units / blocks);
         u_end = (int)((int64_t)(blk + 1) * units / blocks);
@@ -220,19 +219,19 @@ __global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_att
             before += w < wave ? scan[w] : 0;
             units += scan[w];
         }
-        const int blocks = min((int)gridDim.x >> a.wh_lg, units);
-        if (blockIdx.x > 0 && blk >= blocks) return;
+        const int blocks = min(all_blocks >> a.wh_lg, units);
+        if (block > 0 && blk >= blocks) return;
         u = blocks ? (int)((int64_t)blk * units / blocks) : 0;
         u_end = blocks ? (int)((int64_t)(blk + 1) * units / blocks) : 0;
-        if (blockIdx.x == 0 || (u >= before && u < before + own_units)) {
+        if (block == 0 || (u >= before && u < before + own_units)) {
             for (int r = r0; r < r1; ++r) {
                 const int len = a.lens[r], n = span_of<SEL>(a, len).units * per;
                 if (u >= before && u < before + n) { found[0] = r; found[1] = before; found[2] = len; }
-                if (blockIdx.x == 0) a.start[r] = before;
+                if (block == 0) a.start[r] = before;
                 before += n;
             }
         }
-        if (blockIdx.x == 0 && tid == 0) a.start[a.batch] = units;
+        if (block == 0 && tid == 0) a.start[a.batch] = units;
         __syncthreads();
         if (u >= u_end) return;
         row = found[0];
@@ -478,7 +477,7 @@ __global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_att
         }
         __syncthreads();
         const bool whole = first == 0 && last == sp.units && !a.fixed;
-        const int slot = 2 * (int)blockIdx.x + (first == 0 && !a.fixed ? 1 : 0);
+        const int slot = 2 * block + (first == 0 && !a.fixed ? 1 : 0);
         const int d4 = a.d / 4;
         for (int i = tid; i < nh * d4; i += W * 64) {
             const int h = i / d4, e = (i - h * d4) * 4;
@@ -503,6 +502,12 @@ __global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_att
             }
         }
     }
+}
+
+template <int CT, int DP, bool EXACT, int W, bool SEL>
+__global__ void __launch_bounds__(W * 64, (Tile<CT, DP, W>::PER_SIMD)) paged_attn_kernel(Kp a) {
+    extern __shared__ float lds[];
+    paged_attn_block<CT, DP, EXACT, W, SEL>(a, blockIdx.x, gridDim.x, lds);
 }
 
 // Joins the pieces of a (row, query head): piece i's share is scaled by
@@ -614,8 +619,9 @@ int64_t align16(int64_t n) { return (n + 15) & ~int64_t(15); }
 // (row, kv head)s that occupy the chip with a wave each, by the waves that the work is cut for
 int64_t waves_of(int64_t d) { return (d <= 128 ? 2 : 1) * 4 * kCUs; }
 
-template <int CT, int DP, bool EXACT, int W, bool SEL>
-hipError_t go_w(Kp &k, int &grid, hipStream_t stream) {
+// how the work is cut for blocks of W waves; returns the shared memory of a block
+template <int CT, int DP, int W>
+size_t plan_w(Kp &k, int &grid) {
     using T = Tile<CT, DP, W>;
     k.unit = T::UNIT;
     k.unit_lg = __builtin_ctz(T::UNIT);
@@ -628,7 +634,11 @@ hipError_t go_w(Kp &k, int &grid, hipStream_t stream) {
     // heads of 128, bf16, 1000 tokens 10.2 us by lengths, 9.7 by sizes; 32000 34.1 and 33.6
     if (k.batch == 1 && !k.whole && grid >> k.wh_lg >= 2 * per) k.fixed = (grid >> k.wh_lg) / per;
     if (k.wh_lg > 0) grid = (grid + group - 1) / group * group;
-    const size_t lds = std::max((size_t)W * k.gmax * (DP + 4) * sizeof(float), T::QLDS ? (size_t)T::KC * T::QW * 1024 : 0);
+    return std::max((size_t)W * k.gmax * (DP + 4) * sizeof(float), T::QLDS ? (size_t)T::KC * T::QW * 1024 : 0);
+}
+template <int CT, int DP, bool EXACT, int W, bool SEL>
+hipError_t go_w(Kp &k, int &grid, hipStream_t stream) {
+    const size_t lds = plan_w<CT, DP, W>(k, grid);
     if (lds > 32 * 1024) {               // more than a block has unasked, from 64 KiB on
         const hipError_t e = hipFuncSetAttribute((const void *)paged_attn_kernel<CT, DP, EXACT, W, SEL>,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
@@ -650,15 +660,22 @@ hipError_t go_w(Kp &k, int &grid, hipStream_t stream) {
 // 12.1, 16.7 (one block of four a compute unit in bf16; in 8 bits two fit, and four waves still idle on rows of 3
 // tiles).  In pieces, four waves share the tokens of one, and fewer pieces are left to join; one row of 100000
 // tokens 32.8 us by waves, 23.1 by fours.  (Taken with weights in two bf16 parts; three are up to 3% slower either way.)
-template <int CT, int DP, bool EXACT, bool SEL>
-hipError_t go(Kp &k, int &grid, hipStream_t stream) {
+struct Form { bool whole, one_wave; };
+template <int CT, int DP>
+Form form_of(const Kp &k) {
     using T = Tile<CT, DP, 1>;
     const int64_t heads = (int64_t)k.batch * k.n_kv * k.passes, waves = waves_of(DP);
     const int tiles = ((k.window > 0 ? k.window : k.max_len) + T::NT - 1) / T::NT;
     const bool by_wave = tiles <= 1 || (heads > waves / 4 && tiles <= (heads >= waves ? 32 : heads >= waves / 2 ? 16 : 8));
     const bool by_block = tiles <= (heads >= waves / 4 ? 40 : heads >= waves / 8 ? 20 : 12);
-    k.whole = (by_wave || by_block) && heads < (1 << 22);      // (a grid's threads are counted in 32 bits)
-    return (k.whole ? by_wave : heads >= waves) ? go_w<CT, DP, EXACT, 1, SEL>(k, grid, stream) : go_w<CT, DP, EXACT, 4, SEL>(k, grid, stream);
+    const bool whole = (by_wave || by_block) && heads < (1 << 22);      // (a grid's threads are counted in 32 bits)
+    return {whole, whole ? by_wave : heads >= waves};
+}
+template <int CT, int DP, bool EXACT, bool SEL>
+hipError_t go(Kp &k, int &grid, hipStream_t stream) {
+    const Form f = form_of<CT, DP>(k);
+    k.whole = f.whole;
+    return f.one_wave ? go_w<CT, DP, EXACT, 1, SEL>(k, grid, stream) : go_w<CT, DP, EXACT, 4, SEL>(k, grid, stream);
 }
 template <int CT, int DP, bool SEL>
 hipError_t go_d(Kp &k, int &grid, hipStream_t stream) {
@@ -682,9 +699,8 @@ int64_t most_blocks(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t 
 // pages that a row of the work has at most
 inline int64_t rows_pages(const PagedAttnArgs &a) { return a.selected && a.top_k < a.max_pages ? a.top_k : a.max_pages; }
 
-template <bool SEL>
-hipError_t launch_form(const PagedAttnArgs &a, hipStream_t stream, const char **kernel_name) {
-    *kernel_name = "paged_attn_kernel";
+// what the kernels need of a call's arguments
+Kp kernel_args(const PagedAttnArgs &a) {
     const int e = a.kv_dtype == SSM_KV_F32 ? 4 : a.kv_dtype == SSM_KV_BF16 ? 2 : 1, qe = a.kv_dtype == SSM_KV_F32 ? 4 : 2;
     Kp k = {};
     k.q = (const char *)a.q; k.k = (const char *)a.k_cache; k.v = (const char *)a.v_cache;
@@ -706,11 +722,11 @@ hipError_t launch_form(const PagedAttnArgs &a, hipStream_t stream, const char **
     k.window = a.window > 0 && a.window < k.max_len ? (int)a.window : 0;
     k.scale2 = a.scale * (a.kv_dtype == SSM_KV_F8E4M3 ? a.k_scale : 1.0f) * kLog2e;
     k.v_scale = a.kv_dtype == SSM_KV_F8E4M3 ? a.v_scale : 1.0f;
-    int grid = 0;
-    const hipError_t rc = a.kv_dtype == SSM_KV_F32 ? go_type<KF32, SEL>(k, grid, stream)
-                        : a.kv_dtype == SSM_KV_BF16 ? go_type<KBF16, SEL>(k, grid, stream)
-                                                    : go_type<KF8, SEL>(k, grid, stream);
-    if (rc != hipSuccess || k.whole) return rc;
+    return k;
+}
+
+// joins what the blocks of `grid` left
+hipError_t launch_join(const PagedAttnArgs &a, const Kp &k, int grid, hipStream_t stream, const char **kernel_name) {
     *kernel_name = "paged_attn_join_kernel";
     // Where a head has many pieces, a block joins it, or several of 32 dims each; else its waves a head
     // each.  One row of 100000 tokens 22.7 us with, 46 without the split; 256 rows of up to 60
@@ -724,6 +740,17 @@ hipError_t launch_form(const PagedAttnArgs &a, hipStream_t stream, const char **
     else if (bf16) hipLaunchKernelGGL((paged_attn_join_kernel<true, 4>), g, dim3(kNT), 0, stream, k, grid);
     else hipLaunchKernelGGL((paged_attn_join_kernel<false, 4>), g, dim3(kNT), 0, stream, k, grid);
     return hipGetLastError();
+}
+
+template <bool SEL>
+hipError_t launch_form(const PagedAttnArgs &a, hipStream_t stream, const char **kernel_name) {
+    *kernel_name = "paged_attn_kernel";
+    Kp k = kernel_args(a);
+    int grid = 0;
+    const hipError_t rc = a.kv_dtype == SSM_KV_F32 ? go_type<KF32, SEL>(k, grid, stream)
+                        : a.kv_dtype == SSM_KV_BF16 ? go_type<KBF16, SEL>(k, grid, stream)
+                                                    : go_type<KF8, SEL>(k, grid, stream);
+    return rc != hipSuccess || k.whole ? rc : launch_join(a, k, grid, stream, kernel_name);
 }
 
 }  // namespace

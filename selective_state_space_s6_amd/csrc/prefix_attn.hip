@@ -1,17 +1,24 @@
 // prefix_attn.hip -- attention of one new token a row where rows share a long prefix
 // (ssm_prefix_attn_decode_fwd in include/ssm_longctx.h).
 //
-// Three steps: attention over each row's own tokens (paged_attn.hip, its output in fp32), attention of
-// all rows over the prefixes (prefix_attn_kernel), and the join of both by their maxima and sums.
+// One launch has the blocks of the prefixes and, behind them, those of the rows' own tokens (paged_attn_kernel.hpp's
+// work, its output in fp32 and normalised); another joins both by their maxima and sums, o = sum_i o_i 2^(m_i - m) / l.
+// Own tokens of a length that is cut into pieces are joined by a launch of their own before it.
 //
-// The prefix kernel has up to 64 (row, query head) pairs of a kv head in a block, as 16 NQ columns of the matrix
-// products, so a prefix's K and V are read from HBM once and by a block once for 64 columns; its 4 waves
-// walk tiles of tokens of their own and join at the end.  Operands go from global memory straight
-// into the matrix instructions' registers as in paged_attn_kernel.hpp (scores S^T = K Q^T, output O^T = V^T P^T,
-// V transposed by byte permutations, here once for all columns); q waits in shared memory.
-// A block's share is (16 NQ columns, kv head, one of `splits` parts of their rows' prefixes, end to end).  Blocks of the same part and
-// other columns run on one XCD at one time, so that all but the first of them find K and V in its L2.
-// Bound: for few columns HBM; from about 100 columns a kv head on the matrix cores and the exponentials beside them.
+// The (row, query head) pairs of a kv head are columns of the matrix products: scores S^T = K Q^T, output O^T = V^T P^T.
+// A block has the columns of some rows and one of `splits` parts of their prefixes, end to end, so a prefix is read from
+// HBM once and by a block once for all its columns.  Blocks of the same part and other columns run on one XCD at one
+// time, so that all but the first of them find K and V in its L2.  Two forms:
+//   few: up to 32 columns; the 4 waves walk tiles of tokens of their own, K and V straight from global memory into the
+//     matrix instructions' registers (V transposed by byte permutations), and join at the end.
+//   many: 4 waves of 16 or 32 columns each; K and V come through shared memory once for all, the next tile's while
+//     one is worked on.
+//
+// Figures (us): 64 rows of 32 + 8 heads of 128, bf16, behind 16384 tokens, 512 own, 71: 61 for both kinds of blocks and 9 for
+// the join.  Its 134 MB would take 26; the prefix' part is bound by the exponentials and the matrix cores at
+// the clock that both together leave (1.7 GHz, matrix cores 47% busy, the vector pipe most of the rest).  13 rows of
+// 20 + 4 heads, 8 bits, behind three prompts of 4001 15.7, and 2 rows behind 8192 tokens 15.2: the way through a block
+// (its prefixes, pages, first loads; then the parts) and the second launch.
 //
 // The running maximum is raised only where a score exceeds it by more than 2^8 in its weight: weights up
 // to 2^8 lose nothing in fp32, and the outputs are not rescaled for every new maximum.  Weights enter their
@@ -21,15 +28,12 @@
 #include <stdint.h>
 #include <algorithm>
 
-#include "attn_device.hpp"
-#include "attn_launchers.hpp"
-#include "device_common.hpp"
+#include "paged_attn_kernel.hpp"
 
 namespace ssm {
 namespace {
 
-constexpr int kW = 4, kNT = kW * 64;
-constexpr int kCUs = 256;
+constexpr int kW = 4;               // waves of a block (of kNT threads)
 constexpr float kSlack = 8.0f;      // log2 of what a weight may exceed 1 by
 
 struct Pp {
@@ -58,8 +62,8 @@ template <int CT, int DP> struct PTile {
 
 // A block's place in the work: 16-column groups are (row, head) pairs of one kv head
 struct Place { int split, tile, kv, row0, nrows, nh, h0; };
-__device__ __forceinline__ bool place_of(const Pp &a, Place &p) {
-    const int j = blockIdx.x >> 3, combo = j / a.tiles * 8 + (blockIdx.x & 7);
+__device__ __forceinline__ bool place_of(const Pp &a, int block, Place &p) {
+    const int j = block >> 3, combo = j / a.tiles * 8 + (block & 7);
     if (combo >= a.combos) return false;
     p.tile = j % a.tiles;
     p.split = combo % a.splits;
@@ -95,15 +99,14 @@ __device__ __forceinline__ Line line_of(const Pp &a, const Place &p, int lane, i
 }
 
 template <int CT, int DP, bool EXACT, int NQ>
-__global__ void __launch_bounds__(kNT, DP * NQ <= 256 ? 2 : 1) prefix_few_kernel(Pp a) {
+__device__ __forceinline__ void prefix_few_block(const Pp &a, int block, float *lds) {
     using T = PTile<CT, DP>;
     constexpr int VD = T::VD, VB = T::VB, PITCH = DP + 4;
-    extern __shared__ float lds[];          // q, and at the end the waves' outputs, 16 columns at a time
-    u32x4 *q_lds = (u32x4 *)lds;
+    u32x4 *q_lds = (u32x4 *)lds;            // q, and at the end the waves' outputs, 16 columns at a time
     __shared__ float wave_m[kW][16 * NQ], wave_l[kW][16 * NQ];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
     Place at;
-    if (!place_of(a, at)) return;
+    if (!place_of(a, block, at)) return;
     const int split = at.split, kv = at.kv, row0 = at.row0, nrows = at.nrows, nh = at.nh, h0 = at.h0;
     const PageSize ps(a.page_size);
 
@@ -459,13 +462,12 @@ __device__ __forceinline__ float minus(uint32_t ph, uint32_t which, float x) {
 }
 
 template <int CT, int DP, bool EXACT, int NQ>
-__global__ void __launch_bounds__(kNT, 2) prefix_many_kernel(Pp a) {
-    using T = FTile<CT, DP>;
+__device__ __forceinline__ void prefix_many_block(const Pp &a, int block, u32x4 *bufs) {
+    using T = FTile<CT, DP>;                 // bufs: two of: K's operands, V's operands
     constexpr int VD = T::VD, VB = T::VB;
-    extern __shared__ u32x4 bufs[];          // two of: K's operands, V's operands
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
     Place at;
-    if (!place_of(a, at)) return;
+    if (!place_of(a, block, at)) return;
     const PageSize ps(a.page_size);
     Line line = line_of(a, at, lane, T::NT);
 
@@ -786,6 +788,20 @@ __global__ void __launch_bounds__(kNT, 2) prefix_many_kernel(Pp a) {
     }
 }
 
+// The prefixes' blocks, and behind them those of the rows' own tokens (o: paged_attn_kernel.hpp's work).  Behind, since a prefix'
+// block takes longer and own ones fill what is left: 64 rows behind 16384 tokens 69 us, 74 in launches of their own, 90 with
+// 8 blocks of one kind and 8 of the other in turn; 13 rows of three prompts 24.8, 30.7 in launches of their own.
+template <int CT, int DP, bool EXACT, int NQ, bool MANY>
+__global__ void __launch_bounds__(kNT, MANY || DP * NQ <= 256 ? 2 : 1) prefix_attn_kernel(Pp a, Kp o, int prefix_blocks, int own_blocks) {
+    extern __shared__ u32x4 lds[];
+    if ((int)blockIdx.x < prefix_blocks) {
+        if constexpr (MANY) prefix_many_block<CT, DP, EXACT, NQ>(a, blockIdx.x, lds);
+        else prefix_few_block<CT, DP, EXACT, NQ>(a, blockIdx.x, (float *)lds);
+    } else {
+        paged_attn_block<CT, DP, EXACT, kW, false>(o, blockIdx.x - prefix_blocks, own_blocks, (float *)lds);
+    }
+}
+
 // Joins the parts of a (row, query head), a wave each; the row's own tokens are one more part, already
 // normalised.  Lane i forms the weight of part i; then 64 / (d / 4) parts at a time are added up, 4 dims a lane.
 template <bool BF16>
@@ -839,57 +855,89 @@ __global__ void __launch_bounds__(kNT) prefix_join_kernel(Pp a) {
 }
 
 // ------------------------------------------------------------------ host ----
-int64_t align16(int64_t n) { return (n + 15) & ~int64_t(15); }
-
-// How the columns of all rows are cut into blocks
+// How the columns of all rows are cut into blocks.  us, all rows behind one prefix, 100 tokens of their own
+// (few of 16 columns, few of 32, many of 64, many of 128; for d = 256 the last is not built):
+//   heads of 128, bf16, 8 kv heads, 16384 tokens:  16 columns 25.4, 26.1, 26.0, 30.2;  40: 29.8, 27.6, 29.1, 34.1;
+//     128: 53, 38, 38, 46;  256: 89, 57, 55, 57;  384: 153, 78, 70, 71;  1024: 311, 178, 157, 145
+//   of 128, 8 bits, 4 kv heads, 16384 tokens:  256: 38, 33, 42, 42;  512: 64, 50, 60, 53;  1024: 111, 82, 97, 80
+//   of 64, bf16, 4 kv heads, 16384 tokens:  256: 35, 27, 30, 33;  512: 58, 40, 42, 41;  1024: 106, 66, 67, 61
+//   of 128, fp32, 4 kv heads, 4000 tokens:  16: 13.8, 16.3, 20.3, 30.2;  128: 30.5, 33.2, 29.4, 38.8;  1024: 118, 109, 109, 113
+//   of 256, bf16, 4 kv heads, 4000 tokens:  16: 18.0, 17.5, 19.1;  32: 22.6, 19.3, 21.4;  64: 32, 27.5, 25.5;  1024: 115, 89, 81
+// So 32 columns to a block, 16 if there are no more; up to 128 dims many of 128 from 2^25 scores on, where K and V out of
+// the L2s cost more than the way through shared memory; above 128 dims, where a wave of 32 columns keeps one block a
+// compute unit, many of 64 from 33 columns on.
+//
+// Two blocks a compute unit from 2^24 scores on, one below, where the own tokens' blocks then run beside them and there are
+// fewer parts to join (two, one): 48 columns of the 8-bit heads above 24.2, 18.3;  160 of them 35.5, 29.1;
+// 256 33.3, 36.7;  512 50.4, 61;  256 of 4 kv heads of 128, 8 bits, 4000 tokens 23.1, 17.7;  1024 of these 40.7, 37.1.
 struct Cut { int nq, gm, passes, rows, tiles, splits; bool many; };
 Cut cut_of(int64_t batch, int64_t n_heads, int64_t n_kv, int64_t d, int64_t max_len, int64_t n_prefixes) {
     Cut c;
     const int64_t group = n_heads / n_kv, all = batch * group;
-    c.many = all > 32;
-    c.nq = !c.many ? (all > 16 ? 2 : 1) : all > 64 && d <= 128 ? 2 : 1;
+    const double scores = (double)n_kv * all * max_len;       // of all rows with one prefix
+    c.many = d > 128 ? all > 32 : all > 64 && scores >= 1 << 25;
+    c.nq = d > 128 && c.many ? 1 : all > 16 ? 2 : 1;
     const int64_t cols = 16 * c.nq * (c.many ? kW : 1);
     c.gm = (int)std::min<int64_t>(group, cols);
     c.passes = (int)((group + c.gm - 1) / c.gm);
     c.rows = (int)std::min<int64_t>(std::min<int64_t>(batch, cols / c.gm), 64);
     c.tiles = (int)((batch + c.rows - 1) / c.rows);
-    // two blocks a compute unit, of at least some 128 tokens
-    const int64_t heads = c.tiles * n_kv * c.passes;
+    // the same number of blocks on each XCD, of at least some 128 tokens (2 rows of 4 kv heads of 128, 8 bits, behind 4000:
+    // of 64 14.6 us, 128 11.8, 256 11.1, 512 13.0; bf16 of 64 11.9, 10.0, 10.7, 12.7)
     const int64_t units = std::max<int64_t>(1, (max_len + 127) / 128 * std::min<int64_t>(n_prefixes, c.rows));
-    c.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(2 * kCUs / heads, units), 64));
+    const int64_t each = kCUs / 8 * (scores >= 1 << 24 ? 2 : 1) / c.tiles;
+    c.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(8 * each / (n_kv * c.passes), units), 64));
     return c;
 }
 
-template <typename F>
-hipError_t launch_with(F kernel, size_t lds, const Pp &k, hipStream_t stream) {
+int blocks_of(const Pp &k) { return (k.combos + 7) / 8 * 8 * k.tiles; }
+
+template <typename F, typename... A>
+hipError_t launch_with(F kernel, size_t lds, int grid, hipStream_t stream, A... args) {
     if (lds > 32 * 1024) {               // more than a block has unasked, from 64 KiB on
         const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess) return e;
     }
-    const unsigned grid = (unsigned)((k.combos + 7) / 8 * 8 * k.tiles);
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kNT), lds, stream, k);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kNT), lds, stream, args...);
     return hipGetLastError();
 }
-template <int CT, int DP, bool EXACT, int NQ>
-hipError_t go_q(const Pp &k, bool many, hipStream_t stream) {
+
+// A call: `own` the rows' own tokens, whose output goes to the workspace.
+struct Call { const PagedAttnArgs &own; const Cut &cut; hipStream_t stream; const char **kernel_name; };
+
+template <int CT, int DP, bool EXACT, int NQ, bool MANY>
+hipError_t go_m(const Pp &k, const Call &c) {
     using T = PTile<CT, DP>;
-    if constexpr (DP <= 128 || NQ == 1) {
-        if (many) return launch_with(prefix_many_kernel<CT, DP, EXACT, NQ>, 2 * FTile<CT, DP>::BUF * 16, k, stream);
+    const size_t lds = MANY ? 2 * FTile<CT, DP>::BUF * 16
+                            : std::max((size_t)kW * 16 * NQ * (DP + 4) * sizeof(float), (size_t)T::KC * T::QW * NQ * 1024);
+    Kp o = kernel_args(c.own);
+    o.whole = form_of<CT, DP>(o).whole;
+    int own_blocks = 0;
+    const int blocks = blocks_of(k);
+    const size_t own_lds = plan_w<CT, DP, kW>(o, own_blocks);
+    *c.kernel_name = "prefix_attn_kernel";
+    const hipError_t e = launch_with(prefix_attn_kernel<CT, DP, EXACT, NQ, MANY>, std::max(lds, own_lds), blocks + own_blocks, c.stream,
+                                     k, o, blocks, own_blocks);
+    return e != hipSuccess || o.whole ? e : launch_join(c.own, o, own_blocks, c.stream, c.kernel_name);
+}
+template <int CT, int DP, bool EXACT, int NQ>
+hipError_t go_q(const Pp &k, const Call &c) {
+    if constexpr (NQ == (DP <= 128 ? 2 : 1)) {
+        if (c.cut.many) return go_m<CT, DP, EXACT, NQ, true>(k, c);
     }
-    const size_t lds = std::max((size_t)kW * 16 * NQ * (DP + 4) * sizeof(float), (size_t)T::KC * T::QW * NQ * 1024);
-    return launch_with(prefix_few_kernel<CT, DP, EXACT, NQ>, lds, k, stream);
+    return go_m<CT, DP, EXACT, NQ, false>(k, c);
 }
 template <int CT, int DP>
-hipError_t go_d(const Pp &k, const Cut &c, hipStream_t stream) {
-    if (k.d == DP) return c.nq == 2 ? go_q<CT, DP, true, 2>(k, c.many, stream) : go_q<CT, DP, true, 1>(k, c.many, stream);
-    return c.nq == 2 ? go_q<CT, DP, false, 2>(k, c.many, stream) : go_q<CT, DP, false, 1>(k, c.many, stream);
+hipError_t go_d(const Pp &k, const Call &c) {
+    if (k.d == DP) return c.cut.nq == 2 ? go_q<CT, DP, true, 2>(k, c) : go_q<CT, DP, true, 1>(k, c);
+    return c.cut.nq == 2 ? go_q<CT, DP, false, 2>(k, c) : go_q<CT, DP, false, 1>(k, c);
 }
 template <int CT>
-hipError_t go_type(const Pp &k, const Cut &c, hipStream_t stream) {
-    if (k.d <= 64) return go_d<CT, 64>(k, c, stream);
-    if (k.d <= 128) return go_d<CT, 128>(k, c, stream);
-    if (k.d <= 192) return go_d<CT, 192>(k, c, stream);
-    return go_d<CT, 256>(k, c, stream);
+hipError_t go_type(const Pp &k, const Call &c) {
+    if (k.d <= 64) return go_d<CT, 64>(k, c);
+    if (k.d <= 128) return go_d<CT, 128>(k, c);
+    if (k.d <= 192) return go_d<CT, 192>(k, c);
+    return go_d<CT, 256>(k, c);
 }
 
 }  // namespace
@@ -926,11 +974,9 @@ hipError_t launch_prefix_attn(const PrefixAttnArgs &p, hipStream_t stream, const
     k.v_scale = a.kv_dtype == SSM_KV_F8E4M3 ? a.v_scale : 1.0f;
 
     a.o = (void *)k.o_own; a.lse = (float *)k.lse_own; a.o_f32 = true;
-    hipError_t rc = launch_paged_attn(a, stream, kernel_name);
-    if (rc != hipSuccess) return rc;
-    *kernel_name = c.many ? "prefix_many_kernel" : "prefix_few_kernel";
-    rc = a.kv_dtype == SSM_KV_F32 ? go_type<KF32>(k, c, stream)
-       : a.kv_dtype == SSM_KV_BF16 ? go_type<KBF16>(k, c, stream) : go_type<KF8>(k, c, stream);
+    const Call call{a, c, stream, kernel_name};
+    const hipError_t rc = a.kv_dtype == SSM_KV_F32 ? go_type<KF32>(k, call)
+                        : a.kv_dtype == SSM_KV_BF16 ? go_type<KBF16>(k, call) : go_type<KF8>(k, call);
     if (rc != hipSuccess) return rc;
     *kernel_name = "prefix_join_kernel";
     const dim3 grid((unsigned)((rh + kW - 1) / kW));

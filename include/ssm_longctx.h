@@ -39,9 +39,9 @@ extern "C" {
  * as in ssm_paged_attn_decode_fwd, also for a row that has no token at all
  * (o = 0, lse = -inf).
  *
- * A prefix's keys and values are read once for up to 64 query heads of rows
- * that stand next to each other: rows of one prefix cost least side by side,
- * and any order is right.
+ * A prefix's keys and values are read once for 16 to 128 (row, query head)
+ * pairs of a kv head whose rows stand next to each other: rows of one prefix cost
+ * least side by side, and any order is right.
  * Arithmetic: as ssm_paged_attn_decode_fwd, except that the softmax weights of
  * a prefix's tokens enter their product with v as two bf16 values (17 bits, an
  * error below 2^-17 of each weight) where v is bf16 or 8-bit.

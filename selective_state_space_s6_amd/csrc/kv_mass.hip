@@ -2,11 +2,15 @@
 // (ssm_kv_mass_update in include/ssm_longctx.h).
 //
 // w_j = sum over rows and heads of 2^(log2(e) (scale q . k_j - lse)): given lse, no maximum and no second pass.
-// A wave has 16 to 64 tokens of a (request, kv head), their keys in registers for as long as it takes to walk
-// the request's (row, head) pairs, 16 at a time, as columns of the matrix products; a lane adds up its
-// column's exponentials, and the 16 lanes of a token are joined once at the end.  No two waves add to one token.
-// Bound: for one row a request HBM, the keys; for prompts the exponentials, one a
-// (row, head, token), with 2 headdim operations on the matrix cores beside each.
+// (row, head) pairs are columns of the matrix products, 16 tokens or more their rows; a lane adds up its columns'
+// exponentials, and the 16 lanes of a token are joined once at the end.  Two forms, and in both one writer a token:
+//   step: a wave has tiles of 16 to 64 tokens from one line of all requests' tiles, cut into equal pieces, the next
+//     tile's keys on their way while one is worked on, and walks the request's columns, 16 at a time.
+//     Bound: HBM, the keys.  64 requests of up to 8192 tokens, 8 kv heads of 128, bf16: 173 us for 819 MB, 4.7 TB/s.
+//   prompt: a block has 64 tokens, their keys in shared memory, and its 8 waves columns of their own from the first row on
+//     that sees the tile; requests go to XCDs in turn.  Bound: the way of q from the L2s, 64 bytes of each of 16 columns a load,
+//     beside one exponential a (row, head, token).  4 prompts of up to 2048 tokens, 32 + 8 heads of 128, bf16: 51 us,
+//     13.9 GFLOP and 54 million exponentials.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <algorithm>
@@ -461,7 +465,14 @@ hipError_t launch_kv_mass(const KvMassArgs &a, hipStream_t stream, const char **
     k.n_tokens = (int)a.n_tokens; k.n_heads = (int)a.n_heads; k.n_kv = (int)a.n_kv_heads; k.group = (int)(a.n_heads / a.n_kv_heads);
     k.d = a.headdim; k.n_pages = (int)a.n_pages; k.page_size = (int)a.page_size; k.row_len = (int)(a.max_pages * a.page_size);
     k.scale2 = a.scale * (a.kv_dtype == SSM_KV_F8E4M3 ? a.k_scale : 1.0f) * kLog2e;
-    const bool prompt = a.n_tokens * k.group >= 128 * a.batch;     // 8 times 16 columns a request and more
+    // by columns a request on average (rows of q that each tile of tokens meets), and from half as many on where a block a
+    // tile is resident at once and the step's form would leave the chip idle.  us (step, prompt):
+    //   16 requests of 2000 tokens, 4 kv heads of 128, bf16:  16 columns 10.8, 31.7;  61: 21.7, 33.8;  123: 39.0, 38.3;  248: 70, 50
+    //   2 of 4000, 4 of 128, fp32:  20: 9.8, 29.4;  80: 20.0, 32.1;  160: 33.7, 37.5
+    //   4 of 1000, 4 of 64, 8 bits:  43: 9.2, 5.9;  86: 13.1, 6.6;  172: 20.9, 7.7
+    //   8 of 2000, 1 of 256, bf16:  35: 8.8, 11.7;  75: 14.8, 12.7;  155: 26.6, 19.4
+    const bool idle = k.row_len <= 64 * (2 * kCUs / (a.batch * a.n_kv_heads)) && a.kv_dtype != SSM_KV_F32;
+    const bool prompt = a.n_tokens * k.group >= (idle ? 64 : 128) * a.batch;
     k.batch = (int)a.batch;
     *kernel_name = prompt ? "kv_mass_prompt_kernel" : "kv_mass_step_kernel";
     return a.kv_dtype == SSM_KV_F32 ? go<KF32>(k, prompt, stream) : a.kv_dtype == SSM_KV_BF16 ? go<KBF16>(k, prompt, stream)

@@ -2,12 +2,14 @@
 // that a page's keys can have with the row's queries (ssm_kv_page_select_fwd in include/ssm_longctx.h).
 //
 // Two launches: the scores of every page as 32-bit keys into the workspace, and the choice, a block for
-// each (row, kv head).  Bound: HBM by the bounds, 2 headdim values a page and kv head, read once for
-// up to 8 query heads; next to it the products in 64 bits, 2 headdim multiply-adds a page and query head at half
-// the 32-bit rate.  64 bits because the result is an order: sums in 32 bits would differ with the order of
+// each (row, kv head).  Products in 64 bits because the result is an order: sums in 32 bits would differ with the order of
 // their terms in the last places, and with them which of two close pages is taken.
-// Four lanes have a page, 16 bytes of its bounds each; max(q, 0) and min(q, 0) wait in shared memory
-// in 64 bits and are read once for the two pages of a lane.
+// Four lanes have a page, 16 bytes of its bounds each, read once for up to 8 query heads; max(q, 0) and min(q, 0) wait in shared
+// memory in 64 bits and are read once for the two pages of a lane (for four 46 us, more registers than two blocks
+// leave; q in registers and exchanged between lanes 42 to 65; two 37).
+// Bound: the shared memory's reads of q, 16 bytes a dim and head, beside 2 headdim multiply-adds in 64 bits; HBM would take
+// 25.  32 rows of up to 2048 pages, 32 + 8 heads of 128, bf16 (127 MB): 37 us, and 7.6 for the choice, 12 passes or so over keys
+// in shared memory.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <algorithm>
@@ -21,7 +23,7 @@ namespace {
 constexpr int kNT = 256;            // threads of a scoring block
 constexpr int kPages = 2;           // pages of a lane
 constexpr int kStep = kNT / 4 * kPages;      // pages of a block
-constexpr int kBlocks = 2048;       // scoring blocks: twice what is resident at once, since rows' lengths differ
+constexpr int kBlocks = 2048;       // scoring blocks: twice what is resident at once, since rows' lengths differ (37 us above; 41 with half)
 constexpr int kKept = 8192;         // keys that the choice keeps in shared memory
 
 template <int CT> struct Wide {

@@ -47,7 +47,10 @@ template <int CT, int DP> struct MTile {
     static constexpr int OCC = HELD <= 112 ? 3 : HELD <= 192 ? 2 : 1;    // waves on a SIMD
     // a prompt's tile, in shared memory, and 16-column groups of a wave in a round
     static constexpr int PSUB = 4, PNT = 64;
-    static constexpr int NC = QR <= 32 ? 2 : 1;
+    // (two where both fit the registers: of heads of 128 in fp32 and of 256 in bf16 two spilled, 73 us instead of 60 and 229
+    // instead of 128; tiles of 128 tokens 66 us for 4 prompts of up to 2048 tokens, 56 with 64, and blocks of 16 columns a wave
+    // two a compute unit 86)
+    static constexpr int NC = QR <= 24 ? 2 : 1;
 };
 
 // A lane's token of a tile
@@ -465,14 +468,15 @@ hipError_t launch_kv_mass(const KvMassArgs &a, hipStream_t stream, const char **
     k.n_tokens = (int)a.n_tokens; k.n_heads = (int)a.n_heads; k.n_kv = (int)a.n_kv_heads; k.group = (int)(a.n_heads / a.n_kv_heads);
     k.d = a.headdim; k.n_pages = (int)a.n_pages; k.page_size = (int)a.page_size; k.row_len = (int)(a.max_pages * a.page_size);
     k.scale2 = a.scale * (a.kv_dtype == SSM_KV_F8E4M3 ? a.k_scale : 1.0f) * kLog2e;
-    // by columns a request on average (rows of q that each tile of tokens meets), and from half as many on where a block a
+    // by columns a request on average (rows of q that each tile of tokens meets), and from a quarter as many on where a block a
     // tile is resident at once and the step's form would leave the chip idle.  us (step, prompt):
-    //   16 requests of 2000 tokens, 4 kv heads of 128, bf16:  16 columns 10.8, 31.7;  61: 21.7, 33.8;  123: 39.0, 38.3;  248: 70, 50
-    //   2 of 4000, 4 of 128, fp32:  20: 9.8, 29.4;  80: 20.0, 32.1;  160: 33.7, 37.5
-    //   4 of 1000, 4 of 64, 8 bits:  43: 9.2, 5.9;  86: 13.1, 6.6;  172: 20.9, 7.7
-    //   8 of 2000, 1 of 256, bf16:  35: 8.8, 11.7;  75: 14.8, 12.7;  155: 26.6, 19.4
-    const bool idle = k.row_len <= 64 * (2 * kCUs / (a.batch * a.n_kv_heads)) && a.kv_dtype != SSM_KV_F32;
-    const bool prompt = a.n_tokens * k.group >= (idle ? 64 : 128) * a.batch;
+    //   16 requests of 2000 tokens, 4 kv heads of 128, bf16:  16 columns 10.9, 32.0;  61: 22.1, 34.3;  123: 39.5, 38.5;  248: 70, 50
+    //   16 of 4000, 4 of 128, fp32:  122: 235, 138;   32 of 2000, 4 of 256, bf16:  38: 78, 75
+    //   2 of 4000, 4 of 128, fp32:  20: 9.5, 13.4;  80: 20.0, 16.7;  160: 33.4, 23.0
+    //   4 of 1000, 4 of 64, 8 bits:  43: 9.2, 5.9;  86: 13.0, 6.6;  172: 20.9, 7.7
+    //   8 of 2000, 1 of 256, bf16:  35: 8.9, 6.9;  75: 14.8, 7.9;  155: 26.3, 11.0
+    const bool idle = k.row_len <= 64 * (2 * kCUs / (a.batch * a.n_kv_heads));
+    const bool prompt = a.n_tokens * k.group >= (idle ? 32 : 128) * a.batch;
     k.batch = (int)a.batch;
     *kernel_name = prompt ? "kv_mass_prompt_kernel" : "kv_mass_step_kernel";
     return a.kv_dtype == SSM_KV_F32 ? go<KF32>(k, prompt, stream) : a.kv_dtype == SSM_KV_BF16 ? go<KBF16>(k, prompt, stream)

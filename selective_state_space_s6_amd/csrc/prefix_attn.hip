@@ -15,8 +15,8 @@
 //     one is worked on.
 //
 // Figures (us): 64 rows of 32 + 8 heads of 128, bf16, behind 16384 tokens, 512 own, 71: 61 for both kinds of blocks and 9 for
-// the join.  Its 134 MB would take 26; the prefix' part is bound by the exponentials and the matrix cores at
-// the clock that both together leave (1.7 GHz, matrix cores 47% busy, the vector pipe most of the rest).  13 rows of
+// the join.  Its 134 MB would take 26; the prefix' part is bound by matrix and vector instructions (17 and 20 to 25
+// us of issue at the 1.7 GHz that both together leave) that two waves on a SIMD overlap in part.  13 rows of
 // 20 + 4 heads, 8 bits, behind three prompts of 4001 15.7, and 2 rows behind 8192 tokens 15.2: the way through a block
 // (its prefixes, pages, first loads; then the parts) and the second launch.
 //

@@ -77,7 +77,7 @@ int ssm_prefix_attn_decode_fwd(const void *q, const void *k_cache, const void *v
  * forms them anew, after an eviction for instance.)
  * Layouts: k_cache as above; bounds (n_pages, n_kv_heads, 2, headdim) [kv_dtype]
  * contiguous, updated in place; block_table, len_old, lens (batch) int32.  A page
- * that new tokens stand on belongs to one request.
+ * that new tokens stand on belongs to one request, and stands once in its table.
  * Limits: batch <= SSM_KV_MAX_BATCH; headdim and the cache's strides as in
  * ssm_paged_attn_decode_fwd; bounds 16-byte aligned.  No workspace. */
 int ssm_kv_page_bounds_update(const void *k_cache, void *bounds, const int32_t *block_table,
@@ -156,7 +156,8 @@ int ssm_select_attn_decode_fwd(const void *q, const void *k_cache, const void *v
  * Layouts: q (n_tokens, n_heads, headdim) [dtype] strided; lse (n_tokens, n_heads)
  * fp32; mass (n_pages, n_kv_heads, page_size) fp32 contiguous, updated in place;
  * starts (batch + 1), positions (n_tokens), len_old, lens (batch) int32.  starts
- * outside [0, n_tokens] are cut to it.  A page belongs to one request here.
+ * outside [0, n_tokens] are cut to it.  A page belongs to one request here, and
+ * stands once in its table.
  * Limits: batch <= SSM_KV_MAX_BATCH; those of ssm_paged_attn_decode_fwd, and n_pages *
  * n_kv_heads * page_size below 2^31.  n_tokens may be 0 (q, lse and positions may then be NULL).  No
  * workspace. */
@@ -184,7 +185,8 @@ int ssm_kv_mass_update(const void *q, const void *k_cache, const float *lse, flo
  * A token whose old or new place is on a page outside [0, n_pages) is not moved.
  * Layouts: k_cache, v_cache as above, mass (n_pages, n_kv_heads, page_size) fp32
  * contiguous, all updated in place; block_table, lens; len_out (batch), kept
- * (batch, n_kv_heads, budget) int32.  A page belongs to one request here.
+ * (batch, n_kv_heads, budget) int32.  A page belongs to one request here, and
+ * stands once in its table.
  * Limits: 1 <= budget <= 2^30, 0 <= recent <= budget; batch * n_kv_heads * budget and
  * n_pages * n_kv_heads * page_size below 2^31; headdim and strides as in
  * ssm_paged_attn_decode_fwd, and different rows of a cache in different places.  No

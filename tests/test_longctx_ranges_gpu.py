@@ -57,6 +57,32 @@ def test_infinite_and_nan_keys_of_many_rows(cuda_device):
         assert (o[50:100:2] == 0).all() and np.isneginf(lse[50:100:2]).all() and np.isfinite(lse[:50]).all()
 
 
+def test_bad_pages_and_long_lengths_of_many_rows(cuda_device):
+    """Pages outside the cache hold no token, lengths end with their table, tables and q are strided, and the workspace holds
+    NaN before."""
+    import torch
+    m = lib()
+    for cache, d in (("bf16", 128), ("f8", 64), ("f32", 64)):
+        s = _wide(Shared(cuda_device, 122, [200, 90], [i % 2 for i in range(90)], [i % 70 for i in range(90)], 8, 2, d, cache, 16))
+        s.ptable[0, 3], s.ptable[0, 5], s.ptable[1, 0], s.own[1, 0] = -1, s.pages, 1 << 30, -7
+        s.ptable[0, 12] = -(1 << 31)
+        s.plens = np.array([1 << 30, 90])                     # every place of the table, most of them without a page
+        s.rows = s.rows.copy()
+        s.rows[5], s.rows[6] = -1, 1 << 30
+        s.k, s.v = (torch.nan_to_num(c.float(), nan=0.5).to(c.dtype) for c in (s.k, s.v))
+        proj = torch.randn((90, 8 * d + 64), device=cuda_device).to(s.q.dtype)
+        s.q = proj[:, 64:].unflatten(1, (8, d))
+        big = torch.full((90, s.own.shape[1] + 4), -1, dtype=torch.int32, device=cuda_device)
+        big[:, :s.own.shape[1]] = s.t(s.own)
+        pbig = torch.full((2, s.ptable.shape[1] + 3), 5, dtype=torch.int32, device=cuda_device)
+        pbig[:, :s.ptable.shape[1]] = s.t(s.ptable)
+        ws = torch.full((m.ssm_prefix_attn_decode_fwd_workspace_size(90, 8, 2, d, s.ptable.shape[1], s.own.shape[1], 16),), 255,
+                        dtype=torch.uint8, device=cuda_device)
+        got = m.ssm_prefix_attn_decode_fwd(s.q, s.k, s.v, s.t(s.prefix), pbig[:, :s.ptable.shape[1]], s.t(s.plens), big[:, :s.own.shape[1]],
+                                           s.t(s.rows), scale=s.sc, k_scale=s.scale, v_scale=s.scale, return_lse=True, workspace=ws)
+        s.check("bad pages of many rows " + cache, got)
+
+
 def test_many_rows_in_a_graph(cuda_device):
     """Captured once, two graphs with one workspace; everything changes in place between replays, with eager calls between."""
     import torch

@@ -174,7 +174,7 @@ def test_the_same_as_pages_in_the_rows_own_tables(cuda_device):
     joined = np.concatenate([np.repeat(s.ptable[:, :20], 9, 0), s.own], 1)
     b = m.ssm_paged_attn_decode_fwd(s.q, s.k, s.v, s.t(joined), s.t(s.rows + 320), scale=s.sc, return_lse=True)
     # each is within half of a bf16 step and its weights' error of the exact value
-    assert ((n64(a[0]) - n64(b[0])) <= 2.0 ** -7 * np.abs(n64(b[0])) + 1e-4).all()
+    assert (np.abs(n64(a[0]) - n64(b[0])) <= 2.0 ** -7 * np.abs(n64(b[0])) + 1e-4).all()
     assert np.abs(n64(a[1]) - n64(b[1])).max() <= 1e-4
 
 

@@ -44,7 +44,9 @@ template <int CT, int DP> struct MTile {
     static constexpr int SUB = KC <= 2 ? 4 : KC <= 4 ? 2 : 1;
     static constexpr int NT = SUB * 16;
     static constexpr int HELD = KC * SUB * 8 + QR * 2;               // registers of two tiles' keys and columns
-    static constexpr int OCC = HELD <= 112 ? 3 : HELD <= 192 ? 2 : 1;    // waves on a SIMD
+    // waves on a SIMD (8-bit keys widen in registers of their own: on three, heads of 128 spilled, 207 us for 64 requests of up
+    // to 8192 tokens, 99 on two; 108 on three with tiles of 32 tokens)
+    static constexpr int OCC = HELD <= (CT == KF8 ? 64 : 112) ? 3 : HELD <= 192 ? 2 : 1;
     // a prompt's tile, in shared memory, and 16-column groups of a wave in a round
     static constexpr int PSUB = 4, PNT = 64;
     // (two where both fit the registers: of heads of 128 in fp32 and of 256 in bf16 two spilled, 73 us instead of 60 and 229

@@ -9,8 +9,8 @@
 // rows are cut along headdim, which are moves of their own, as are k, v and mass.
 //
 // Bound: HBM, the moved rows read and written.  64 requests of 8 kv heads of 128, bf16, 4160 tokens cut to 4096 of random
-// mass: 532 us, 15 of them the choice, for 2.1 GB (418 us at the rate of a large copy); 91 where the evicted ones
-// are the newest that may go.  One request of 30000 tokens cut to 29000: 163, of one kv head of 64, by the chain of its runs.
+// mass: 495 us, 15 of them the choice, for 2.1 GB (418 us at the rate of a large copy); 91 where the evicted ones
+// are the newest that may go.  One request of 30000 tokens cut to 29000: 113, of one kv head of 64, by the chain of its runs.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <algorithm>
@@ -21,7 +21,6 @@
 namespace ssm {
 namespace {
 
-constexpr int kMove = 256;          // threads of the move
 constexpr int kRun = 8;             // 16-byte pieces of a thread in a run
 constexpr int kMostKept = 32768;    // keys that the choice keeps in shared memory at most
 
@@ -70,6 +69,7 @@ __global__ void __launch_bounds__(kPick) evict_pick_kernel(KvEvictArgs a, int ro
 }
 
 // the first i < n with kept[i] != i (n if none): once one is, all later ones are
+template <int kMove>                // threads
 __device__ __forceinline__ int first_moved(const int32_t *kept, int n) {
     __shared__ int at;
     const int step = (n + kMove - 1) / kMove;
@@ -90,6 +90,7 @@ __device__ __forceinline__ int first_moved(const int32_t *kept, int n) {
 }
 
 // slices: parts of a row's 16-byte pieces for k and for v; block 2 * slices of a head moves mass
+template <int kMove>                // threads
 __global__ void __launch_bounds__(kMove) evict_move_kernel(KvEvictArgs a, int slices) {
     const int tid = threadIdx.x;
     const int hr = blockIdx.x / (2 * slices + 1), part = blockIdx.x - hr * (2 * slices + 1);
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kMove) evict_move_kernel(KvEvictArgs a, int sl
     const int run = side * kRun;
     // (the look costs 1 to 2 us, and saves the way through what stays: 128 requests of 2000 tokens cut to 1000 with the
     // evicted ones last 85 us without, 56 with)
-    const int from = first_moved(kept, a.budget);
+    const int from = first_moved<kMove>(kept, a.budget);
     struct Move { int src, dst; };                // token places among all (page * page_size + place); src < 0: none
     Move now[kRun], next[kRun];
     auto look_up = [&](Move (&m)[kRun], int base) {
@@ -182,11 +183,16 @@ hipError_t launch_kv_evict(const KvEvictArgs &a, hipStream_t stream, const char 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || most <= a.budget) return e;
     *kernel_name = "evict_move_kernel";
-    // rows of 64 bytes and more, until there are 512 moves of k: 256 heads of 2900 tokens of 256 bytes 162 us whole, 179 in
+    // rows of 64 bytes and more, until there are 512 moves of k (on blocks of 4 waves): 256 heads of 2900 tokens of 256 bytes 162 us whole, 179 in
     // halves, 215 in quarters; 512 heads of 4096 532 whole and 476 in halves; 32 heads of 500 within 10% of one another
     int slices = 1;
     while (slices * 4 <= a.row_bytes / 16 && heads * slices < 512) slices *= 2;
-    hipLaunchKernelGGL(evict_move_kernel, dim3((unsigned)(heads * (2 * slices + 1))), dim3(kMove), 0, stream, a, slices);
+    const dim3 grid((unsigned)(heads * (2 * slices + 1)));
+    // 16 waves where requests keep many runs of 4 (us with 4, with 16: 64 requests of 8 heads, 4160 -> 4096 tokens 529, 479 (of random mass, from a new cache); one of
+    // 8192 -> 8000 79, 68; one head of 30000 -> 29000 163, 113; 16 requests of 2000 -> 1900 90, 88; 8 of 2000 -> 1000 54, 58;
+    // 300 of 300 -> 256 49, 61)
+    if (a.budget >= 2048) hipLaunchKernelGGL((evict_move_kernel<1024>), grid, dim3(1024), 0, stream, a, slices);
+    else hipLaunchKernelGGL((evict_move_kernel<256>), grid, dim3(256), 0, stream, a, slices);
     return hipGetLastError();
 }
 

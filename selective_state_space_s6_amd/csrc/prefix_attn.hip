@@ -788,11 +788,17 @@ __device__ __forceinline__ void prefix_many_block(const Pp &a, int block, u32x4 
     }
 }
 
+// Waves on a SIMD.  Heads of 256 of few columns are left to one where own tokens' share would spill (4 rows of 4 fp32
+// kv heads behind 3000 tokens 30.3 us with two, 20.9; in bf16 behind 4000 19.9, 16.1); of many columns two hide more (in bf16
+// 512 columns behind 16384 99 with two, 138 with one).
+template <int CT, int DP, int NQ, bool MANY>
+constexpr int waves_of_prefix() { return MANY || (DP * NQ <= 256 && (DP < 256 || CT == KF8)) ? 2 : 1; }
+
 // The prefixes' blocks, and behind them those of the rows' own tokens (o: paged_attn_kernel.hpp's work).  Behind, since a prefix'
 // block takes longer and own ones fill what is left: 64 rows behind 16384 tokens 69 us, 74 in launches of their own, 90 with
 // 8 blocks of one kind and 8 of the other in turn; 13 rows of three prompts 24.8, 30.7 in launches of their own.
 template <int CT, int DP, bool EXACT, int NQ, bool MANY>
-__global__ void __launch_bounds__(kNT, MANY || DP * NQ <= 256 ? 2 : 1) prefix_attn_kernel(Pp a, Kp o, int prefix_blocks, int own_blocks) {
+__global__ void __launch_bounds__(kNT, (waves_of_prefix<CT, DP, NQ, MANY>())) prefix_attn_kernel(Pp a, Kp o, int prefix_blocks, int own_blocks) {
     extern __shared__ u32x4 lds[];
     if ((int)blockIdx.x < prefix_blocks) {
         if constexpr (MANY) prefix_many_block<CT, DP, EXACT, NQ>(a, blockIdx.x, lds);

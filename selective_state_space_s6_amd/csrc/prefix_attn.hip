@@ -98,6 +98,13 @@ __device__ __forceinline__ Line line_of(const Pp &a, const Place &p, int lane, i
     return n;
 }
 
+// A lane's number out of the compiler's sight: what is formed from it behind the loop over tokens is formed there, and takes
+// no registers of the loop.
+__device__ __forceinline__ int formed_here(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 template <int CT, int DP, bool EXACT, int NQ>
 __device__ __forceinline__ void prefix_few_block(const Pp &a, int block, float *lds) {
     using T = PTile<CT, DP>;
@@ -110,46 +117,55 @@ __device__ __forceinline__ void prefix_few_block(const Pp &a, int block, float *
     const int split = at.split, kv = at.kv, row0 = at.row0, nrows = at.nrows, nh = at.nh, h0 = at.h0;
     const PageSize ps(a.page_size);
 
-    // this lane's columns: their row in the block (-1: none) and head
-    int crow[NQ], chead[NQ];
+    // this lane's columns: their row in the block (-1: none)
+    int crow[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
         const int c = n * 16 + col, r = c / a.gm;
-        chead[n] = c - r * a.gm;
-        crow[n] = r < nrows && chead[n] < nh ? r : -1;
+        crow[n] = r < nrows && c - r * a.gm < nh ? r : -1;
     }
     // q (with the sign of the scale), as the scores' second operand
     const uint32_t flip = a.scale2 < 0.0f ? (CT == KF32 ? 0x80000000u : 0x80008000u) : 0u;
     const float scale2 = fabsf(a.scale2);
+    auto load_q = [&](int lane) {
+        const int col = lane & 15, grp = lane >> 4;
 #pragma unroll
-    for (int i = 0; i < T::KC * T::QW; ++i) {
-        if (i % kW != wave) continue;
-        const int dim = i / T::QW * 4 * T::KD + grp * T::KD + i % T::QW * 8;
+        for (int i = 0; i < T::KC * T::QW; ++i) {
+            if (i % kW != wave) continue;
+            const int dim = i / T::QW * 4 * T::KD + grp * T::KD + i % T::QW * 8;
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-            u32x4 x = {0, 0, 0, 0};
-            if (crow[n] >= 0 && (EXACT || dim < a.d))
-                x = *(const u32x4 *)(a.q + (row0 + crow[n]) * a.q_sr + (h0 + chead[n]) * a.q_sh + dim * (CT == KF32 ? 4 : 2));
+            for (int n = 0; n < NQ; ++n) {
+                u32x4 x = {0, 0, 0, 0};
+                const int c = n * 16 + col, r = c / a.gm, h = c - r * a.gm;
+                if (r < nrows && h < nh && (EXACT || dim < a.d))
+                    x = *(const u32x4 *)(a.q + (row0 + r) * a.q_sr + (h0 + h) * a.q_sh + dim * (CT == KF32 ? 4 : 2));
 #pragma unroll
-            for (int w = 0; w < 4; ++w) x[w] ^= flip;
-            q_lds[(i * NQ + n) * 64 + lane] = x;
+                for (int w = 0; w < 4; ++w) x[w] ^= flip;
+                q_lds[(i * NQ + n) * 64 + lane] = x;
+            }
         }
-    }
+    };
+    load_q(lane);
     Line line = line_of(a, at, lane, T::UNIT);
     const int first = line.first, last = line.last;
     __syncthreads();
 
     float m[NQ], l[NQ];                      // of the columns; l over this lane's tokens only
     f32x4 acc[NQ][VB][VD];
+    auto restart = [&]() {
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-        m[n] = -INFINITY;
-        l[n] = 0.0f;
+        for (int n = 0; n < NQ; ++n) {
+            m[n] = -INFINITY;
+            l[n] = 0.0f;
 #pragma unroll
-        for (int b = 0; b < VB; ++b)
+            for (int b = 0; b < VB; ++b)
 #pragma unroll
-            for (int i = 0; i < VD; ++i) acc[n][b][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-    }
+                for (int i = 0; i < VD; ++i) acc[n][b][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        }
+    };
+    restart();
+    const int64_t to0 = ((int64_t)split * a.batch + row0) * a.n_heads + h0;
+    bool left = false;                       // the part of column `tid` has been written
     const char *kb = a.k + kv * a.c_sh + grp * 16, *vb = a.v + kv * a.c_sh;
 
     // one prefix after the other, with the columns of its rows
@@ -197,8 +213,7 @@ __device__ __forceinline__ void prefix_few_block(const Pp &a, int block, float *
                 }
             }
         };
-        int t0 = u0 * T::UNIT + wave * T::NT;
-        if (t0 >= t_end) continue;
+        int t0 = u0 * T::UNIT + wave * T::NT;    // (a wave without a tile reads the cache's first row)
         int page = page_of(t0);
         uint64_t ok = __ballot((uint32_t)page < (uint32_t)a.n_pages) & ALL;
         uint64_t off = off_of(t0, page);
@@ -372,55 +387,70 @@ __device__ __forceinline__ void prefix_few_block(const Pp &a, int block, float *
                 }
             }
         }
-    }
 
-    // ---- join the block's waves
+        // ---- join the block's waves, for the columns of this prefix; the others start anew: their weights were 0, but 0
+        // times a V that is not finite is NaN
+        const int t = formed_here(tid), t_col = t & 15, t_grp = (t & 63) >> 4, t_wave = t >> 6;
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-        l[n] = head_sum(l[n]);
-        if (grp == 0) { wave_m[wave][n * 16 + col] = m[n]; wave_l[wave][n * 16 + col] = l[n]; }
-    }
-    __syncthreads();                         // (readers of q, too)
-    const int64_t to0 = ((int64_t)split * a.batch + row0) * a.n_heads + h0;
-    // a column's maximum and sum, by one thread
-    if (tid < 16 * NQ) {
-        const int r = tid / a.gm, h = tid - r * a.gm;
-        float mt = -INFINITY, ls = 0.0f;
+        for (int n = 0; n < NQ; ++n) {
+            l[n] = head_sum(l[n]);
+            if (t_grp == 0) { wave_m[t_wave][n * 16 + t_col] = m[n]; wave_l[t_wave][n * 16 + t_col] = l[n]; }
+        }
+        __syncthreads();                     // (readers of q, too)
+        auto has = [&](int r, int h) { return r < nrows && h < nh && (mine >> r & 1); };
+        // a column's maximum and sum, by one thread
+        if (t < 16 * NQ) {
+            const int r = t / a.gm, h = t - r * a.gm;
+            float mt = -INFINITY, ls = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kW; ++w) mt = fmaxf(mt, wave_m[w][tid]);
+            for (int w = 0; w < kW; ++w) mt = fmaxf(mt, wave_m[w][t]);
 #pragma unroll
-        for (int w = 0; w < kW; ++w) ls += wave_l[w][tid] * (mt == -INFINITY ? 1.0f : exp2_fast(wave_m[w][tid] - mt));
-        if (r < nrows && h < nh) *(float2 *)(a.ml + (to0 + r * a.n_heads + h) * 2) = make_float2(mt, ls);
-    }
-    if (first >= last) return;               // no tokens: weighs nothing
+            for (int w = 0; w < kW; ++w) ls += wave_l[w][t] * (mt == -INFINITY ? 1.0f : exp2_fast(wave_m[w][t] - mt));
+            if (has(r, h)) {
+                *(float2 *)(a.ml + (to0 + r * a.n_heads + h) * 2) = make_float2(mt, ls);
+                left = true;
+            }
+        }
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-        float top = wave_m[0][n * 16 + col];
+        for (int n = 0; n < NQ; ++n) {
+            float top = wave_m[0][n * 16 + t_col];
 #pragma unroll
-        for (int w = 1; w < kW; ++w) top = fmaxf(top, wave_m[w][n * 16 + col]);
-        const float f = top == -INFINITY ? 0.0f : exp2_fast(m[n] - top);
-        float *to = lds + (wave * 16 * NQ + n * 16 + col) * PITCH;
+            for (int w = 1; w < kW; ++w) top = fmaxf(top, wave_m[w][n * 16 + t_col]);
+            const float f = top == -INFINITY ? 0.0f : exp2_fast(m[n] - top);
+            float *to = lds + (t_wave * 16 * NQ + n * 16 + t_col) * PITCH;
 #pragma unroll
-        for (int b = 0; b < VB; ++b)
+            for (int b = 0; b < VB; ++b)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+                for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int i = 0; i < VD; i += 4)
-                    *(float4 *)(to + (b * 16 + grp * 4 + r) * VD + i) =
-                        make_float4(acc[n][b][i][r] * f, acc[n][b][i + 1][r] * f, acc[n][b][i + 2][r] * f, acc[n][b][i + 3][r] * f);
-    }
-    __syncthreads();
-    constexpr int D4 = DP / 4, SIDE = kNT / D4;          // columns side by side, 4 dims a thread
-    const int cc = tid / D4, e = (tid - cc * D4) * 4;
-    if (cc >= SIDE || (!EXACT && e >= a.d)) return;
+                    for (int i = 0; i < VD; i += 4)
+                        *(float4 *)(to + (b * 16 + t_grp * 4 + r) * VD + i) =
+                            make_float4(acc[n][b][i][r] * f, acc[n][b][i + 1][r] * f, acc[n][b][i + 2][r] * f, acc[n][b][i + 3][r] * f);
+        }
+        __syncthreads();
+        constexpr int D4 = DP / 4, SIDE = kNT / D4;          // columns side by side, 4 dims a thread
+        const int cc = t / D4, e = (t - cc * D4) * 4;
+        if (cc < SIDE && (EXACT || e < a.d)) {
 #pragma unroll 4
-    for (int c = cc; c < 16 * NQ; c += SIDE) {
-        const int r = c / a.gm, h = c - r * a.gm;
-        if (r >= nrows || h >= nh) continue;
-        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int c = cc; c < 16 * NQ; c += SIDE) {
+                const int r = c / a.gm, h = c - r * a.gm;
+                if (!has(r, h)) continue;
+                f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int w = 0; w < kW; ++w) v += *(const f32x4 *)(lds + (w * 16 * NQ + c) * PITCH + e);
-        *(f32x4 *)(a.part + (to0 + r * a.n_heads + h) * a.d + e) = v;
+                for (int w = 0; w < kW; ++w) v += *(const f32x4 *)(lds + (w * 16 * NQ + c) * PITCH + e);
+                *(f32x4 *)(a.part + (to0 + r * a.n_heads + h) * a.d + e) = v;
+            }
+        }
+        if (end >= last) break;
+        __syncthreads();                     // the next prefix: q again, where the outputs were
+        load_q(formed_here(lane));
+        restart();
+        __syncthreads();
+    }
+    // columns without a token in this part weigh nothing
+    if (tid < 16 * NQ && !left) {
+        const int r = tid / a.gm, h = tid - r * a.gm;
+        if (r < nrows && h < nh) *(float2 *)(a.ml + (to0 + r * a.n_heads + h) * 2) = make_float2(-INFINITY, 0.0f);
     }
 }
 
@@ -471,22 +501,22 @@ __device__ __forceinline__ void prefix_many_block(const Pp &a, int block, u32x4 
     const PageSize ps(a.page_size);
     Line line = line_of(a, at, lane, T::NT);
 
-    // this lane's columns: their row in the block (-1: none) and head; q with the sign of the scale
+    // this lane's columns: their row in the block (-1: none); q with the sign of the scale
     const uint32_t flip = a.scale2 < 0.0f ? (T::F32 ? 0x80000000u : 0x80008000u) : 0u;
     const float scale2 = fabsf(a.scale2);
-    int crow[NQ], chead[NQ];
+    int crow[NQ];
     u32x4 q[NQ][T::KC * T::QW];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
         const int c = (wave * NQ + n) * 16 + col, r = c / a.gm;
-        chead[n] = c - r * a.gm;
-        crow[n] = r < at.nrows && chead[n] < at.nh ? r : -1;
+        const int h = c - r * a.gm;
+        crow[n] = r < at.nrows && h < at.nh ? r : -1;
 #pragma unroll
         for (int i = 0; i < T::KC * T::QW; ++i) {
             const int dim = i / T::QW * 4 * T::KD + grp * T::KD + i % T::QW * 8;
             u32x4 x = {0, 0, 0, 0};
             if (crow[n] >= 0 && (EXACT || dim < a.d))
-                x = *(const u32x4 *)(a.q + (at.row0 + crow[n]) * a.q_sr + (at.h0 + chead[n]) * a.q_sh + dim * (T::F32 ? 4 : 2));
+                x = *(const u32x4 *)(a.q + (at.row0 + crow[n]) * a.q_sr + (at.h0 + h) * a.q_sh + dim * (T::F32 ? 4 : 2));
 #pragma unroll
             for (int w = 0; w < 4; ++w) x[w] ^= flip;
             q[n][i] = x;
@@ -501,15 +531,23 @@ __device__ __forceinline__ void prefix_many_block(const Pp &a, int block, u32x4 
     // of fp32 it is the first place, over this lane's tokens only.
     float m[NQ];
     f32x4 l[NQ], acc[NQ][VB][VD];
+    auto restart = [&]() {
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-        m[n] = -INFINITY;
-        l[n] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        for (int n = 0; n < NQ; ++n) {
+            m[n] = -INFINITY;
+            l[n] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int b = 0; b < VB; ++b)
+            for (int b = 0; b < VB; ++b)
 #pragma unroll
-            for (int i = 0; i < VD; ++i) acc[n][b][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-    }
+                for (int i = 0; i < VD; ++i) acc[n][b][i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        }
+    };
+    restart();
+    bool left[NQ] = {};                      // the column's part has been written
+    auto place = [&](int n) {
+        const int c = formed_here((wave * NQ + n) * 16 + col), r = c / a.gm;
+        return ((int64_t)at.split * a.batch + at.row0 + r) * a.n_heads + at.h0 + c - r * a.gm;
+    };
     // -1 in the low or the high half of a pair.  (Out of the compiler's sight: as a constant, 0x0000bf80 becomes the
     // instruction's own -1.0, which stands in the high half.)
     uint32_t low = 0xbf80u, high = 0xbf800000u;
@@ -765,27 +803,36 @@ __device__ __forceinline__ void prefix_many_block(const Pp &a, int block, u32x4 
             }
             __syncthreads();
         }
+
+        // The columns of this prefix are done, since a row has one.  All start anew, the others too: their weights were 0,
+        // but 0 times a V that is not finite is NaN.
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            const float sum = T::F32 ? head_sum(l[n][0]) : l[n][0];
+            if (!in[n]) continue;
+            const int64_t to = place(n);
+            const int g = formed_here(grp);
+            if (g == 0) *(float2 *)(a.ml + to * 2) = make_float2(m[n], sum);
+#pragma unroll
+            for (int b = 0; b < VB; ++b)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int dim = (b * 16 + g * 4 + r) * VD;
+                    if (!EXACT && dim >= a.d) continue;
+#pragma unroll
+                    for (int i = 0; i < VD; i += 4)
+                        *(f32x4 *)(a.part + to * a.d + dim + i) =
+                            (f32x4){acc[n][b][i][r], acc[n][b][i + 1][r], acc[n][b][i + 2][r], acc[n][b][i + 3][r]};
+                }
+            left[n] = true;
+        }
+        restart();
     }
 
+    if (grp != 0) return;
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-        const float sum = T::F32 ? head_sum(l[n][0]) : l[n][0];
-        if (crow[n] < 0) continue;
-        const int64_t to = ((int64_t)at.split * a.batch + at.row0 + crow[n]) * a.n_heads + at.h0 + chead[n];
-        if (grp == 0) *(float2 *)(a.ml + to * 2) = make_float2(m[n], sum);
-        if (line.first >= line.last) continue;       // no tokens: weighs nothing
-#pragma unroll
-        for (int b = 0; b < VB; ++b)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int dim = (b * 16 + grp * 4 + r) * VD;
-                if (!EXACT && dim >= a.d) continue;
-#pragma unroll
-                for (int i = 0; i < VD; i += 4)
-                    *(f32x4 *)(a.part + to * a.d + dim + i) =
-                        (f32x4){acc[n][b][i][r], acc[n][b][i + 1][r], acc[n][b][i + 2][r], acc[n][b][i + 3][r]};
-            }
-    }
+    for (int n = 0; n < NQ; ++n)             // no token in this part: weighs nothing
+        if (crow[n] >= 0 && !left[n]) *(float2 *)(a.ml + place(n) * 2) = make_float2(-INFINITY, 0.0f);
 }
 
 // Waves on a SIMD.  Heads of 256 of few columns are left to one where own tokens' share would spill (4 rows of 4 fp32

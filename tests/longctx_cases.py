@@ -99,6 +99,22 @@ def compare(got, want, rows_of, q, scale, bf16, weights):
     return worst
 
 
+def ratios(got, want, rows_of, q, scale, bf16, weights):
+    """Ratios of error and bound of o (rows, heads, d) and of lse (rows, heads), as `compare` bounds them; inf where a
+    result is NaN or infinite and should not be, and where a query without tokens has anything but o = 0 and lse = -inf."""
+    o, lse, q = n64(got[0]), n64(got[1]), n64(q)
+    ro, rl = np.full(o.shape, np.inf), np.full(lse.shape, np.inf)
+    for r in range(o.shape[0]):
+        for h in range(o.shape[1]):
+            k, v = rows_of(r, h)
+            if len(k) == 0:
+                ro[r, h], rl[r, h] = np.where(o[r, h] == 0, 0.0, np.inf), 0.0 if lse[r, h] == -np.inf else np.inf
+                continue
+            bo, bl = attention_bound(q[r, h], k, v, want[0][r, h], scale, bf16, weights, want[1][r, h])
+            ro[r, h], rl[r, h] = np.abs(o[r, h] - want[0][r, h]) / bo, abs(lse[r, h] - want[1][r, h]) / bl
+    return np.where(np.isnan(ro), np.inf, ro), np.where(np.isnan(rl), np.inf, rl)
+
+
 def captured(call):
     """`call` run once on a side stream and then captured; the graph."""
     side = torch.cuda.Stream()

@@ -49,8 +49,9 @@ extern "C" {
  * Layouts: prefix (batch) int32; prefix_table (n_prefixes, max_prefix_pages)
  * int32, row stride prefix_stride; prefix_lens (n_prefixes) int32; the others as
  * in ssm_paged_attn_decode_fwd.  No output may alias an input.
- * Limits: those of ssm_paged_attn_decode_fwd, for (batch, max_pages) and for
- * (n_prefixes, max_prefix_pages) in their place; batch * n_heads below 2^24.
+ * Limits: those of ssm_paged_attn_decode_fwd; n_prefixes from 1 to 2^31 - 1,
+ * max_prefix_pages * page_size at most 2^30, and min(n_prefixes, 64) times that / 16
+ * (rounded up) below 2^31; batch * n_heads below 2^24.
  * Workspace: ssm_prefix_attn_decode_fwd_workspace_size() bytes, 16-byte aligned. */
 size_t ssm_prefix_attn_decode_fwd_workspace_size(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t headdim,
                                                  int64_t max_prefix_pages, int64_t max_pages, int64_t page_size);

@@ -72,6 +72,10 @@ int ssm_prefix_attn_decode_fwd(const void *q, const void *k_cache, const void *v
     if (n_prefixes >= k2p31 || prefix_stride >= (int64_t(1) << 40) || batch * n_heads >= (1 << 24) ||
         (double)max_prefix_pages * (double)page_size > 1073741824.0)
         return fail(SSM_ERR_UNSUPPORTED, "%s: problem too large", E);
+    // (the prefixes of a block's rows, 64 at most, stand in one line of tiles of 16 tokens or more, counted in 32 bits)
+    if ((n_prefixes < 64 ? n_prefixes : 64) * ((max_prefix_pages * page_size + 15) / 16) >= k2p31)
+        return fail(SSM_ERR_UNSUPPORTED, "%s: prefixes of up to %lld tokens are too long together", E,
+                    (long long)(max_prefix_pages * page_size));
     if (batch == 0) return SSM_OK;
     REQUIRE_PTR(E, q); REQUIRE_PTR(E, k_cache); REQUIRE_PTR(E, v_cache); REQUIRE_PTR(E, prefix); REQUIRE_PTR(E, prefix_table);
     REQUIRE_PTR(E, prefix_lens); REQUIRE_PTR(E, block_table); REQUIRE_PTR(E, lens); REQUIRE_PTR(E, o);

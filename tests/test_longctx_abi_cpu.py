@@ -119,6 +119,19 @@ def test_prefix_checks(lib):
                                             "prefix_lens": "prefix_lens", "table": "block_table", "lens": "lens"}))
 
 
+def test_prefixes_too_long_together(lib):
+    """What a block may walk is counted in 32 bits: 64 prefixes, or all of them, in tiles of 16 tokens."""
+    base = _base(PREFIX, 10, n_prefixes=3, max_prefix_pages=16, prefix_stride=1 << 26, ws=None, ws_bytes=0)
+    long = lambda n, tokens: dict(n_prefixes=n, max_prefix_pages=tokens // 16)  # noqa: E731
+    _table(lib, "ssm_prefix_attn_decode_fwd", PREFIX, base, [
+        (long(32, 1 << 30), UNSUPPORTED, "too long together"), (long(31, 1 << 30), WORKSPACE, "workspace"),
+        (long(64, 1 << 29), UNSUPPORTED, "too long together"), (long(64, (1 << 29) - 16), WORKSPACE, "workspace"),
+        (long(1 << 20, 1 << 29), UNSUPPORTED, "too long together"), (long(1 << 20, (1 << 29) - 16), WORKSPACE, "workspace"),
+        (dict(n_prefixes=32, page_size=1 << 20, n_pages=8, c_st=64, c_sh=64, c_sp=64, max_prefix_pages=1 << 10), UNSUPPORTED, "too long together"),
+        (dict(n_prefixes=1 << 31), UNSUPPORTED, "too large"),
+    ])
+
+
 BOUNDS = ["k", "bounds", "table", "len_old", "lens", "batch", "n_kv", "d", "max_pages", "table_stride"] + CACHE + STRIDES + ["kv", "stream"]
 
 

@@ -86,8 +86,9 @@ __global__ void __launch_bounds__(kNT) kv_bounds_kernel(KvBoundsArgs a) {
     while (2 * side * chunks <= 64) side *= 2;
     const int sub = lane / chunks, c = lane - sub * chunks;
     const bool works = sub < side;
-    for (int item = (int)blockIdx.x * kWaves + wave; item < items; item += (int)gridDim.x * kWaves) {
-        const int touch = item / a.n_kv, g = item - touch * a.n_kv;
+    // (items are fewer than 2^31, and a step behind the last of them may pass that)
+    for (uint32_t item = blockIdx.x * kWaves + wave; item < (uint32_t)items; item += gridDim.x * kWaves) {
+        const int touch = (int)item / a.n_kv, g = (int)item - touch * a.n_kv;
         int r = 0, end = a.batch - 1;             // the first request with upto > touch
         while (r < end) {
             const int mid = (r + end) >> 1;

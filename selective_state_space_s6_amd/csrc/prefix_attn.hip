@@ -527,15 +527,13 @@ __device__ __forceinline__ void prefix_many_block(const Pp &a, int block, u32x4 
     for (int n = 0; n < NQ; ++n) any = any || crow[n] >= 0;
     const bool works = __any(any);           // (a wave without columns only brings K and V)
 
-    // Maxima and sums of the columns.  A sum is a row of the output with V = 1, the same in all four of its places;
-    // of fp32 it is the first place, over this lane's tokens only.
-    float m[NQ];
-    f32x4 l[NQ], acc[NQ][VB][VD];
+    float m[NQ], l[NQ];                      // of the columns; l over this lane's tokens only
+    f32x4 acc[NQ][VB][VD];
     auto restart = [&]() {
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             m[n] = -INFINITY;
-            l[n] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+            l[n] = 0.0f;
 #pragma unroll
             for (int b = 0; b < VB; ++b)
 #pragma unroll
@@ -744,10 +742,8 @@ __device__ __forceinline__ void prefix_many_block(const Pp &a, int block, u32x4 
 #pragma unroll
                             for (int i = 0; i < NX; ++i) s[n][i >> 2][i & 3] = counts(n, i) ? s[n][i >> 2][i & 3] : 0.0f;
                         }
-                        if constexpr (T::F32) {
 #pragma unroll
-                            for (int i = 0; i < NX; ++i) l[n][0] += s[n][i >> 2][i & 3];
-                        }
+                        for (int i = 0; i < NX; ++i) l[n] += s[n][i >> 2][i & 3];
                     }
                     if constexpr (T::F32) {
                         const u32x4 *vp = vop + part * NX * VB * 64;
@@ -774,12 +770,6 @@ __device__ __forceinline__ void prefix_many_block(const Pp &a, int block, u32x4 
                                 ph[n][i] = pack_bf16(x0, x1);
                                 pl[n][i] = pack_bf16(minus(ph[n][i], low, x0), minus(ph[n][i], high, x1));
                             }
-#pragma unroll
-                        for (int n = 0; n < NQ; ++n) {
-                            const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-                            l[n] = mfma_bf16(ones, ph[n], l[n]);
-                            l[n] = mfma_bf16(ones, pl[n], l[n]);
-                        }
 #pragma unroll
                         for (int b = 0; b < VB; ++b)
 #pragma unroll
@@ -808,7 +798,7 @@ __device__ __forceinline__ void prefix_many_block(const Pp &a, int block, u32x4 
         // but 0 times a V that is not finite is NaN.
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-            const float sum = T::F32 ? head_sum(l[n][0]) : l[n][0];
+            const float sum = head_sum(l[n]);
             if (!in[n]) continue;
             const int64_t to = place(n);
             const int g = formed_here(grp);

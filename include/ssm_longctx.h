@@ -42,9 +42,7 @@ extern "C" {
  * A prefix's keys and values are read once for 16 to 128 (row, query head)
  * pairs of a kv head whose rows stand next to each other: rows of one prefix cost
  * least side by side, and any order is right.
- * Arithmetic: as ssm_paged_attn_decode_fwd, except that the softmax weights of
- * a prefix's tokens enter their product with v as two bf16 values (17 bits, an
- * error below 2^-17 of each weight) where v is bf16 or 8-bit.
+ * Arithmetic: as ssm_paged_attn_decode_fwd.
  *
  * Layouts: prefix (batch) int32; prefix_table (n_prefixes, max_prefix_pages)
  * int32, row stride prefix_stride; prefix_lens (n_prefixes) int32; the others as

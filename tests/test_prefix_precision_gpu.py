@@ -3,7 +3,9 @@ tokens' shares nearly cancel, so that an error of a weight is far above the outp
 
 A prefix has two tokens, of scores 0 and s in [-1.2, 0): weights 1, exactly, and p = exp(s).  s is a sum of two products,
 exact but for one rounding, times log2(e), rounded twice, so its exponential is within 4 u |s| + 2 u < 8 u of p (u = 2^-24)
-where 2^x is within 2 u of itself.  v0 = -n1, v1 = n2 and q are such that p n2 is n1 (1 + 2^-14) or so, for each (row, head)
+where 2^x is within 2 u of itself; products with v and their sums in fp32 are at most six roundings of what they add up, and
+the quotient two more: 16 u (|v0| + p |v1|) / (1 + p) in all, with the output's own rounding behind it, 2^-8 |o|.  A weight
+of 17 bits is off by up to 2^-18, 64 u.  v0 = -n1, v1 = n2 and q are such that p n2 is n1 (1 + 2^-14) or so, for each (row, head)
 in one dim of its own."""
 import numpy as np
 import pytest
@@ -58,4 +60,15 @@ def test_lse_keeps_all_its_bits(cuda_device, form):
     got, want = n64(s.call()[1]), np.log1p(s.p[..., 0])
     ratio = np.abs(got - want) / (8 * U)
     report("lse %s" % (form,), of_bound=float(ratio.max()))
+    assert (ratio <= 1.0).all()
+
+
+@pytest.mark.parametrize("form", FORMS, ids=IDS)
+def test_weights_keep_all_their_bits(cuda_device, form):
+    s = Two(cuda_device, *form)
+    o = n64(s.call()[0])
+    want = (s.v0 + s.p * s.v1) / (1 + s.p)
+    bound = 16 * U * (np.abs(s.v0) + s.p * s.v1) / (1 + s.p) + 2.0 ** -8 * np.abs(want)
+    ratio = np.abs(o - want) / bound
+    report("weights %s" % (form,), of_bound=float(ratio.max()))
     assert (ratio <= 1.0).all()

@@ -50,7 +50,7 @@ struct PagedAttnArgs {
     int64_t max_pages, table_stride, n_pages, page_size, q_sr, q_sh, c_sp, c_st, c_sh;
     float scale, k_scale, v_scale; int64_t window; int kv_dtype; void *workspace;
     const int32_t *selected; int64_t top_k;      // (batch, kv heads, top_k) pages of each (row, kv head), or NULL
-    bool o_f32;                                  // o in fp32 whatever the cache's type
+    bool raw;                                    // o in fp32 and unnormalised, without v_scale; lse: (rows, heads, 2), maxima (of log2 units) and sums
 };
 size_t paged_attn_workspace_bytes(int64_t batch, int64_t n_heads, int64_t n_kv_heads, int64_t headdim,
                                   int64_t max_pages, int64_t page_size);

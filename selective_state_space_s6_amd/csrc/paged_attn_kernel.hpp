@@ -64,7 +64,7 @@ struct Kp {
     int fixed;                      // > 0: one row, of which each (kv head, pass) has as many pieces, empty ones too
     float scale2, v_scale;          // scale2: score -> log2 units
     const int32_t *sel; int top;    // (batch, kv heads, top) pages of each (row, kv head), or NULL: all of them
-    bool o_f32;                     // o in fp32 whatever the cache's type
+    bool raw;                       // o in fp32 and unnormalised, without v_scale; lse: a maximum (of log2 units) and a sum each
 };
 
 // The tokens of a row: [lo, hi), in `units` units.  Of chosen pages (SEL) tokens are counted through
@@ -174,9 +174,10 @@ __device__ __forceinline__ void paged_attn_block(const Kp &a, int block, int all
             const int kvs = hp / a.passes, pass = hp - kvs * a.passes, kv = (kvs << a.wh_lg) + side;
             const int nh = min(a.gmax, a.group - pass * a.gmax);
             const int64_t h = (int64_t)row * a.n_heads + kv * a.group + pass * a.gmax;
-            const int OE = CT == KF32 || a.o_f32 ? 4 : 2;
+            const int OE = CT == KF32 || a.raw ? 4 : 2;
             for (int i = tid; i < nh * a.d * OE / 16; i += W * 64) *(u32x4 *)(a.o + h * a.d * OE + i * 16) = (u32x4){0, 0, 0, 0};
-            if (a.lse && tid < nh) a.lse[h + tid] = -INFINITY;
+            if (a.raw && tid < nh) ((float2 *)a.lse)[h + tid] = make_float2(-INFINITY, 0.0f);
+            else if (a.lse && tid < nh) a.lse[h + tid] = -INFINITY;
             return;
         }
     } else if (a.fixed) {
@@ -491,11 +492,12 @@ __device__ __forceinline__ void paged_attn_block(const Kp &a, int block, int all
 #pragma unroll
             for (int w = 0; w < W; ++w) ls += wave_l[w][h] * (mt == -INFINITY ? 0.0f : exp2_fast(wave_m[w][h] - mt));
             if (whole) {
-                const float n = ls > 0.0f || ls != ls ? a.v_scale / ls : 0.0f;
-                const int64_t to = ((int64_t)row * a.n_heads + h0 + h) * a.d + e;
-                if (CT == KF32 || a.o_f32) *(f32x4 *)(a.o + to * 4) = v * n;
+                const float n = a.raw ? 1.0f : ls > 0.0f || ls != ls ? a.v_scale / ls : 0.0f;
+                const int64_t rh = (int64_t)row * a.n_heads + h0 + h, to = rh * a.d + e;
+                if (CT == KF32 || a.raw) *(f32x4 *)(a.o + to * 4) = v * n;
                 else *(uint2 *)(a.o + to * 2) = make_uint2(pack_bf16(v[0] * n, v[1] * n), pack_bf16(v[2] * n, v[3] * n));
-                if (e == 0 && a.lse) a.lse[(int64_t)row * a.n_heads + h0 + h] = (mt == -INFINITY ? 0.0f : mt * kLn2) + logf(ls);
+                if (e == 0 && a.raw) ((float2 *)a.lse)[rh] = make_float2(mt, ls);
+                else if (e == 0 && a.lse) a.lse[rh] = (mt == -INFINITY ? 0.0f : mt * kLn2) + logf(ls);
             } else {
                 *(f32x4 *)(a.part + ((int64_t)slot * a.gmax + h) * a.d + e) = v;
                 if (e == 0) *(float2 *)(a.ml + ((int64_t)slot * a.gmax + h) * 2) = make_float2(mt, ls);
@@ -530,10 +532,10 @@ __global__ void __launch_bounds__(kNT) paged_attn_join_kernel(Kp a, int grid) {
     };
     // The threads of a head: slice sl of its pieces, dims e..e+3; the caller adds up the slices.
     // Every wave forms the maximum and the sum for itself: lane i has pieces i, i + 64, ...
-    // n: pieces (1: the head was written whole); scale, lse: of the sum
-    struct Joined { f32x4 v; int n; float scale, lse; };
+    // n: pieces (1: the head was written whole); scale, lse: of the sum; m, l: maximum and sum
+    struct Joined { f32x4 v; int n; float scale, lse, m, l; };
     auto join = [&](int h, int sl, int slices, int e) {
-        Joined r = {{0.0f, 0.0f, 0.0f, 0.0f}, 1, 0.0f, -INFINITY};
+        Joined r = {{0.0f, 0.0f, 0.0f, 0.0f}, 1, 0.0f, -INFINITY, -INFINITY, 0.0f};
         const int kv = h / a.group, side = kv & ((1 << a.wh_lg) - 1), pass = (h - kv * a.group) / a.gmax;
         const int hh = h - kv * a.group - pass * a.gmax;
         // the blocks whose pieces hold this head's first and last unit
@@ -556,6 +558,7 @@ __global__ void __launch_bounds__(kNT) paged_attn_join_kernel(Kp a, int grid) {
         for (int i = lane + 64; i < n; i += 64) m = fmaxf(m, a.ml[place(i) * 2]);
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+        r.m = m;
         m = m == -INFINITY ? 0.0f : m;
         const float scale = exp2_fast(own.x - m);
         float l = own.y * scale;
@@ -575,16 +578,22 @@ __global__ void __launch_bounds__(kNT) paged_attn_join_kernel(Kp a, int grid) {
             for (int i = sl + 2 * slices; i < n; i += slices)
                 add(*(const f32x4 *)(a.part + place(i) * a.d + e), exp2_fast(a.ml[place(i) * 2] - m));
         }
-        r.scale = l > 0.0f || l != l ? a.v_scale / l : 0.0f;
+        r.scale = a.raw ? 1.0f : l > 0.0f || l != l ? a.v_scale / l : 0.0f;
         r.lse = m * kLn2 + logf(l);
+        r.l = l;
         return r;
+    };
+    auto store_lse = [&](int h, const Joined &r) {
+        const int64_t rh = (int64_t)row * a.n_heads + h;
+        if (a.raw) ((float2 *)a.lse)[rh] = make_float2(r.m, r.l);
+        else if (a.lse) a.lse[rh] = r.lse;
     };
     const int h0 = (int)blockIdx.y * HB, h1 = min(h0 + HB, a.n_heads);
     // (a head's pieces lie within nu units, a block's share is total / blocks of them)
     if (HB > 1 && (nu == 0 || nu * blocks / total + 2 <= 16)) {
         const int h = h0 + wave, slices = 64 / d4, sl = lane / d4, e = (lane - sl * d4) * 4;
         if (h >= h1) return;
-        Joined r = {{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0.0f, -INFINITY};
+        Joined r = {{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0.0f, -INFINITY, -INFINITY, 0.0f};
         if (nu > 0) r = join(h, sl, slices, e);
         if (r.n == 1) return;
         f32x4 v = r.v;
@@ -592,12 +601,12 @@ __global__ void __launch_bounds__(kNT) paged_attn_join_kernel(Kp a, int grid) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] += __shfl(r.v[i], lane + s * d4);
         if (sl == 0) store(h, e, v * r.scale);
-        if (lane == 0 && a.lse) a.lse[(int64_t)row * a.n_heads + h] = r.lse;
+        if (lane == 0) store_lse(h, r);
         return;
     }
     const int cols = d4 / gridDim.z, slices = kNT / cols, sl = tid / cols, e = ((int)blockIdx.z * cols + tid - sl * cols) * 4;
     for (int h = h0; h < h1; ++h) {
-        Joined r = {{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0.0f, -INFINITY};
+        Joined r = {{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0.0f, -INFINITY, -INFINITY, 0.0f};
         if (nu > 0) r = join(h, sl, slices, e);
         if (r.n == 1) continue;                  // the same in the whole block
         out[tid] = r.v;
@@ -607,7 +616,7 @@ __global__ void __launch_bounds__(kNT) paged_attn_join_kernel(Kp a, int grid) {
             for (int s = 1; s < min(slices, r.n); ++s) v += out[s * cols + tid];
             store(h, e, v * r.scale);
         }
-        if (tid == 0 && blockIdx.z == 0 && a.lse) a.lse[(int64_t)row * a.n_heads + h] = r.lse;
+        if (tid == 0 && blockIdx.z == 0) store_lse(h, r);
         __syncthreads();
     }
 }
@@ -718,7 +727,7 @@ Kp kernel_args(const PagedAttnArgs &a) {
     k.d = a.headdim; k.n_pages = (int)a.n_pages; k.page_size = (int)a.page_size;
     k.row_len = (int)(a.max_pages * a.page_size);
     k.max_len = (int)(rows_pages(a) * a.page_size);
-    k.sel = a.selected; k.top = (int)a.top_k; k.o_f32 = a.o_f32;
+    k.sel = a.selected; k.top = (int)a.top_k; k.raw = a.raw;
     k.window = a.window > 0 && a.window < k.max_len ? (int)a.window : 0;
     k.scale2 = a.scale * (a.kv_dtype == SSM_KV_F8E4M3 ? a.k_scale : 1.0f) * kLog2e;
     k.v_scale = a.kv_dtype == SSM_KV_F8E4M3 ? a.v_scale : 1.0f;
@@ -734,7 +743,7 @@ hipError_t launch_join(const PagedAttnArgs &a, const Kp &k, int grid, hipStream_
     const int64_t pieces = (grid >> k.wh_lg) / (a.batch * (a.n_kv_heads >> k.wh_lg) * k.passes);
     const int split = pieces >= 64 && a.headdim % 32 == 0 ? a.headdim / 32 : 1, hb = pieces >= 8 ? 1 : 4;
     const dim3 g((unsigned)a.batch, (unsigned)((a.n_heads + hb - 1) / hb), (unsigned)split);
-    const bool bf16 = a.kv_dtype != SSM_KV_F32 && !a.o_f32;
+    const bool bf16 = a.kv_dtype != SSM_KV_F32 && !a.raw;
     if (hb == 1 && bf16) hipLaunchKernelGGL((paged_attn_join_kernel<true, 1>), g, dim3(kNT), 0, stream, k, grid);
     else if (hb == 1) hipLaunchKernelGGL((paged_attn_join_kernel<false, 1>), g, dim3(kNT), 0, stream, k, grid);
     else if (bf16) hipLaunchKernelGGL((paged_attn_join_kernel<true, 4>), g, dim3(kNT), 0, stream, k, grid);

@@ -2,7 +2,7 @@
 // (ssm_prefix_attn_decode_fwd in include/ssm_longctx.h).
 //
 // One launch has the blocks of the prefixes and, behind them, those of the rows' own tokens (paged_attn_kernel.hpp's
-// work, its output in fp32 and normalised); another joins both by their maxima and sums, o = sum_i o_i 2^(m_i - m) / l.
+// work, its output in fp32 and unnormalised); another joins both by their maxima and sums, o = sum_i o_i 2^(m_i - m) / l.
 // Own tokens of a length that is cut into pieces are joined by a launch of their own before it.
 //
 // The (row, query head) pairs of a kv head are columns of the matrix products: scores S^T = K Q^T, output O^T = V^T P^T.
@@ -41,7 +41,9 @@ struct Pp {
     const char *q; const char *k; const char *v; const int32_t *prefix; const int32_t *table; const int32_t *lens;
     float *part;                    // unnormalised outputs (split, row, head, d)
     float *ml;                      // and their maxima and sums (split, row, head, 2)
-    const float *o_own; const float *lse_own; char *o; float *lse;
+    const float *o_own;             // and those of the rows' own tokens (row, head, d), (row, head, 2)
+    const float *ml_own;
+    char *o; float *lse;
     int64_t table_stride, q_sr, q_sh, c_sh, c_sp, c_st;       // q and cache strides in bytes
     int batch, n_heads, n_kv, group, gm, passes, rows, tiles; // gm query heads and `rows` rows make a block's columns
     int d, n_prefixes, n_pages, page_size, max_len, splits, combos;
@@ -859,8 +861,7 @@ __global__ void __launch_bounds__(kNT, (waves_of_prefix<CT, DP, NQ, MANY>())) pr
     }
 }
 
-// Joins the parts of a (row, query head), a wave each; the row's own tokens are one more part, already
-// normalised.  Lane i forms the weight of part i; then 64 / (d / 4) parts at a time are added up, 4 dims a lane.
+// Joins the parts of a (row, query head), a wave each; the row's own tokens are one more part.  Lane i forms the weight of part i; then 64 / (d / 4) parts at a time are added up, 4 dims a lane.
 template <bool BF16>
 __global__ void __launch_bounds__(kNT) prefix_join_kernel(Pp a) {
     const int lane = threadIdx.x & 63;
@@ -868,21 +869,21 @@ __global__ void __launch_bounds__(kNT) prefix_join_kernel(Pp a) {
     if (rh >= all) return;
     const int d4 = a.d / 4, side = 64 / d4, sub = lane / d4, e = (lane - sub * d4) * 4;
     const bool has = sub < side;
-    const float own = a.lse_own[rh] * kLog2e;
+    const float2 own = *(const float2 *)(a.ml_own + rh * 2);
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
     if (lane < d4) o = *(const f32x4 *)(a.o_own + rh * a.d + e);
     float2 w = make_float2(-INFINITY, 0.0f);                  // (at most 64 parts)
     if (lane < a.splits) w = *(const float2 *)(a.ml + (lane * all + rh) * 2);
-    float m = fmaxf(own, w.x);
+    float m = fmaxf(own.x, w.x);
 #pragma unroll
     for (int x = 32; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
-    const float m_use = m == -INFINITY ? 0.0f : m, f = exp2_fast(w.x - m_use), own_f = exp2_fast(own - m_use);
+    const float m_use = m == -INFINITY ? 0.0f : m, f = exp2_fast(w.x - m_use), own_f = exp2_fast(own.x - m_use);
     float sum = w.y == 0.0f ? 0.0f : w.y * f;
 #pragma unroll
     for (int x = 32; x > 0; x >>= 1) sum += __shfl_xor(sum, x);
-    sum += own_f;
-    o *= own_f;
-    // what weighs nothing may never have been written
+    sum += own.y == 0.0f ? 0.0f : own.y * own_f;
+    // what weighs nothing is not added, and of a part may never have been written
+    o = own_f > 0.0f && own.y != 0.0f ? o * (own_f * a.v_scale) : (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
     const float part_f = f > 0.0f && w.y != 0.0f ? f * a.v_scale : 0.0f;
     // (read all the same, eight on their way together, and not used)
     const float *part = a.part + rh * a.d + (has ? e : 0);
@@ -1004,7 +1005,7 @@ size_t prefix_attn_workspace_bytes(int64_t batch, int64_t n_heads, int64_t n_kv_
     const Cut c = cut_of(batch, n_heads, n_kv_heads, headdim, max_prefix_pages * page_size, batch);   // (the most splits that any number has)
     const int64_t rh = batch * n_heads;
     return align16(paged_attn_workspace_bytes(batch, n_heads, n_kv_heads, headdim, max_pages, page_size)) +
-           align16(rh * headdim * 4) + align16(rh * 4) + align16(c.splits * rh * 8) + c.splits * rh * headdim * 4;
+           align16(rh * headdim * 4) + align16(rh * 8) + align16(c.splits * rh * 8) + c.splits * rh * headdim * 4;
 }
 
 hipError_t launch_prefix_attn(const PrefixAttnArgs &p, hipStream_t stream, const char **kernel_name) {
@@ -1015,7 +1016,7 @@ hipError_t launch_prefix_attn(const PrefixAttnArgs &p, hipStream_t stream, const
     char *ws = (char *)a.workspace + align16(paged_attn_workspace_bytes(a.batch, a.n_heads, a.n_kv_heads, a.headdim, a.max_pages, a.page_size));
     Pp k = {};
     k.o_own = (const float *)ws; ws += align16(rh * a.headdim * 4);
-    k.lse_own = (const float *)ws; ws += align16(rh * 4);
+    k.ml_own = (const float *)ws; ws += align16(rh * 8);
     k.ml = (float *)ws; ws += align16(c.splits * rh * 8);
     k.part = (float *)ws;
     k.q = (const char *)a.q; k.k = (const char *)a.k_cache; k.v = (const char *)a.v_cache;
@@ -1030,7 +1031,7 @@ hipError_t launch_prefix_attn(const PrefixAttnArgs &p, hipStream_t stream, const
     k.scale2 = a.scale * (a.kv_dtype == SSM_KV_F8E4M3 ? a.k_scale : 1.0f) * kLog2e;
     k.v_scale = a.kv_dtype == SSM_KV_F8E4M3 ? a.v_scale : 1.0f;
 
-    a.o = (void *)k.o_own; a.lse = (float *)k.lse_own; a.o_f32 = true;
+    a.o = (void *)k.o_own; a.lse = (float *)k.ml_own; a.raw = true;
     const Call call{a, c, stream, kernel_name};
     const hipError_t rc = a.kv_dtype == SSM_KV_F32 ? go_type<KF32>(k, call)
                         : a.kv_dtype == SSM_KV_BF16 ? go_type<KBF16>(k, call) : go_type<KF8>(k, call);

@@ -72,3 +72,45 @@ def test_weights_keep_all_their_bits(cuda_device, form):
     ratio = np.abs(o - want) / bound
     report("weights %s" % (form,), of_bound=float(ratio.max()))
     assert (ratio <= 1.0).all()
+
+
+# prefix tokens, own tokens of the rows, H, Hk, d, cache; room for long prefixes
+JOINED = [(300, [299], 8, 2, 128, "bf16", False), (3000, [2999], 4, 1, 64, "f32", False), (2000, [2001], 8, 2, 128, "f8", False),
+          (3000, [2999, 0, 3000, 17], 4, 2, 128, "f32", False), (900, [899, 901, 1, 0, 900, 17, 902], 6, 1, 96, "bf16", False),
+          (40, [39, 41, 0, 40] * 20, 4, 2, 64, "f32", False), (40, [39, 41, 0, 40, 1] * 20, 16, 2, 128, "bf16", True),
+          (40, [39, 41, 0, 40, 1] * 20, 16, 2, 64, "f8", True), (40, [39, 41, 0, 40, 1] * 20, 16, 2, 128, "f32", True),
+          (2000, [1999, 2001] * 20, 4, 1, 256, "f32", False), (100, [99, 101, 100, 0] * 10, 4, 1, 256, "bf16", False)]
+
+
+@pytest.mark.parametrize("score", [1024.0, -1000.0])
+@pytest.mark.parametrize("case", JOINED, ids=lambda c: "%d-%d-%d-H%d-%d-d%d-%s-%s" % ((c[0], len(c[1]), max(c[1])) + c[2:6] + ("many" if c[6] else "few",)))
+def test_prefix_and_own_tokens_weigh_the_same(cuda_device, case, score):
+    """Every token of the prefix and of the rows' own has the same score, large and exact (a scale whose product with
+    log2(e) is 1), so every weight is 1: of N values -1 and n values 1, o = (n - N) / (n + N) but for the roundings of 1 / (n + N),
+    of its product and of the output.  A join by lse, in fp32, would take the own tokens' weight to be off by up to
+    4 u |lse|, some 2^-12."""
+    N, lens, H, Hk, d, cache, room = case
+    s = Shared(cuda_device, 8, [N], [0] * len(lens), lens, H, Hk, d, cache, 16)
+    if room:
+        _wide(s)
+    s.sc = float(np.float32(np.log(2.0)))
+    assert np.float32(s.sc) * np.float32(1.4426950408889634) == 1.0
+    used = torch.tensor(s.used(), device=cuda_device)
+    prefix = torch.zeros(s.pages, dtype=torch.bool, device=cuda_device)
+    prefix[torch.tensor(s.ptable[s.ptable >= 0], device=cuda_device)] = True
+    k, v = (torch.full(s.k.shape, float("nan"), device=cuda_device) for _ in range(2))
+    k[used] = 0.0
+    k[..., 0][used] = 1.0 / s.scale
+    v[used] = 1.0 / s.scale
+    v[prefix] *= -1.0
+    s.k, s.v = k.to(s.k.dtype), v.to(s.v.dtype)
+    s.q = torch.zeros_like(s.q)
+    s.q[..., 0] = score
+    o, lse = (n64(x) for x in s.call())
+    n = np.array(lens, float)
+    want = ((n - N) / (n + N))[:, None, None]
+    step = 4 * U if cache == "f32" else 2.0 ** -8 + 4 * U
+    assert (np.abs(o - want) <= step * np.abs(want)).all(), np.abs(o - want).max()
+    # the logarithm of a whole number, exact, and the maximum times ln 2: 2 u each, and a rounding of their sum
+    want = (score * s.sc + np.log(n + N))[:, None]
+    assert (np.abs(lse - want) <= 6 * U * (abs(score) + np.log(n + N)[:, None])).all(), np.abs(lse - want).max() / U / abs(score)

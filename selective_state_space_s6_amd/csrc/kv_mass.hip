@@ -1,15 +1,17 @@
 // kv_mass.hip -- the softmax weight that each cached token gathers from a step's queries
 // (ssm_kv_mass_update in include/ssm_longctx.h).
 //
-// w_j = sum over rows and heads of 2^(log2(e) (scale q . k_j - lse)): given lse, no maximum and no second pass.
+// w_j = sum over rows and heads of 2^(log2(e) (scale q . k_j - lse)): given lse, no maximum and no second pass.  log2(e) lse is
+// a float and a rest, whose power of two is the column's factor: a multiply-add in place of an addition, and without it
+// all weights of a column are off by up to u log2(e) |lse| the same way.
 // (row, head) pairs are columns of the matrix products, 16 tokens or more their rows; a lane adds up its columns'
 // exponentials, and the 16 lanes of a token are joined once at the end.  Two forms, and in both one writer a token:
 //   step: a wave has tiles of 16 to 64 tokens from one line of all requests' tiles, cut into equal pieces, the next
 //     tile's keys on their way while one is worked on, and walks the request's columns, 16 at a time.
-//     Bound: HBM, the keys.  64 requests of up to 8192 tokens, 8 kv heads of 128, bf16: 173 us for 819 MB, 4.7 TB/s.
+//     Bound: HBM, the keys.  64 requests of up to 8192 tokens, 8 kv heads of 128, bf16: 176 us for 819 MB, 4.7 TB/s.
 //   prompt: a block has 64 tokens, their keys in shared memory, and its 8 waves columns of their own from the first row on
 //     that sees the tile; requests go to XCDs in turn.  Bound: the way of q from the L2s, 64 bytes of each of 16 columns a load,
-//     beside one exponential a (row, head, token).  4 prompts of up to 2048 tokens, 32 + 8 heads of 128, bf16: 51 us,
+//     beside one exponential a (row, head, token).  4 prompts of up to 2048 tokens, 32 + 8 heads of 128, bf16: 54 us,
 //     13.9 GFLOP and 54 million exponentials.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -92,17 +94,20 @@ __device__ __forceinline__ void load_keys(Keys<CT, DP> &k, const char *kb, uint6
 }
 
 // 16 columns of the scores: a lane's part of their queries, the last token that its column sees
-// (-1: none), log2(e) lse
+// (-1: none), log2(e) lse, and 2^-(what that is short of)
 template <int CT, int DP> struct Column {
     u32x4 q[MTile<CT, DP>::KC * MTile<CT, DP>::QW];
     int pos;
-    float lse2;
+    float lse2, rest;
 };
 template <int CT, int DP, bool EXACT>
 __device__ __forceinline__ void load_column(const Mp &a, Column<CT, DP> &x, const char *qp, float lse, int pos, int grp) {
     using T = MTile<CT, DP>;
     x.pos = lse == -INFINITY ? -1 : pos;
     x.lse2 = lse * kLog2e;
+    // (log2(e) is kLog2e + 1.925963033e-8; of an infinite lse there is no rest)
+    const float low = fmaf(lse, 1.925963033e-8f, fmaf(lse, kLog2e, -x.lse2));
+    x.rest = fabsf(lse) < INFINITY ? exp2_fast(-low) : 1.0f;
 #pragma unroll
     for (int k = 0; k < T::KC; ++k)
 #pragma unroll
@@ -139,11 +144,11 @@ __device__ __forceinline__ f32x4 scores(const u32x4 (&k)[MTile<CT, DP>::KC], con
 }
 // adds a column's weights to w; t: the first of the lane's four tokens, ALL: the column sees them all
 template <bool ALL>
-__device__ __forceinline__ void weigh(float (&w)[4], f32x4 s, float scale2, float lse2, int t, int pos) {
+__device__ __forceinline__ void weigh(float (&w)[4], f32x4 s, float scale2, float lse2, float rest, int t, int pos) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float p = exp2_fast(fmaf(s[e], scale2, -lse2));
-        w[e] += ALL || t + e <= pos ? p : 0.0f;
+        w[e] = fmaf(ALL || t + e <= pos ? p : 0.0f, rest, w[e]);
     }
 }
 
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(kW * 64, (MTile<CT, DP>::OCC)) kv_mass_step_ke
             if (!__any(x.x.pos >= here.t0)) continue;
 #pragma unroll
             for (int b = 0; b < T::SUB; ++b) {
-                weigh<false>(w[b], scores<CT, DP>(x.k.r[b], x.x), a.scale2, x.x.lse2, here.t0 + b * 16 + grp * 4, x.x.pos);
+                weigh<false>(w[b], scores<CT, DP>(x.k.r[b], x.x), a.scale2, x.x.lse2, x.x.rest, here.t0 + b * 16 + grp * 4, x.x.pos);
                 if constexpr (CT == KF8) __builtin_amdgcn_sched_barrier(0);      // (widened keys of one block at a time)
             }
         }
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(kShare * 64, 2) kv_mass_prompt_kernel(Mp a) {
                     for (int y = 0; y < T::KC; ++y) k[y] = keys[(b * T::KC + y) * 64 + lane];
 #pragma unroll
                     for (int n = 0; n < NC; ++n)
-                        weigh<decltype(every)::value>(w[b], scores<CT, DP>(k, r.x[n]), a.scale2, r.x[n].lse2, t0 + b * 16 + grp * 4, r.x[n].pos);
+                        weigh<decltype(every)::value>(w[b], scores<CT, DP>(k, r.x[n]), a.scale2, r.x[n].lse2, r.x[n].rest, t0 + b * 16 + grp * 4, r.x[n].pos);
                 }
             };
             if (__all(all)) go(std::true_type{});

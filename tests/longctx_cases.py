@@ -115,6 +115,17 @@ def ratios(got, want, rows_of, q, scale, bf16, weights):
     return np.where(np.isnan(ro), np.inf, ro), np.where(np.isnan(rl), np.inf, rl)
 
 
+def attended(s):
+    """rows_of of `ratios` for rows behind shared prefixes (test_prefix_attn_gpu.Shared)."""
+    from oracle.longctx import _tokens
+    k64, v64, at = s.k64(), s.v64(), []
+    for r, p in enumerate(s.prefix):
+        t = _tokens(s.ptable[p], s.plens[p], s.ps, s.pages) if 0 <= p < len(s.plens) else []
+        t = t + _tokens(s.own[r], s.rows[r], s.ps, s.pages)
+        at.append((np.array([x[1] for x in t], int), np.array([x[2] for x in t], int)))
+    return lambda r, h: (k64[(*at[r], h * s.Hk // s.H)], v64[(*at[r], h * s.Hk // s.H)])
+
+
 def captured(call):
     """`call` run once on a side stream and then captured; the graph."""
     side = torch.cuda.Stream()

@@ -147,8 +147,12 @@ int ssm_select_attn_decode_fwd(const void *q, const void *k_cache, const void *v
  *   w = sum over rows t with j <= positions[t] and query heads h of g of
  *       exp(scale * k_scale * q[t,h] . k[j,g] - lse[t,h])
  *   mass[page, g, j % page_size] = w + (j < len_old[r] ? mass[page, g, j % page_size] : 0)
- * with lse what attention of the same rows gave (a row with lse = -inf adds
- * nothing).  Tokens from len_old[r] on are new: what their place held is dropped.
+ * with lse what attention of the same rows over all the tokens that they see gave
+ * (a row with lse = -inf adds nothing): ssm_paged_attn_decode_fwd without a window,
+ * where each of a prompt's rows is a row of its own, with its request's line of the
+ * table and the length positions[t] + 1; or ssm_prefix_attn_decode_fwd, whose rows' own
+ * tokens then gather their shares of the whole.  Not that of attention over chosen
+ * pages or a window: tokens that it left out would gather weights of any size.  Tokens from len_old[r] on are new: what their place held is dropped.
  * A request without a row that counts keeps its mass for the tokens below len_old.
  * Arithmetic: products as in ssm_paged_attn_decode_fwd, exponentials and sums in
  * fp32, in an order fixed by the shapes.

@@ -88,7 +88,8 @@ def ssm_kv_mass_update(q, k_cache, lse, mass, block_table, starts, positions, le
     """Adds the softmax weights of a step's queries to each cached token's running sum, mass
     (pages, Hk, page_size) fp32, in place.  q (tokens, H, d) and lse (tokens, H) fp32 of the step's
     rows; request r has rows starts[r]..starts[r+1]-1, row t at place positions[t] of its cache
-    (what ssm_kv_pages_step returns); tokens from len_old[r] to lens[r] - 1 are new and start from 0."""
+    (what ssm_kv_pages_step returns); tokens from len_old[r] to lens[r] - 1 are new and start from 0.
+    lse is that of attention over all the tokens that a row sees, not over chosen pages or a window."""
     _finished(_bind.mass_update(q, k_cache, lse, mass, block_table, starts, positions, len_old, lens, scale, k_scale))
 
 

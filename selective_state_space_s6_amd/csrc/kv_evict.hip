@@ -9,7 +9,7 @@
 // rows are cut along headdim, which are moves of their own, as are k, v and mass.
 //
 // Bound: HBM, the moved rows read and written.  64 requests of 8 kv heads of 128, bf16, 4160 tokens cut to 4096 of random
-// mass: 495 us, 15 of them the choice, for 2.1 GB (418 us at the rate of a large copy); 91 where the evicted ones
+// mass: 499 us on a new cache, 15 of them the choice, for 2.1 GB (418 us at the rate of a large copy); 91 where the evicted ones
 // are the newest that may go.  One request of 30000 tokens cut to 29000: 113, of one kv head of 64, by the chain of its runs.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -183,7 +183,7 @@ hipError_t launch_kv_evict(const KvEvictArgs &a, hipStream_t stream, const char 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || most <= a.budget) return e;
     *kernel_name = "evict_move_kernel";
-    // rows of 64 bytes and more, until there are 512 moves of k (on blocks of 4 waves): 256 heads of 2900 tokens of 256 bytes 162 us whole, 179 in
+    // slices of 32 bytes and more of a row, until there are 512 moves of k (on blocks of 4 waves): 256 heads of 2900 tokens of 256 bytes 162 us whole, 179 in
     // halves, 215 in quarters; 512 heads of 4096 532 whole and 476 in halves; 32 heads of 500 within 10% of one another
     int slices = 1;
     while (slices * 4 <= a.row_bytes / 16 && heads * slices < 512) slices *= 2;

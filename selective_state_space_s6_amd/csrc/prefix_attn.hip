@@ -14,17 +14,22 @@
 //   many: 4 waves of 16 or 32 columns each; K and V come through shared memory once for all, the next tile's while
 //     one is worked on.
 //
-// Figures (us): 64 rows of 32 + 8 heads of 128, bf16, behind 16384 tokens, 512 own, 71: 61 for both kinds of blocks and 9 for
-// the join.  Its 134 MB would take 26; the prefix' part is bound by matrix and vector instructions (17 and 20 to 25
-// us of issue at the 1.7 GHz that both together leave) that two waves on a SIMD overlap in part.  13 rows of
-// 20 + 4 heads, 8 bits, behind three prompts of 4001 15.7, and 2 rows behind 8192 tokens 15.2: the way through a block
-// (its prefixes, pages, first loads; then the parts) and the second launch.
+// A row's columns are done where its prefix ends: their part is written there and all columns start anew, so that a V
+// that is not finite reaches the rows behind its own prefix alone (weights of 0 for the others would not do: 0 times it is
+// NaN).  In the form for few, q then comes to shared memory again, where the outputs were.
+//
+// Figures (us): 64 rows of 32 + 8 heads of 128, bf16, behind 16384 tokens, 512 own, 74 a call; in a trace of the kernels, 70
+// for both kinds of blocks and 9 for the join.  Its 134 MB would take 26; the prefix' part is bound by matrix and vector
+// instructions (21 and 25 us of issue at the 1.7 GHz that both together leave) that two waves on a SIMD overlap in
+// part.  13 rows of 20 + 4 heads, 8 bits, behind three prompts of 4001 17.4, and 2 rows behind 8192 tokens 15.3: the way
+// through a block (its prefixes, pages, first loads; then the parts) and the second launch.
 //
 // The running maximum is raised only where a score exceeds it by more than 2^8 in its weight: weights up
 // to 2^8 lose nothing in fp32, and the outputs are not rescaled for every new maximum.  Weights enter their
 // product with a bf16 or 8-bit v as the sum of three bf16 values, all of their 24 bits.  (Two keep 17, and outputs in which
 // the tokens' shares cancel show it: us with two and with three, 64 rows behind 16384 tokens, bf16 72.1, 79.2, 8 bits
-// 57.4, 62.5; 128 rows behind five prompts 49.4, 57.0; 13 rows of three prompts in 8 bits 17.2, 17.7.)
+// 57.4, 62.5; 128 rows behind five prompts 49.4, 57.0; 13 rows of three prompts in 8 bits 17.2, 17.7.  The figures beside
+// the choices below were taken with two.)
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <algorithm>
@@ -924,6 +929,9 @@ __global__ void __launch_bounds__(kNT) prefix_join_kernel(Pp a) {
 // So 32 columns to a block, 16 if there are no more; up to 128 dims many of 128 from 2^25 scores on, where K and V out of
 // the L2s cost more than the way through shared memory; above 128 dims, where a wave of 32 columns keeps one block a
 // compute unit, many of 64 from 33 columns on.
+//
+// Form and parts go by the room of prefix_table, since the host does not know the lengths: the 13 rows of three prompts of up to 4001
+// tokens take 17.3 us with room for up to 32768, and 23.3 with room for 131072, where they are of the form for many.
 //
 // Two blocks a compute unit from 2^24 scores on, one below, where the own tokens' blocks then run beside them and there are
 // fewer parts to join (two, one): 48 columns of the 8-bit heads above 24.2, 18.3;  160 of them 35.5, 29.1;
